@@ -487,6 +487,137 @@ sfa_status varbsr_plan_set_logits_soft_cap(varbsr_plan_t plan, float logits_soft
 /* Frees the plan's host state.  Safe on NULL. */
 void varbsr_plan_destroy(varbsr_plan_t plan);
 
+/* ------------------------------------------------------------------------ */
+/* Paged KV cache and dense attention over it and over packed rows: the
+ * serving operators next to the sparse ones above (grouped heads, causal
+ * alignment, log-sum-exp, per-head FP8 scales, status codes and streams as
+ * there). */
+
+/*
+ * A paged KV cache: pools of pages of `page_size` tokens, and for each of
+ * `num_seqs` sequences the list of its pages and its length.
+ *   k, v        device page pools, contiguous:
+ *               NHD (num_pages, page_size, num_kv_heads, head_dim) or
+ *               HND (num_pages, num_kv_heads, page_size, head_dim).
+ *   page_table  device int32 (num_seqs, max_pages): token j of sequence b is
+ *               in page page_table[b][j / page_size], place j % page_size.
+ *               Entries behind a sequence's last page are not read.
+ *   kv_lens     device int32 (num_seqs): tokens of each sequence, the newest
+ *               included; read as at most max_pages * page_size, at least 0.
+ *   page_size   any size >= 1.
+ *   head_dim    64 or 128 in this build.
+ *   dtype       F16 or BF16, or E4M3 / E5M2 codes.
+ *   scale_k, scale_v  device float32 [num_kv_heads] dequantisation scales of an
+ *               8-bit cache (a code times its kv head's scale is the value it
+ *               stands for, as in bsr_run_scaled), or NULL = 1.0; each positive
+ *               and finite (other values give unspecified numbers, never a
+ *               fault).  Must be NULL for a 16-bit cache.
+ * A page number outside [0, num_pages) is never dereferenced: its tokens
+ * count as absent (masked in attention, read as zero, not written).  What the
+ * pools hold in places behind a sequence's last token never matters.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    const int32_t* page_table;
+    const int32_t* kv_lens;
+    int num_seqs, num_pages, page_size, max_pages;
+    int num_kv_heads, head_dim;
+    sfa_kv_layout kv_layout;
+    sfa_dtype dtype;
+    const float* scale_k;
+    const float* scale_v;
+} paged_kv;
+
+/*
+ * Packed rows.  The rows of all sequences lie one after the other: sequence b
+ * has rows cu[b] .. cu[b + 1] - 1 of `num_tokens` rows (cu: device int32
+ * (num_seqs + 1), non-decreasing, any of them empty; entries are read as
+ * clamped to [0, num_tokens]).  Rows before the first or behind the last
+ * sequence are left alone: not read, not written.  Row t of a tensor with
+ * `stride` starts at t * stride elements (a multiple of 8, at least heads *
+ * head_dim), its heads contiguous: slices of a fused projection's output
+ * need no copy.  In the paged calls the rows of sequence b are its newest
+ * tokens: with n = cu[b + 1] - cu[b], row t is token kv_lens[b] - (cu[b + 1] - t).
+ */
+
+/*
+ * paged_append -- writes new tokens' keys and values into the cache.
+ *   k_new, v_new  device packed rows of num_kv_heads heads, `dtype` (F16 or
+ *                 BF16; a 16-bit cache's own).
+ * Into an 8-bit cache the value x of kv head h is written as the code nearest
+ * to x / scale[h] (exact quotient, ties to even, saturating to the largest
+ * finite value; NaN stays NaN), into a 16-bit cache unchanged.  A token whose
+ * position is negative or behind the page table is not written.  Two rows of
+ * one call must not name the same place.
+ * Errors: SFA_ERR_INVALID_ARG / SFA_ERR_UNSUPPORTED before any launch.
+ */
+sfa_status paged_append(const paged_kv* cache, const void* k_new, const void* v_new,
+                        int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens,
+                        int num_tokens, sfa_dtype dtype, sfa_stream_t stream);
+
+/*
+ * paged_read -- the newest cu_seqlens[b + 1] - cu_seqlens[b] tokens of every
+ * sequence b (all of them with cu_seqlens the running sum of kv_lens) back as
+ * packed rows: code * scale[h], rounded once to `dtype`, or a 16-bit cache's
+ * elements as they are.  Tokens without a place (a negative position, a page
+ * out of range) are written as zeros.
+ *   k_out, v_out  device (num_tokens, num_kv_heads, head_dim) of `dtype`.
+ */
+sfa_status paged_read(const paged_kv* cache, const int32_t* cu_seqlens, int num_tokens,
+                      sfa_dtype dtype, void* k_out, void* v_out, sfa_stream_t stream);
+
+/* Bytes of workspace paged_run / varlen_run need for these sizes on the
+ * current device.  Host only. */
+sfa_status paged_workspace_size(int num_seqs, int num_tokens, int num_qo_heads, int num_kv_heads,
+                                int head_dim, size_t* bytes);
+sfa_status varlen_workspace_size(int num_seqs, int num_tokens, int num_qo_heads, int num_kv_heads,
+                                 int head_dim, size_t* bytes);
+
+/*
+ * paged_run -- attention of each sequence's newest tokens over its cached
+ * ones (append them first): one token each (decode), or a chunk.  Query row i
+ * of sequence b (n_b rows, L_b = kv_lens[b]), qo head h, kv head
+ * g = h / (num_qo_heads / num_kv_heads):
+ *     s_j = scale * <q_i, k_j>,  j < L_b, and with causal j <= i + L_b - n_b
+ *     out = sum_j softmax(s)_j v_j,  lse = ln sum_j exp(s_j).
+ * A row with no visible key writes out = +0 and lse = -inf.
+ *   q          device packed rows of num_qo_heads heads, `dtype` (F16 or BF16,
+ *              a 16-bit cache's own).
+ *   max_q_len  an upper bound of n_b, or 0 = unknown: it chooses between two
+ *              kernels, results are right whatever it says.
+ *   scale      softmax scale, finite; <= 0 selects 1/sqrt(head_dim).
+ *   out        device (num_tokens, num_qo_heads, head_dim), dtype.
+ *   lse        device float32 (num_tokens, num_qo_heads) or NULL.
+ *   workspace  device, 16-byte aligned, paged_workspace_size() bytes; nothing
+ *              in it needs clearing or is kept between calls.  Calls that may
+ *              overlap on the GPU (other streams, graphs replayed side by
+ *              side) need one each.
+ * Scores, softmax and sums are fp32.  A NaN or infinity in a visible key or
+ * value makes every row of its sequence that shares a key tile with it
+ * unspecified, causally earlier ones included.
+ * Errors: SFA_ERR_INVALID_ARG / SFA_ERR_UNSUPPORTED / SFA_ERR_WORKSPACE before
+ * any launch; SFA_ERR_CUDA if a launch fails.
+ */
+sfa_status paged_run(const paged_kv* cache, const void* q, int64_t q_stride,
+                     const int32_t* cu_seqlens_q, int num_tokens, int num_qo_heads, int max_q_len,
+                     float scale, int causal, sfa_dtype dtype, void* out, float* lse,
+                     void* workspace, size_t workspace_bytes, sfa_stream_t stream);
+
+/*
+ * varlen_run -- the same attention over packed keys and values: sequence b's
+ * n_b query rows (cu_seqlens_q, num_tokens rows) over its L_b key rows
+ * (cu_seqlens_k, num_keys rows), L_b any (a whole prompt: the same list for
+ * both).  k, v: device packed rows of num_kv_heads heads, q's dtype.  Other
+ * arguments, workspace (varlen_workspace_size) and errors as paged_run.
+ */
+sfa_status varlen_run(const void* q, const void* k, const void* v, int64_t q_stride,
+                      int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens_q,
+                      const int32_t* cu_seqlens_k, int num_seqs, int num_tokens, int num_keys,
+                      int num_qo_heads, int num_kv_heads, int head_dim, int max_q_len, float scale,
+                      int causal, sfa_dtype dtype, void* out, float* lse, void* workspace,
+                      size_t workspace_bytes, sfa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
