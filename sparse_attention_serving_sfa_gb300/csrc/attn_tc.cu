@@ -1,0 +1,728 @@
+// Dense attention of many query rows over packed rows or a paged cache on the
+// 5th-generation tensor cores.
+//
+//     s_j = scale * q.k_j  (j < kv_len; causal: j <= i + kv_len - q_len)
+//     out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  m the running maximum
+//
+// A work item is one kv head and 2 x TR query tokens of a sequence, TR =
+// 128 / G: two M-tiles of 128 rows (row r of a tile: token r / G, head r % G,
+// so a K / V tile serves all G heads), against all its visible keys in steps
+// of 128, or against one of `splits` equal shares of them (parts merged by
+// attn_tc_merge in order of their keys) when there are too few items for the
+// SMs.  CTAs are persistent (one per SM) and walk the items, longest first
+// within a sequence, in boustrophedon order, so that a CTA's long and short
+// ones even out.
+//
+// Warp roles, 384 threads:
+//   - softmax warpgroups 0, 1: tile t, thread = row = TMEM lane.  Read the
+//     128 scores of a step, mask them (only where a row's limit or a missing
+//     page falls into the step), update m (O is rescaled only when m grows by
+//     more than 2^8), write P = exp2(s - m) rounded to 16 bits over S.  At the
+//     end divide and store.
+//   - MMA thread: S_t = Q_t K^T into TMEM, O_t += P_t V with P from TMEM and
+//     V an MN-major operand; tile 0's P.V and next Q.K^T run while the
+//     softmax works on tile 1, and the other way round.
+//   - producer warp: Q tiles and a ring of 128-key K and V tiles by TMA, in
+//     the order the MMAs use them, running ahead across items.
+// TMEM: tile t at column 256 t: S / P in [0, 128), O in [128, 128 + D).
+//
+// P is rounded once to 16 bits (at most half a step of the output's type per
+// weight, so the output moves by no more than its own rounding of
+// sum_j p_j |v_j|); a second P.V on the remainders would cost half as many
+// MMAs again.  fp16 P carries a factor 2^7 so that weights down to 2^-21 of the
+// largest stay normal.  Sums of P use the unrounded fp32 values.
+//
+// V rows behind kv_len (the next sequence's, or whatever a page holds) would
+// turn 0 x NaN into NaN: the producer waits for such a tile itself, writes
+// zeros over those rows and then hands it on.
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "paged.h"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace sfa {
+namespace {
+
+constexpr int kTileM = 128;
+constexpr int kStep = 128;                  // keys of a step
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 384;
+constexpr int kRegsLaunch = 168, kRegsControl = 80, kRegsSoftmax = 208;
+static_assert(kRegsSoftmax * kSoftWarps * 32 + kRegsControl * 128 <= kRegsLaunch * kThreads,
+              "the register split fits what the block was launched with");
+constexpr int kTmemCols = 512, kTileCols = 256, kOCol = 128;
+constexpr float kRescale = 8.0f;            // log2 units
+constexpr int kMinSplitSteps = 4;           // steps below which a share is not cut further
+
+template <int D>
+struct TcSmem {
+    static constexpr int panels = D / 64;
+    static constexpr int panel = kStep * 128;              // 128 rows x 128 bytes
+    static constexpr int tile = panels * panel;            // Q, K or V tile
+    static constexpr int slots = D == 128 ? 5 : 8;
+    static constexpr int q = 0;
+    static constexpr int ring = 2 * tile;
+    static constexpr int bars = ring + slots * tile;
+    static constexpr int abort = bars + 8 * 40;
+    static constexpr int tmem_slot = abort + 4;
+    static constexpr int total = abort + 16;
+    static constexpr int alloc = total + 1024;             // room to align the base to 1024
+    static_assert(alloc <= 232448, "dynamic shared memory per block");
+};
+
+enum {
+    B_Q = 0,            // Q tiles of the item landed
+    B_Q_FREE = 1,       // every Q.K^T of the item done
+    B_S = 2,            // + t: S_t written (and the P.V before it done)
+    B_P = 4,            // + t: P_t written
+    B_O = 6,            // + t: O_t of the item complete
+    B_TAIL = 8,         // V tile landed whose tail is still to be cleared
+    B_DRAIN = 9,
+    B_FULL = 10,        // + slot
+    B_FREE = 20         // + slot
+};
+
+struct TcParams {
+    SeqAttn a;
+    int TR, splits, hnd;
+    int box, box_shift, boxes;          // keys of a TMA box (and its log2), boxes of a step
+    float* ws_o;                        // [splits][tokens * Hq][D]
+    float* ws_ml;                       // [splits][tokens * Hq][2]
+};
+
+// What an item is; the same in every thread of a warp.
+struct Item {
+    int b, h, split;
+    int q_row, n_q, tok0;       // packed row of the sequence's first token, its rows, the item's first token
+    int k_row, kv_len;
+    int s0, n[2];               // first step, steps of each tile
+    bool whole;                 // the first share holds all the keys
+    bool skip;                  // a share behind the last
+};
+
+// Keys visible to the last of tokens [0, tok_end) of a sequence.
+__device__ __forceinline__ int visible(const SeqAttn& a, int kv_len, int n_q, int tok_end) {
+    if (!a.causal) return kv_len;
+    return max(0, min(kv_len, tok_end + kv_len - n_q));
+}
+
+// Steps of share `split` of N: first, count, and whether the first share holds all.
+__device__ __forceinline__ void share(int N, int splits, int split, int& first, int& count, bool& whole) {
+    int per = max((N + splits - 1) / splits, kMinSplitSteps);
+    if (splits == 1) per = max(N, 1);
+    first = min(split * per, N);
+    count = min(N - first, per);
+    whole = N <= per;
+}
+
+// Walks the items of this CTA: item numbers run over (sequence, tile from the
+// last, kv head, split), the split fastest.  Every warp walks on its own.
+struct Walk {
+    int round = 0;
+    int b = 0;
+    int64_t base = 0;          // first item of sequence b
+
+    __device__ __forceinline__ bool next(const TcParams& p, Item& it) {
+        const SeqAttn& a = p.a;
+        const int rnd = round++;
+        const int64_t i = (int64_t)rnd * gridDim.x +
+                          ((rnd & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const int lane = threadIdx.x & 31;
+        const int per_tile = a.kv.Hkv * p.splits;
+        while (b < a.kv.num_seqs) {
+            // 32 sequences at a time
+            const int x = b + lane;
+            int64_t items = 0;
+            if (x < a.kv.num_seqs) {
+                const int2 r = seq_rows(a.cu_q, x, a.tokens);
+                items = (int64_t)((r.y - r.x + 2 * p.TR - 1) / (2 * p.TR)) * per_tile;
+            }
+            int64_t inc = items;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned above = __ballot_sync(0xffffffffu, base + inc > i);
+            if (!above) {
+                base += __shfl_sync(0xffffffffu, inc, 31);
+                b += 32;
+                continue;
+            }
+            const int w = __ffs(above) - 1;
+            base += __shfl_sync(0xffffffffu, inc - items, w);
+            b += w;
+            break;
+        }
+        if (b >= a.kv.num_seqs) return false;
+        const int2 qr = seq_rows(a.cu_q, b, a.tokens);
+        const int2 kr = seq_keys(a.kv, b);
+        const int rel = (int)(i - base);
+        it.b = b;
+        it.split = rel % p.splits;
+        it.h = (rel / p.splits) % a.kv.Hkv;
+        it.q_row = qr.x;
+        it.n_q = qr.y - qr.x;
+        const int tiles = (it.n_q + 2 * p.TR - 1) / (2 * p.TR);
+        it.tok0 = (tiles - 1 - rel / per_tile) * 2 * p.TR;
+        it.k_row = kr.x;
+        it.kv_len = kr.y;
+        const int mid = it.tok0 + p.TR;
+        const int v0 = visible(a, it.kv_len, it.n_q, min(mid, it.n_q));
+        const int v1 = mid < it.n_q ? visible(a, it.kv_len, it.n_q, min(mid + p.TR, it.n_q)) : 0;
+        int count;
+        share((max(v0, v1) + kStep - 1) / kStep, p.splits, it.split, it.s0, count, it.whole);
+        it.skip = it.split > 0 && count == 0;
+        it.n[0] = max(0, min((v0 + kStep - 1) / kStep - it.s0, count));
+        it.n[1] = max(0, min((v1 + kStep - 1) / kStep - it.s0, count));
+        return true;
+    }
+};
+
+template <class E, int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, const TcParams p) {
+    using L = TcSmem<D>;
+    constexpr bool kBf16 = std::is_same<E, BF16>::value;
+    constexpr uint32_t kIdescQK = idesc_f16(kTileM, kStep, kBf16, false, false);
+    constexpr uint32_t kIdescPV = idesc_f16(kTileM, D, kBf16, false, true);
+    constexpr float kPShift = kBf16 ? 0.f : 7.f;
+
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int i) { return sbase + L::bars + 8 * i; };
+    const SeqAttn& a = p.a;
+    const int G = a.G;
+    int* err = a.err_word;
+
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort);
+    if (tid == 0) {
+        *abort_flag = 0;
+        mbar_init(bar(B_Q), 1);
+        mbar_init(bar(B_Q_FREE), 1);
+        mbar_init(bar(B_TAIL), 1);
+        mbar_init(bar(B_DRAIN), 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(B_S + t), 1);
+            mbar_init(bar(B_P + t), 128);
+            mbar_init(bar(B_O + t), 1);
+        }
+        for (int s = 0; s < L::slots; ++s) {
+            mbar_init(bar(B_FULL + s), 1);
+            mbar_init(bar(B_FREE + s), 1);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 0) tmem_alloc(sbase + L::tmem_slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::tmem_slot);
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    Walk walk;
+    Item it;
+    if (warp >= kSoftWarps) {
+        regs_release<kRegsControl>();
+        if (warp == kLoadWarp) {
+            // ============================ producer ============================
+            if (lane == 0) {
+                tma_prefetch_map(&mq);
+                tma_prefetch_map(&mk);
+                tma_prefetch_map(&mv);
+            }
+            int items = 0, loads = 0, tails = 0;   // items with keys, tiles loaded, tiles cleared
+            bool ok = true;
+            while (ok && walk.next(p, it)) {
+                const int n = max(it.n[0], it.n[1]);
+                if (n == 0) continue;
+                if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int tiles = it.tok0 + p.TR < it.n_q ? 2 : 1;
+                    mbar_arrive_expect_tx(bar(B_Q), tiles * L::panels * p.TR * G * 128);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int pn = 0; pn < L::panels; ++pn)
+                            tma_load_3d(sbase + L::q + t * L::tile + pn * L::panel, &mq, pn * 64, it.h * G,
+                                        it.q_row + it.tok0 + t * p.TR, bar(B_Q));
+                }
+                ++items;
+                // page of this lane's box of a step, -1 if there is none to read
+                auto page_of = [&](int st) -> int {
+                    const int key = (it.s0 + st) * kStep + lane * p.box;
+                    if (st >= n || lane >= p.boxes || key >= it.kv_len) return -1;
+                    const int pg = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
+                    return (unsigned)pg < (unsigned)a.kv.num_pages ? pg : -1;
+                };
+                int page = 0;
+                if constexpr (PAGED) page = page_of(0);
+                for (int st = 0; st < n && ok; ++st) {
+                    const int key0 = (it.s0 + st) * kStep;
+                    const int pg = page;
+                    if constexpr (PAGED) page = page_of(st + 1);
+                    for (int kv = 0; kv < 2 && ok; ++kv) {
+                        const int s = loads % L::slots;
+                        if (loads >= L::slots)
+                            ok = mbar_wait(bar(B_FREE + s), (loads / L::slots - 1) & 1, err, abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const uint32_t dst = sbase + L::ring + s * L::tile;
+                        const int real = it.kv_len - key0;             // keys of this tile that exist
+                        const bool tail = kv == 1 && real < kStep;
+                        const uint32_t b = bar(tail ? B_TAIL : B_FULL + s);
+                        const CUtensorMap* map = kv ? &mv : &mk;
+                        if (lane == 0) mbar_arrive_expect_tx(b, L::tile);
+                        __syncwarp();
+                        if constexpr (PAGED) {
+                            if (lane < p.boxes) {
+                                // a box without a page reads page num_pages: outside, zeros
+                                const int at = pg < 0 ? a.kv.num_pages : pg;
+                                const int place = pg < 0 ? 0 : (key0 + lane * p.box) % a.kv.page_size;
+                                for (int pn = 0; pn < L::panels; ++pn) {
+                                    const uint32_t to = dst + pn * L::panel + lane * p.box * 128;
+                                    if (p.hnd) tma_load_4d(to, map, pn * 64, place, it.h, at, b);
+                                    else tma_load_4d(to, map, pn * 64, it.h, place, at, b);
+                                }
+                            }
+                        } else if (lane == 0) {
+                            for (int pn = 0; pn < L::panels; ++pn)
+                                tma_load_3d(dst + pn * L::panel, map, pn * 64, it.h, it.k_row + key0, b);
+                        }
+                        if (tail) {
+                            __syncwarp();
+                            ok = mbar_wait(b, tails & 1, err, abort_flag);
+                            ++tails;
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            unsigned char* row = smem + L::ring + s * L::tile;
+                            for (int x = real * 8 + lane; x < kStep * 8; x += 32)
+                                for (int pn = 0; pn < L::panels; ++pn)
+                                    *reinterpret_cast<uint4*>(row + pn * L::panel + x * 16) = make_uint4(0, 0, 0, 0);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(B_FULL + s));
+                        }
+                        ++loads;
+                    }
+                }
+            }
+            if (!ok && lane == 0) {
+                // a wait gave up: let the copies in flight land (bounded) before leaving
+                if (items > 0) mbar_wait(bar(B_Q), (items - 1) & 1, nullptr, nullptr, 100000000ull);
+                for (int x = max(0, loads - L::slots); x < loads; ++x)
+                    mbar_wait(bar(B_FULL + x % L::slots), (x / L::slots) & 1, nullptr, nullptr, 100000000ull);
+            }
+        } else if (warp == kMmaWarp) {
+            // ============================ MMA ============================
+            int items = 0, base = 0;        // items with keys; ring index of the item's first tile
+            int done[2] = {0, 0};           // P tiles consumed
+            bool ok = true;
+            while (ok && walk.next(p, it)) {
+                const int n = max(it.n[0], it.n[1]);
+                if (n == 0) continue;
+                auto full = [&](int x) {
+                    return mbar_wait(bar(B_FULL + x % L::slots), (x / L::slots) & 1, err, abort_flag);
+                };
+                auto qk = [&](int t, int x) {
+                    const uint32_t kb = sbase + L::ring + (x % L::slots) * L::tile;
+                    const uint32_t qb = sbase + L::q + t * L::tile;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * L::panel + (kk & 3) * 32;
+                        tc_mma_f16(tmem + t * kTileCols, sdesc_sw128(qb + off, 16, 1024),
+                                   sdesc_sw128(kb + off, 16, 1024), kIdescQK, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(bar(B_S + t));
+                };
+                auto pv = [&](int t, int x, bool first) {
+                    const uint32_t vb = sbase + L::ring + (x % L::slots) * L::tile;
+#pragma unroll
+                    for (int kk = 0; kk < kStep / 16; ++kk)
+                        tc_mma_f16_ts(tmem + t * kTileCols + kOCol, tmem + t * kTileCols + 8 * kk,
+                                      sdesc_sw128(vb + kk * 16 * 128, L::panel, 1024), kIdescPV,
+                                      first && kk == 0 ? 0u : 1u);
+                };
+                if (lane == 0) {
+                    ok = mbar_wait(bar(B_Q), items & 1, err, abort_flag) && full(base);
+                    if (ok) {
+                        tc_fence_after();
+                        for (int t = 0; t < 2; ++t)
+                            if (it.n[t] > 0) qk(t, base);
+                        tc_commit(bar(B_FREE + base % L::slots));
+                        if (n == 1) tc_commit(bar(B_Q_FREE));
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        const int vx = base + 2 * i + 1, kx = vx + 1;
+                        ok = full(vx);
+                        bool have_k = false;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok || i >= it.n[t]) continue;
+                            ok = mbar_wait(bar(B_P + t), done[t] & 1, err, abort_flag);
+                            if (!ok) continue;
+                            ++done[t];
+                            tc_fence_after();
+                            pv(t, vx, i == 0);
+                            if (i == it.n[t] - 1) {
+                                tc_commit(bar(B_O + t));
+                            } else {
+                                if (!have_k) {
+                                    ok = full(kx);
+                                    if (!ok) continue;
+                                    tc_fence_after();
+                                    have_k = true;
+                                }
+                                qk(t, kx);
+                            }
+                        }
+                        if (!ok) break;
+                        tc_commit(bar(B_FREE + vx % L::slots));
+                        if (i + 1 < n) tc_commit(bar(B_FREE + kx % L::slots));
+                        if (i + 2 == n) tc_commit(bar(B_Q_FREE));
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                base += 2 * n;
+                ++items;
+            }
+            if (!ok && lane == 0) {
+                tc_commit(bar(B_DRAIN));
+                mbar_wait(bar(B_DRAIN), 0, nullptr, nullptr, 100000000ull);
+            }
+        }
+    } else {
+        // ============================ softmax ============================
+        regs_acquire<kRegsSoftmax>();
+        const int t = warp >> 2;
+        const int r = tid & 127;                            // row of the tile = TMEM lane
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + t * kTileCols;
+        int steps = 0, outs = 0;                            // barrier phases of this tile so far
+        bool ok = true;
+        while (ok && walk.next(p, it)) {
+            const int n = it.n[t];
+            if (it.skip) continue;
+            const int tok = it.tok0 + t * p.TR + r / G, head = it.h * G + r % G;
+            const bool valid = r < p.TR * G && tok < it.n_q;
+            // keys this row sees (a row of no token: all, its result is dropped)
+            const int lim = a.causal && valid ? max(0, min(it.kv_len, tok + it.kv_len - it.n_q + 1)) : it.kv_len;
+            const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+            const float rs = a.scale_log2;
+            float m_used = -INFINITY, l = 0.f;
+            auto page_bad = [&](int st) -> bool {
+                const int key = (it.s0 + st) * kStep + lane * p.box;
+                if (st >= n || lane >= p.boxes || key >= it.kv_len) return false;
+                const int pg = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
+                return (unsigned)pg >= (unsigned)a.kv.num_pages;
+            };
+            bool bad = false;
+            if constexpr (PAGED) bad = page_bad(0);
+            for (int st = 0; st < n; ++st) {
+                unsigned missing = 0;
+                if constexpr (PAGED) {
+                    missing = __ballot_sync(0xffffffffu, bad);
+                    bad = page_bad(st + 1);
+                }
+                ok = mbar_wait(bar(B_S + t), steps & 1, err, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                ++steps;
+                tc_fence_after();
+                uint32_t sv[128];
+                tmem_ld128_sync(lane_base, sv);
+                const int key0 = (it.s0 + st) * kStep;
+                if (lim_min < key0 + kStep || missing) {
+                    const int rel = lim - key0;
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j >= rel) sv[j] = __float_as_uint(-INFINITY);
+                    if (PAGED && missing) {
+#pragma unroll
+                        for (int j = 0; j < 128; ++j)
+                            if ((missing >> (j >> p.box_shift)) & 1u) sv[j] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sv[j]));
+                // the scale is positive and rounding monotonic: max of scaled = scaled max
+                const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rs);
+                const bool need = m_new > m_used + kRescale;
+                // the P.V before this step's Q.K^T is complete: O is settled
+                if (st > 0 && __any_sync(0xffffffffu, need)) {
+                    const float f = need ? fast_exp2(m_used - m_new) : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t ov[32];
+                        tmem_ld32_sync(lane_base + kOCol + 32 * c, ov);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * f);
+                        tmem_st32(lane_base + kOCol + 32 * c, ov);
+                    }
+                    l *= f;
+                }
+                if (need) m_used = m_new;
+                // (a row that has seen no key has only -inf scores: subtracting 0 gives P = 0)
+                const float sub = m_used == -INFINITY ? 0.f : m_used - kPShift;
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 64; ++k) {
+                    const float p0 = fast_exp2(fmaf(__uint_as_float(sv[2 * k]), rs, -sub));
+                    const float p1 = fast_exp2(fmaf(__uint_as_float(sv[2 * k + 1]), rs, -sub));
+                    ls[k & 3] += p0 + p1;
+                    sv[k] = E::pack2(p0, p1);
+                }
+                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                tmem_st32(lane_base, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                tmem_st32(lane_base + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(B_P + t));
+            }
+            if (!ok) break;
+            // ---- epilogue ----
+            if (n > 0) {
+                ok = mbar_wait(bar(B_O + t), outs & 1, err, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                ++outs;
+                tc_fence_after();
+            }
+            const bool none = l == 0.f;          // no visible key (a NaN sum is not that)
+            const int64_t row = (int64_t)(it.q_row + tok) * a.Hq + head;
+            const float inv = it.whole ? (none ? 0.f : 1.f / l) : 1.f;
+            float* part = p.ws_o + ((int64_t)it.split * a.tokens * a.Hq + row) * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                if (n > 0) {
+                    tmem_ld32_sync(lane_base + kOCol + 32 * c, ov);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) ov[j] = 0u;
+                }
+                if (!valid) continue;
+                if (it.whole) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<typename E::T*>(a.out) + row * D + 32 * c);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        auto two = [&](int x) {
+                            return none ? 0u : E::pack2(__uint_as_float(ov[x]) * inv, __uint_as_float(ov[x + 1]) * inv);
+                        };
+                        dst[j / 8] = make_uint4(two(j), two(j + 2), two(j + 4), two(j + 6));
+                    }
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(part + 32 * c);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) dst[j / 4] = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
+                }
+            }
+            // O has been read: the MMAs of the next item may overwrite it (they wait for its P)
+            tc_fence_before();
+            if (valid) {
+                if (!it.whole)
+                    *reinterpret_cast<float2*>(p.ws_ml + ((int64_t)it.split * a.tokens * a.Hq + row) * 2) =
+                        make_float2(m_used, l);
+                else if (a.lse)
+                    a.lse[row] = none ? -INFINITY : (m_used + __log2f(l) - kPShift) * kLn2;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the shares of every row whose keys were cut: one warp per row.
+template <class E, int D>
+__global__ void __launch_bounds__(256) attn_tc_merge(const TcParams p) {
+    const SeqAttn& a = p.a;
+    constexpr float kPShift = std::is_same<E, BF16>::value ? 0.f : 7.f;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    grid_dependency_wait();
+    if (row >= (int64_t)a.tokens * a.Hq) return;
+    const int t = (int)(row / a.Hq);
+    // the sequence of token t: the number of list entries behind the first that are <= t
+    int b = 0;
+    for (int x0 = 0; x0 < a.kv.num_seqs; x0 += 32) {
+        const int x = x0 + lane;
+        const int c = __popc(__ballot_sync(0xffffffffu, x < a.kv.num_seqs && a.cu_q[1 + x] <= t));
+        b += c;
+        if (c < 32) break;
+    }
+    if (b >= a.kv.num_seqs) return;
+    const int2 qr = seq_rows(a.cu_q, b, a.tokens);
+    if (t < qr.x || t >= qr.y) return;
+    const int n_q = qr.y - qr.x, kv_len = seq_keys(a.kv, b).y;
+    const int tok0 = (t - qr.x) / (2 * p.TR) * (2 * p.TR);
+    const int N = (visible(a, kv_len, n_q, min(tok0 + 2 * p.TR, n_q)) + kStep - 1) / kStep;
+    int first, count;
+    bool whole;
+    share(N, p.splits, 0, first, count, whole);
+    if (whole) return;
+    const int per = count, parts = (N + per - 1) / per;
+    const int64_t rows = (int64_t)a.tokens * a.Hq;
+    constexpr int W = D / 32;
+    float M = -INFINITY;
+    for (int s = 0; s < parts; ++s) M = fmaxf(M, p.ws_ml[(s * rows + row) * 2]);
+    float l = 0.f, acc[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+        const float2 x = *reinterpret_cast<const float2*>(p.ws_ml + (s * rows + row) * 2);
+        const float f = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);
+        l += f * x.y;
+        const float* src = p.ws_o + (s * rows + row) * D + lane * W;
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[i] += f * src[i];
+    }
+    const bool none = l == 0.f;
+    const float inv = none ? 0.f : 1.f / l;
+    typename E::T* out = static_cast<typename E::T*>(a.out) + row * D + lane * W;
+#pragma unroll
+    for (int i = 0; i < W; i += 2)
+        *reinterpret_cast<uint32_t*>(out + i) = none ? 0u : E::pack2(acc[i] * inv, acc[i + 1] * inv);
+    if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (M + __log2f(l) - kPShift) * kLn2;
+}
+
+// q, or packed k / v: [rows][heads][D] with rows `stride` elements apart; box
+// 64 dims x hb heads x rb rows, 128-byte swizzle.
+bool rows_map(CUtensorMap* m, const void* base, bool bf16, int D, int heads, int rows, int64_t stride, int hb, int rb) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t st[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)hb, (cuuint32_t)rb};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
+              dim, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A page pool: (dim, head, place, page) or, HND, (dim, place, head, page); box
+// 64 dims x `box` places.
+bool pool_map(CUtensorMap* m, const void* base, bool bf16, const SeqKV& kv, bool hnd, int box_rows) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t D = kv.D, H = kv.Hkv, P = kv.page_size;
+    const cuuint64_t dim[4] = {D, hnd ? P : H, hnd ? H : P, (cuuint64_t)kv.num_pages};
+    const cuuint64_t st[3] = {D * 2, (hnd ? P : H) * D * 2, H * P * D * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(hnd ? box_rows : 1), (cuuint32_t)(hnd ? 1 : box_rows), 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base),
+              dim, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class E, int D, bool PAGED>
+cudaError_t launch_tc_t(const TcParams& p, int64_t items, int num_sms, cudaStream_t stream) {
+    using L = TcSmem<D>;
+    const SeqAttn& a = p.a;
+    const bool bf16 = std::is_same<E, BF16>::value;
+    CUtensorMap mq, mk, mv;
+    if (!rows_map(&mq, a.q, bf16, D, a.Hq, a.tokens, a.q_stride, a.G, p.TR)) return cudaErrorInvalidValue;
+    if (PAGED ? (!pool_map(&mk, a.kv.k, bf16, a.kv, p.hnd, p.box) || !pool_map(&mv, a.kv.v, bf16, a.kv, p.hnd, p.box))
+              : (!rows_map(&mk, a.kv.k, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.s_tok, 1, kStep) ||
+                 !rows_map(&mv, a.kv.v, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.sv_tok, 1, kStep)))
+        return cudaErrorInvalidValue;
+    auto kern = attn_tc_kernel<E, D, PAGED>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::alloc);
+    if (err != cudaSuccess) return err;
+    // the register split assumes a launch with kRegsLaunch registers a thread
+    static int regs_ok = -1;
+    if (regs_ok < 0) {
+        cudaFuncAttributes fa;
+        err = cudaFuncGetAttributes(&fa, kern);
+        if (err != cudaSuccess) return err;
+        regs_ok = fa.numRegs == kRegsLaunch ? 1 : 0;
+    }
+    if (!regs_ok) return cudaErrorInvalidConfiguration;
+    const int grid = (int)(items < num_sms ? items : num_sms);
+    err = launch_pdl(kern, dim3(grid), dim3(kThreads), L::alloc, stream, mq, mk, mv, p);
+    if (err != cudaSuccess) return err;
+    count_launches(1);
+    if (p.splits > 1) {
+        const int64_t rows = (int64_t)a.tokens * a.Hq;
+        err = launch_pdl(attn_tc_merge<E, D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p);
+        if (err == cudaSuccess) count_launches(1);
+    }
+    return err;
+}
+
+// Items of the call at most: every sequence may end in a part tile.
+int64_t items_bound(int num_seqs, int tokens, int Hkv, int TR) {
+    const int64_t tiles = (int64_t)tokens / (2 * TR) + (num_seqs < tokens ? num_seqs : tokens);
+    return (tiles > 0 ? tiles : 1) * Hkv;
+}
+
+// Shares the keys of an item are cut into: enough for every SM to have one
+// when the items are fewer (counting one item per 2 TR rows, at least one a
+// sequence with rows).
+int splits_for(int num_seqs, int tokens, int Hkv, int TR, int num_sms) {
+    const int64_t tiles = (tokens + 2 * TR - 1) / (2 * TR);
+    const int64_t items = (tiles > num_seqs ? tiles : (num_seqs < tokens ? num_seqs : tokens)) * Hkv;
+    const int64_t s = items > 0 ? num_sms / items : 1;
+    return (int)(s < 1 ? 1 : s);
+}
+
+}  // namespace
+
+bool attn_tc_supported(const SeqKV& kv, int G) {
+    if (G > kTileM) return false;
+    if (!kv.page_table) return true;
+    return kv.f8 == 0 && kv.page_size % 16 == 0;
+}
+
+size_t attn_tc_ws_bytes(int num_seqs, int tokens, int Hq, int Hkv, int D, int num_sms) {
+    const int G = Hq / Hkv;
+    if (G > kTileM || tokens < 1) return 0;
+    const int s = splits_for(num_seqs, tokens, Hkv, kTileM / G, num_sms);
+    return s > 1 ? (size_t)s * tokens * Hq * (D + 2) * 4 : 0;
+}
+
+cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaStream_t stream) {
+    TcParams p{};
+    p.a = a;
+    p.TR = kTileM / a.G;
+    p.splits = splits_for(a.kv.num_seqs, a.tokens, a.kv.Hkv, p.TR, num_sms);
+    p.hnd = a.kv.s_tok == a.kv.D && a.kv.Hkv > 1 ? 1 : 0;
+    p.box = kStep;
+    if (a.kv.page_table)
+        while (a.kv.page_size % p.box != 0) p.box /= 2;
+    p.boxes = kStep / p.box;
+    while ((1 << p.box_shift) < p.box) ++p.box_shift;
+    p.ws_o = static_cast<float*>(a.ws);
+    p.ws_ml = p.ws_o + (int64_t)p.splits * a.tokens * a.Hq * a.kv.D;
+    const int64_t items = items_bound(a.kv.num_seqs, a.tokens, a.kv.Hkv, p.TR) * p.splits;
+    const bool bf16 = dtype == SFA_DTYPE_BF16;
+#define SFA_ATTN_TC(D_, PAGED_)                                                      \
+    return bf16 ? launch_tc_t<BF16, D_, PAGED_>(p, items, num_sms, stream)           \
+                : launch_tc_t<F16, D_, PAGED_>(p, items, num_sms, stream);
+    if (a.kv.D == 128) {
+        if (a.kv.page_table) { SFA_ATTN_TC(128, true) }
+        SFA_ATTN_TC(128, false)
+    }
+    if (a.kv.page_table) { SFA_ATTN_TC(64, true) }
+    SFA_ATTN_TC(64, false)
+#undef SFA_ATTN_TC
+}
+
+}  // namespace sfa

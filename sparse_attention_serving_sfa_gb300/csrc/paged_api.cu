@@ -57,7 +57,16 @@ sfa_status resolve_cache(const paged_kv* c, SeqKV& kv) {
 
 // A token stride (elements) of packed rows of `heads` heads.
 bool bad_stride(int64_t stride, int heads, int D) {
-    return stride < (int64_t)heads * D || stride % 8 != 0 || stride > (int64_t)1 << 40;
+    return stride < (int64_t)heads * D || stride % 8 != 0 || stride > (int64_t)1 << 38;
+}
+
+constexpr int kFewRows = 16;
+
+// Workspace of either path.
+size_t attention_ws_bytes(int num_seqs, int tokens, int Hq, int Hkv, int D) {
+    const size_t r = attn_rows_ws_bytes(D);
+    const size_t t = attn_tc_ws_bytes(num_seqs, tokens, Hq, Hkv, D, num_sms());
+    return r > t ? r : t;
 }
 
 sfa_status run_attention(SeqAttn& p, int num_tokens, int num_qo_heads, int max_q_len, float scale,
@@ -72,7 +81,7 @@ sfa_status run_attention(SeqAttn& p, int num_tokens, int num_qo_heads, int max_q
     if ((int64_t)num_tokens * num_qo_heads > 0x7fffffffLL / 2) return SFA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return SFA_OK;
     if (!q || !out || !al(q, 16) || !al(out, 16) || !al(lse, 4)) return SFA_ERR_INVALID_ARG;
-    const size_t need = attn_rows_ws_bytes(p.kv.D);
+    const size_t need = attention_ws_bytes(p.kv.num_seqs, num_tokens, num_qo_heads, p.kv.Hkv, p.kv.D);
     if (!ws || ws_bytes < need) return SFA_ERR_WORKSPACE;
     if (!al(ws, 16)) return SFA_ERR_INVALID_ARG;
     p.q = q; p.out = out; p.lse = lse; p.cu_q = cu_q;
@@ -83,7 +92,18 @@ sfa_status run_attention(SeqAttn& p, int num_tokens, int num_qo_heads, int max_q
     p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)p.kv.D)) * kLog2e;
     p.ws = ws;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return launch_attn_rows(p, dtype, num_sms(), s) == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+    // Few rows a kv head: one 16-row tile reads the keys at HBM's pace, the
+    // 128-row tensor-core tiles would stand mostly empty.
+    const bool few = (int64_t)p.max_q_len * p.G <= kFewRows;
+    cudaError_t err;
+    if (!few && attn_tc_supported(p.kv, p.G)) {
+        p.err_word = device_error_word();
+        if (!p.err_word) return SFA_ERR_CUDA;
+        err = launch_attn_tc(p, dtype, num_sms(), s);
+    } else {
+        err = launch_attn_rows(p, dtype, num_sms(), s);
+    }
+    return err == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
 }  // namespace
@@ -127,7 +147,7 @@ sfa_status varlen_workspace_size(int num_seqs, int num_tokens, int num_qo_heads,
     if (!bytes || num_seqs < 1 || num_tokens < 0) return SFA_ERR_INVALID_ARG;
     sfa_status st = check_heads(num_qo_heads, num_kv_heads, head_dim);
     if (st != SFA_OK) return st;
-    *bytes = attn_rows_ws_bytes(head_dim);
+    *bytes = attention_ws_bytes(num_seqs, num_tokens, num_qo_heads, num_kv_heads, head_dim);
     return SFA_OK;
 }
 
