@@ -496,76 +496,34 @@ def sparse_flash_attention(query, key, value, sparse_indices, scale, layout="BSN
 
 
 # ---------------------------------------------------------------------------
-# Paged KV cache, and dense attention over it and over packed rows.  These take
-# torch tensors, check what the C entry points cannot see (shapes, strides,
-# element types, devices) and run on the tensors' device, on torch's current
-# stream of that device unless `stream` is given.
+# Paged KV cache, and dense attention over it and over packed rows.  paged_append,
+# paged_read, paged_attention and varlen_attention take torch tensors; the module
+# _tensors checks what the C entry points cannot see (shapes, strides, element
+# types, devices: ValueError) and calls them on the tensors' device, on torch's
+# current stream of that device unless `stream` is given.
 
-def _dtype_name(t):
-    import torch
-    names = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float8_e4m3fn: "e4m3",
-             torch.float8_e5m2: "e5m2"}
-    if t not in names:
-        raise ValueError(f"element type {t} is not one of {sorted(DTYPES)}")
-    return names[t]
+_tensors = None
 
 
-def _expect(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-def _rows(x, name, heads=None, dim=None):
-    """(tokens, heads, dim) rows whose heads are contiguous; returns the token stride."""
-    _expect(x.ndim == 3, f"{name}: (tokens, heads, head_dim) expected, got {tuple(x.shape)}")
-    _expect((heads is None or x.shape[1] == heads) and (dim is None or x.shape[2] == dim),
-            f"{name}: {heads} heads of {dim} expected, got {tuple(x.shape)}")
-    T, H, D = x.shape
-    _expect((D < 2 or x.stride(2) == 1) and (H < 2 or x.stride(1) == D),
-            f"{name}: the heads of a row must be contiguous")
-    # the stride of a single row says nothing: its heads' extent serves
-    return x.stride(0) if T > 1 else H * D
-
-
-def _list(x, name, device, n=None):
-    import torch
-    _expect(x.dtype == torch.int32 and x.is_contiguous() and x.device == device,
-            f"{name}: contiguous int32 on {device} expected")
-    _expect(n is None or x.numel() == n, f"{name}: {n} entries expected, got {x.numel()}")
-
-
-def _scales(x, name, device, heads):
-    import torch
-    if x is not None:
-        _expect(x.dtype == torch.float32 and x.is_contiguous() and x.device == device and
-                x.numel() == heads, f"{name}: contiguous float32 ({heads},) on {device} expected")
-
-
-def _on(device, stream):
-    """(guard making `device` current, stream handle)."""
-    import torch
-    _expect(device.type == "cuda", "tensors on a CUDA device expected")
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return torch.cuda.device(device), _stream(s)
-
-
-def _paged_kv(k_pages, v_pages, page_table, kv_lens, kv_layout, scale_k, scale_v):
-    _expect(k_pages.ndim == 4 and k_pages.shape == v_pages.shape and
-            k_pages.dtype == v_pages.dtype and k_pages.device == v_pages.device and
-            k_pages.is_contiguous() and v_pages.is_contiguous(),
-            "k_pages and v_pages: contiguous 4-D pools of one shape, type and device expected")
-    layout = _enum(kv_layout, KV_LAYOUTS)
-    pages, a, b, dim = k_pages.shape
-    page_size, heads = (b, a) if layout == KV_LAYOUTS["HND"] else (a, b)
-    dev = k_pages.device
-    _expect(page_table.ndim == 2, "page_table: (num_seqs, max_pages) expected")
-    _list(page_table, "page_table", dev)
-    _list(kv_lens, "kv_lens", dev, page_table.shape[0])
-    _scales(scale_k, "scale_k", dev, heads)
-    _scales(scale_v, "scale_v", dev, heads)
-    return PagedKV(_ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens),
-                   page_table.shape[0], pages, page_size, page_table.shape[1], heads, dim, layout,
-                   DTYPES[_dtype_name(k_pages.dtype)], _ptr(scale_k), _ptr(scale_v))
+def _native():
+    """The module _tensors, bound to the library (raises if it is missing)."""
+    global _tensors
+    if _tensors is None:
+        import importlib.util
+        lib = load()
+        with _lock:
+            if _tensors is None:
+                path = _build.tensors_path()
+                if not os.path.exists(path):
+                    raise RuntimeError(f"{path} is not built; call build() first")
+                spec = importlib.util.spec_from_file_location(__name__ + "._tensors", path)
+                mod = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(mod)
+                mod.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
+                           (lib.paged_append, lib.paged_read, lib.paged_run,
+                            lib.paged_workspace_size, lib.varlen_run)])
+                _tensors = mod
+    return _tensors
 
 
 def paged_append(k_new, v_new, cu_seqlens, k_pages, v_pages, page_table, kv_lens, kv_layout="NHD",
@@ -573,18 +531,11 @@ def paged_append(k_new, v_new, cu_seqlens, k_pages, v_pages, page_table, kv_lens
     """Forwards to paged_append(): writes the packed rows k_new, v_new (tokens,
     kv heads, head_dim) into the pools as the newest tokens of their sequences
     (kv_lens counts them already)."""
-    c = _paged_kv(k_pages, v_pages, page_table, kv_lens, kv_layout, scale_k, scale_v)
-    dev = k_pages.device
-    _expect(k_new.shape == v_new.shape and k_new.dtype == v_new.dtype and k_new.device == dev and
-            v_new.device == dev, "k_new and v_new: one shape and type, on the pools' device, expected")
-    ks = _rows(k_new, "k_new", c.num_kv_heads, c.head_dim)
-    vs = _rows(v_new, "v_new", c.num_kv_heads, c.head_dim)
-    _list(cu_seqlens, "cu_seqlens", dev, c.num_seqs + 1)
-    guard, s = _on(dev, stream)
-    with guard:
-        _check(load().paged_append(ctypes.byref(c), _ptr(k_new), _ptr(v_new), ks, vs,
-                                   _ptr(cu_seqlens), k_new.shape[0],
-                                   DTYPES[_dtype_name(k_new.dtype)], s), "paged_append")
+    st = (_tensors or _native()).paged_append(k_new, v_new, cu_seqlens, k_pages, v_pages, page_table,
+                                              kv_lens, _enum(kv_layout, KV_LAYOUTS), scale_k, scale_v,
+                                              _stream(stream))
+    if st:
+        raise SfaError(st, "paged_append")
 
 
 def paged_read(k_pages, v_pages, page_table, kv_lens, cu_seqlens, num_tokens, dtype=None,
@@ -594,26 +545,13 @@ def paged_read(k_pages, v_pages, page_table, kv_lens, cu_seqlens, num_tokens, dt
     head_dim).  dtype: "f16" / "bf16" (default: a 16-bit cache's own, else bf16);
     out: a pair of tensors to write instead of new ones (rows of no sequence
     are left alone; in new tensors they are unset)."""
-    import torch
-    c = _paged_kv(k_pages, v_pages, page_table, kv_lens, kv_layout, scale_k, scale_v)
-    dev = k_pages.device
-    _list(cu_seqlens, "cu_seqlens", dev, c.num_seqs + 1)
-    guard, s = _on(dev, stream)
-    shape = (int(num_tokens), c.num_kv_heads, c.head_dim)
-    if out is None:
-        if dtype is None:
-            t = k_pages.dtype if k_pages.element_size() == 2 else torch.bfloat16
-        else:
-            t = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
-        out = tuple(torch.empty(shape, dtype=t, device=dev) for _ in range(2))
-    for x in out:
-        _expect(tuple(x.shape) == shape and x.is_contiguous() and x.device == dev and
-                x.dtype == out[0].dtype, f"out: two contiguous {shape} tensors on {dev} expected")
-    with guard:
-        _check(load().paged_read(ctypes.byref(c), _ptr(cu_seqlens), shape[0],
-                                 DTYPES[_dtype_name(out[0].dtype)], _ptr(out[0]), _ptr(out[1]), s),
-               "paged_read")
-    return tuple(out)
+    st, k, v = (_tensors or _native()).paged_read(
+        k_pages, v_pages, page_table, kv_lens, cu_seqlens, num_tokens,
+        -1 if dtype is None else _enum(dtype, DTYPES), _enum(kv_layout, KV_LAYOUTS), scale_k, scale_v,
+        *((None, None) if out is None else out), _stream(stream))
+    if st:
+        raise SfaError(st, "paged_read")
+    return k, v
 
 
 def paged_workspace_size(num_seqs, num_tokens, num_qo_heads, num_kv_heads, head_dim) -> int:
@@ -656,25 +594,6 @@ def varlen_run(q, k, v, q_stride, k_stride, v_stride, cu_seqlens_q, cu_seqlens_k
     return st
 
 
-def _attention_outputs(q, out, lse, return_lse, workspace, need):
-    import torch
-    dev = q.device
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _expect(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and
-            out.device == dev, "out: a contiguous tensor of q's shape, type and device expected")
-    if lse is None and return_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    if lse is not None:
-        _expect(lse.shape == q.shape[:2] and lse.dtype == torch.float32 and lse.is_contiguous() and
-                lse.device == dev, "lse: contiguous float32 (tokens, qo heads) on q's device expected")
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _expect(workspace.device == dev and workspace.is_contiguous(),
-            "workspace: a contiguous tensor on q's device expected")
-    return out, lse, workspace, workspace.numel() * workspace.element_size()
-
-
 def paged_attention(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, scale=0.0, causal=True,
                     kv_layout="NHD", scale_k=None, scale_v=None, return_lse=False, max_q_len=0,
                     out=None, lse=None, workspace=None, stream=None):
@@ -682,18 +601,12 @@ def paged_attention(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, scal
     Outputs and the workspace are allocated here unless given (a workspace
     from here belongs to this call alone; rows of no sequence are left alone,
     so in a new out they are unset)."""
-    c = _paged_kv(k_pages, v_pages, page_table, kv_lens, kv_layout, scale_k, scale_v)
-    dev = k_pages.device
-    _expect(q.device == dev, "q on the pools' device expected")
-    qs = _rows(q, "q", None, c.head_dim)
-    _list(cu_seqlens_q, "cu_seqlens_q", dev, c.num_seqs + 1)
-    T, Hq = q.shape[:2]
-    guard, s = _on(dev, stream)
-    with guard:
-        need = paged_workspace_size(c.num_seqs, T, Hq, c.num_kv_heads, c.head_dim)
-        out, lse, ws, n = _attention_outputs(q, out, lse, return_lse, workspace, need)
-        paged_run(c, q, qs, cu_seqlens_q, T, Hq, max_q_len, scale, causal, _dtype_name(q.dtype), out,
-                  lse, ws, n, s)
+    st, out, lse = (_tensors or _native()).paged_attention(
+        q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, scale, causal,
+        _enum(kv_layout, KV_LAYOUTS), scale_k, scale_v, return_lse, max_q_len, out, lse, workspace,
+        _stream(stream))
+    if st:
+        raise SfaError(st, "paged_attention")
     return (out, lse) if return_lse else out
 
 
@@ -702,19 +615,9 @@ def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=0.0, causal=True
     """varlen_run() on torch tensors: q (tokens, qo heads, head_dim), k and v
     (keys, kv heads, head_dim), packed.  Outputs and workspace as
     paged_attention."""
-    dev = q.device
-    _expect(k.device == dev and v.device == dev and k.dtype == q.dtype and v.dtype == q.dtype and
-            k.shape == v.shape, "q, k, v: one type and device, k and v of one shape, expected")
-    qs = _rows(q, "q")
-    ks, vs = _rows(k, "k", None, q.shape[2]), _rows(v, "v", None, q.shape[2])
-    _list(cu_seqlens_q, "cu_seqlens_q", dev)
-    _list(cu_seqlens_k, "cu_seqlens_k", dev, cu_seqlens_q.numel())
-    T, Hq, D = q.shape
-    B = cu_seqlens_q.numel() - 1
-    guard, s = _on(dev, stream)
-    with guard:
-        need = varlen_workspace_size(B, T, Hq, k.shape[1], D)
-        out, lse, ws, n = _attention_outputs(q, out, lse, return_lse, workspace, need)
-        varlen_run(q, k, v, qs, ks, vs, cu_seqlens_q, cu_seqlens_k, B, T, k.shape[0], Hq, k.shape[1],
-                   D, max_q_len, scale, causal, _dtype_name(q.dtype), out, lse, ws, n, s)
+    st, out, lse = (_tensors or _native()).varlen_attention(
+        q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, return_lse, max_q_len, out, lse,
+        workspace, _stream(stream))
+    if st:
+        raise SfaError(st, "varlen_attention")
     return (out, lse) if return_lse else out

@@ -1,4 +1,6 @@
-"""Builds libsfa_gb300.so from csrc/*.cu with nvcc for sm_103a (in-tree)."""
+"""Builds libsfa_gb300.so from csrc/*.cu with nvcc for sm_103a, and the module
+_tensors (csrc/tensors.cpp: argument marshalling for torch tensors) with g++
+against the installed torch's headers (both in-tree)."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -12,6 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build", "sfa_gb300")
 LIB_PATH = os.path.join(PKG, "libsfa_gb300.so")
+TENSORS_SRC = os.path.join(CSRC, "tensors.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]
@@ -33,16 +36,57 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def tensors_path() -> str:
+    """The _tensors module of this Python and torch (their C++ interfaces change
+    between versions, so another pair builds its own)."""
+    import sysconfig
+
+    import torch
+    tag = "".join(c if c.isalnum() else "_" for c in torch.__version__)
+    return os.path.join(PKG, f"_tensors_torch_{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _older(path, deps) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(f) > os.path.getmtime(path) for f in deps)
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(f) > t for f in _deps())
+    return _older(LIB_PATH, _deps())
+
+
+def tensors_stale() -> bool:
+    return _older(tensors_path(), [TENSORS_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def build_tensors() -> str:
+    """Compile the _tensors module."""
+    import sysconfig
+
+    import torch
+    where = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.sep in _nvcc() else "/usr/local/cuda"
+    include = [os.path.join(where, "include"), os.path.join(where, "include/torch/csrc/api/include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(where, "lib")
+    out = tensors_path()
+    tmp = out + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
+           *[x for i in include for x in ("-isystem", i)],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-o", tmp, TENSORS_SRC,
+           "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on tensors.cpp:\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every kernel source (in parallel) and link the shared library."""
+    """Compile every kernel source (in parallel) and link the shared library;
+    compile the _tensors module beside it."""
     if not force and not stale():
+        if tensors_stale():
+            build_tensors()
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -58,7 +102,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        tensors = ex.submit(build_tensors) if force or tensors_stale() else None
         results = list(ex.map(compile_one, _sources()))
+        if tensors is not None:
+            tensors.result()
     if verbose:
         for _, log in results:
             print(log)
