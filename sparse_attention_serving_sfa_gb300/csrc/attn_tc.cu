@@ -22,9 +22,19 @@
 //   - MMA thread: S_t = Q_t K^T into TMEM, O_t += P_t V with P from TMEM and
 //     V an MN-major operand; tile 0's P.V and next Q.K^T run while the
 //     softmax works on tile 1, and the other way round.
-//   - producer warp: Q tiles and a ring of 128-key K and V tiles by TMA, in
-//     the order the MMAs use them, running ahead across items.
+//   - producer: Q tiles and a ring of 128-key K and V tiles in the order the
+//     MMAs use them, running ahead across items.  Packed rows and 16-bit pages
+//     of a multiple of 16 tokens come by TMA (one warp; a page is a box of a
+//     4-D map).  8-bit pages, and 16-bit pages of other sizes, come row by row
+//     through three warps' 16-byte cp.async: 8-bit rows into a staging tile,
+//     from which the thread that copied a piece writes it out as fp16 (exact)
+//     into the 128-byte-swizzled tile the MMA reads.  Rows without a key are
+//     zeros.
 // TMEM: tile t at column 256 t: S / P in [0, 128), O in [128, 128 + D).
+//
+// With an 8-bit cache both products run in fp16.  bf16 rows of q are scaled to
+// a largest magnitude in [8, 16) by a power of two each (elements below 2^-28
+// of the row's largest round), which leaves with the scores.
 //
 // P is rounded once to 16 bits (at most half a step of the output's type per
 // weight, so the output moves by no more than its own rounding of
@@ -33,8 +43,8 @@
 // largest stay normal.  Sums of P use the unrounded fp32 values.
 //
 // V rows behind kv_len (the next sequence's, or whatever a page holds) would
-// turn 0 x NaN into NaN: the producer waits for such a tile itself, writes
-// zeros over those rows and then hands it on.
+// turn 0 x NaN into NaN: where TMA brought them the producer waits for such a
+// tile itself, writes zeros over those rows and then hands it on.
 #include <type_traits>
 
 #include "common.cuh"
@@ -50,6 +60,7 @@ constexpr int kTileM = 128;
 constexpr int kStep = 128;                  // keys of a step
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kGather = 96;                 // threads of the gathering producer (warps 9, 10, 11)
 constexpr int kThreads = 384;
 constexpr int kRegsLaunch = 168, kRegsControl = 80, kRegsSoftmax = 208;
 static_assert(kRegsSoftmax * kSoftWarps * 32 + kRegsControl * 128 <= kRegsLaunch * kThreads,
@@ -58,16 +69,24 @@ constexpr int kTmemCols = 512, kTileCols = 256, kOCol = 128;
 constexpr float kRescale = 8.0f;            // log2 units
 constexpr int kMinSplitSteps = 4;           // steps below which a share is not cut further
 
-template <int D>
+// Where K and V come from: packed rows, or pages by TMA; or gathered rows of
+// 16-bit, E4M3 or E5M2 pages.
+enum { SRC_PACKED = 0, SRC_PAGES = 1, SRC_G16 = 2, SRC_E4M3 = 3, SRC_E5M2 = 4 };
+
+template <int D, int SRC>
 struct TcSmem {
+    static constexpr bool f8 = SRC >= SRC_E4M3, gather = SRC >= SRC_G16;
     static constexpr int panels = D / 64;
     static constexpr int panel = kStep * 128;              // 128 rows x 128 bytes
     static constexpr int tile = panels * panel;            // Q, K or V tile
-    static constexpr int slots = D == 128 ? 5 : 8;
+    static constexpr int slots = D == 128 ? (f8 ? 4 : 5) : 8;
     static constexpr int q = 0;
     static constexpr int ring = 2 * tile;
-    static constexpr int bars = ring + slots * tile;
-    static constexpr int abort = bars + 8 * 40;
+    static constexpr int staging = ring + slots * tile;    // two tiles of 8-bit rows
+    static constexpr int rows = staging + (f8 ? 2 * kStep * D : 0);   // row numbers of two steps
+    static constexpr int expo = rows + (gather ? 2 * kStep * 4 : 0);  // exponents of q's rows
+    static constexpr int bars = expo + (f8 ? 2 * kTileM : 0);
+    static constexpr int abort = bars + 8 * 32;
     static constexpr int tmem_slot = abort + 4;
     static constexpr int total = abort + 16;
     static constexpr int alloc = total + 1024;             // room to align the base to 1024
@@ -82,8 +101,10 @@ enum {
     B_O = 6,            // + t: O_t of the item complete
     B_TAIL = 8,         // V tile landed whose tail is still to be cleared
     B_DRAIN = 9,
-    B_FULL = 10,        // + slot
-    B_FREE = 20         // + slot
+    B_EXPO = 10,        // + t: the softmax has read the exponents of tile t's rows
+    B_FULL = 12,        // + slot
+    B_FREE = 20,        // + slot
+    B_ROWS = 28         // row numbers of a step written
 };
 
 struct TcParams {
@@ -183,12 +204,193 @@ struct Walk {
     }
 };
 
-template <class E, int D, bool PAGED>
+// Two 8-bit codes (low 16 bits of x) as two fp16.
+template <bool E5>
+__device__ __forceinline__ uint32_t codes_h2(uint32_t x) {
+    const uint16_t in = (uint16_t)x;
+    uint32_t h;
+    if constexpr (E5) asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(in));
+    else asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(in));
+    return h;
+}
+
+// The gathering producer: three warps, thread x of kGather.  Tile y of an item
+// (K of step y / 2, then its V) is copied while tile y - 1 is finished.
+template <class E, int D, int SRC>
+__device__ __forceinline__ void gather_rows(const TcParams& p, const CUtensorMap& mq, unsigned char* smem,
+                                            uint32_t sbase, int x) {
+    using L = TcSmem<D, SRC>;
+    constexpr bool F8 = L::f8, E5 = SRC == SRC_E5M2;
+    constexpr bool kScaledQ = F8 && std::is_same<E, BF16>::value;
+    constexpr int EB = F8 ? 1 : 2, RB = D * EB;
+    constexpr int PR = RB / 16;                              // 16-byte pieces of a row
+    constexpr int kPieces = kStep * PR;
+    const SeqAttn& a = p.a;
+    int* err = a.err_word;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort);
+    auto bar = [&](int i) { return sbase + L::bars + 8 * i; };
+    uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::rows);
+    const bool hnd = p.hnd != 0;
+    Walk walk;
+    Item it;
+    int items = 0, loads = 0, tables = 0;
+    int read[2] = {0, 0};            // items whose tile t had keys
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+        const int n = max(it.n[0], it.n[1]);
+        if (n == 0) continue;
+        // row numbers (in units of D elements) of step st's keys.  (The table
+        // of a step is written over two steps later: by then every thread
+        // has passed the barrier of the step between, after its last read.)
+        auto find_rows = [&](int st) -> bool {
+            for (int i = x; i < kStep; i += kGather) {
+                const int key = (it.s0 + st) * kStep + i;
+                uint32_t row = 0xffffffffu;
+                if (key < it.kv_len) {
+                    const int slot = key / a.kv.page_size, place = key - slot * a.kv.page_size;
+                    const int pg = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + slot];
+                    if ((unsigned)pg < (unsigned)a.kv.num_pages)
+                        row = hnd ? ((uint32_t)pg * a.kv.Hkv + it.h) * a.kv.page_size + place
+                                  : ((uint32_t)pg * a.kv.page_size + place) * a.kv.Hkv + it.h;
+                }
+                rows[(st & 1) * kStep + i] = row;
+            }
+            mbar_arrive(bar(B_ROWS));
+            return mbar_wait(bar(B_ROWS), tables++ & 1, err, abort_flag);
+        };
+        // tile y, ring index `load`
+        auto copy = [&](int y, int load) -> bool {
+            if (y < 2 * n) {
+                const int st = y >> 1;
+                if (!(y & 1) && !__all_sync(0xffffffffu, find_rows(st))) return false;
+                const char* src = static_cast<const char*>((y & 1) ? a.kv.v : a.kv.k);
+                unsigned char* stage = smem + L::staging + (y & 1) * kStep * D;
+                unsigned char* slot = smem + L::ring + (load % L::slots) * L::tile;
+#pragma unroll 4
+                for (int id = x; id < kPieces; id += kGather) {
+                    const int r = id / PR, ch = id % PR;
+                    const uint32_t row = rows[(st & 1) * kStep + r];
+                    const bool in = row != 0xffffffffu;
+                    unsigned char* dst = F8 ? stage + id * 16
+                                            : slot + (ch >> 3) * L::panel + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                    cp_async_16_zfill(dst, src + (in ? (int64_t)row * RB + ch * 16 : 0), in ? 16 : 0);
+                }
+            }
+            cp_async_commit();
+            return true;
+        };
+        auto wait_free = [&](int load) {
+            return load < L::slots || mbar_wait(bar(B_FREE + load % L::slots), (load / L::slots - 1) & 1, err, abort_flag);
+        };
+        auto all = [](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+
+        // ---- Q ----
+        if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
+        if constexpr (kScaledQ) {
+            for (int t = 0; t < 2; ++t) {
+                if (ok && read[t] > 0) ok = mbar_wait(bar(B_EXPO + t), (read[t] - 1) & 1, err, abort_flag);
+                if (it.n[t] > 0) ++read[t];
+            }
+            ok = all(ok);
+            if (ok) {
+                constexpr int PQ = D / 8;                    // pieces of a q row, one lane each
+                signed char* expo = reinterpret_cast<signed char*>(smem + L::expo);
+                const int ch = x % PQ, tr = p.TR * a.G;
+#pragma unroll 8
+                for (int id = x; id < 2 * kTileM * PQ; id += kGather) {
+                    const int r = id / PQ, t = r / kTileM, rr = r % kTileM;
+                    const int tok = it.tok0 + t * p.TR + rr / a.G;
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (rr < tr && tok < it.n_q)
+                        w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                            (int64_t)(it.q_row + tok) * a.q_stride +
+                                                            (it.h * a.G + rr % a.G) * D + ch * 8);
+                    uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                    float top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = BF16::unpack2(v[i]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+#pragma unroll
+                    for (int o = 1; o < PQ; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e8 = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
+                    const int e = (top == 0.f || e8 > 127) ? 0 : min(max(e8 - 3, -120), 120);
+                    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 y = BF16::unpack2(v[i]);
+                        v[i] = F16::pack2(y.x * f, y.y * f);
+                    }
+                    *reinterpret_cast<uint4*>(smem + L::q + t * L::tile + (ch >> 3) * L::panel + rr * 128 +
+                                              (((ch & 7) ^ (rr & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    if (ch == 0) expo[r] = (signed char)e;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(B_Q));
+            }
+        } else if (ok && x == 0) {
+            const int tiles = it.tok0 + p.TR < it.n_q ? 2 : 1;
+            mbar_arrive_expect_tx(bar(B_Q), tiles * L::panels * p.TR * a.G * 128);
+            for (int t = 0; t < tiles; ++t)
+                for (int pn = 0; pn < L::panels; ++pn)
+                    tma_load_3d(sbase + L::q + t * L::tile + pn * L::panel, &mq, pn * 64, it.h * a.G,
+                                it.q_row + it.tok0 + t * p.TR, bar(B_Q));
+        }
+        ok = all(ok);
+        ++items;
+
+        // ---- K and V ----
+        if (!F8 && ok) ok = all(wait_free(loads));
+        if (ok) ok = copy(0, loads);
+        for (int y = 0; y < 2 * n && ok; ++y) {
+            // tile y + 1 on its way: 8-bit into the other staging tile (this
+            // thread has finished what it held there), 16-bit into its slot
+            if (!F8 && y + 1 < 2 * n) {
+                ok = all(wait_free(loads + 1));
+                if (!ok) break;
+            }
+            ok = copy(y + 1, loads + 1);
+            if (!ok) break;
+            cp_async_wait<1>();
+            if constexpr (F8) {
+                ok = all(wait_free(loads));
+                if (!ok) break;
+                const unsigned char* stage = smem + L::staging + (y & 1) * kStep * D;
+                unsigned char* slot = smem + L::ring + (loads % L::slots) * L::tile;
+#pragma unroll 2
+                for (int id = x; id < kPieces; id += kGather) {
+                    const int r = id / PR, ch = id % PR;
+                    const uint4 c = *reinterpret_cast<const uint4*>(stage + id * 16);
+                    const uint4 lo = make_uint4(codes_h2<E5>(c.x), codes_h2<E5>(c.x >> 16), codes_h2<E5>(c.y),
+                                                codes_h2<E5>(c.y >> 16));
+                    const uint4 hi = make_uint4(codes_h2<E5>(c.z), codes_h2<E5>(c.z >> 16), codes_h2<E5>(c.w),
+                                                codes_h2<E5>(c.w >> 16));
+                    unsigned char* to = slot + (ch >> 2) * L::panel + r * 128;
+                    const int c0 = (ch & 3) * 2, first = ch >> 2;     // panels start on opposite halves: no bank twice
+                    *reinterpret_cast<uint4*>(to + (((c0 + first) ^ (r & 7)) << 4)) = first ? hi : lo;
+                    *reinterpret_cast<uint4*>(to + (((c0 + 1 - first) ^ (r & 7)) << 4)) = first ? lo : hi;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(bar(B_FULL + loads % L::slots));
+            ++loads;
+        }
+    }
+    cp_async_wait<0>();
+    if (!ok && !kScaledQ && x == 0 && items > 0)
+        mbar_wait(bar(B_Q), (items - 1) & 1, nullptr, nullptr, 100000000ull);   // the copy in flight lands
+}
+
+template <class E, int D, int SRC>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const TcParams p) {
-    using L = TcSmem<D>;
-    constexpr bool kBf16 = std::is_same<E, BF16>::value;
+    using L = TcSmem<D, SRC>;
+    constexpr bool PAGED = SRC != SRC_PACKED, F8 = L::f8;
+    constexpr bool kScaledQ = F8 && std::is_same<E, BF16>::value;    // q's rows go to fp16
+    using M = typename std::conditional<F8, F16, E>::type;           // element type of the MMAs
+    constexpr bool kBf16 = std::is_same<M, BF16>::value;
     constexpr uint32_t kIdescQK = idesc_f16(kTileM, kStep, kBf16, false, false);
     constexpr uint32_t kIdescPV = idesc_f16(kTileM, D, kBf16, false, true);
     constexpr float kPShift = kBf16 ? 0.f : 7.f;
@@ -206,7 +408,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort);
     if (tid == 0) {
         *abort_flag = 0;
-        mbar_init(bar(B_Q), 1);
+        mbar_init(bar(B_Q), kScaledQ ? kGather : 1);
+        mbar_init(bar(B_ROWS), kGather);
         mbar_init(bar(B_Q_FREE), 1);
         mbar_init(bar(B_TAIL), 1);
         mbar_init(bar(B_DRAIN), 1);
@@ -214,9 +417,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(bar(B_S + t), 1);
             mbar_init(bar(B_P + t), 128);
             mbar_init(bar(B_O + t), 1);
+            mbar_init(bar(B_EXPO + t), kTileM);
         }
         for (int s = 0; s < L::slots; ++s) {
-            mbar_init(bar(B_FULL + s), 1);
+            mbar_init(bar(B_FULL + s), L::gather ? kGather : 1);
             mbar_init(bar(B_FREE + s), 1);
         }
         fence_barrier_init();
@@ -233,8 +437,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     Item it;
     if (warp >= kSoftWarps) {
         regs_release<kRegsControl>();
-        if (warp == kLoadWarp) {
-            // ============================ producer ============================
+        if (L::gather && warp >= kLoadWarp) {
+            if constexpr (L::gather) gather_rows<E, D, SRC>(p, mq, smem, sbase, tid - kLoadWarp * 32);
+        } else if (warp == kLoadWarp) {
+            // ============================ producer (TMA) ============================
             if (lane == 0) {
                 tma_prefetch_map(&mq);
                 tma_prefetch_map(&mk);
@@ -407,6 +613,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int r = tid & 127;                            // row of the tile = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + t * kTileCols;
         int steps = 0, outs = 0;                            // barrier phases of this tile so far
+        const signed char* expo = reinterpret_cast<const signed char*>(smem + L::expo);
         bool ok = true;
         while (ok && walk.next(p, it)) {
             const int n = it.n[t];
@@ -416,22 +623,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             // keys this row sees (a row of no token: all, its result is dropped)
             const int lim = a.causal && valid ? max(0, min(it.kv_len, tok + it.kv_len - it.n_q + 1)) : it.kv_len;
             const int lim_min = __reduce_min_sync(0xffffffffu, lim);
-            const float rs = a.scale_log2;
+            float rs = a.scale_log2;
+            if constexpr (F8)
+                if (a.kv.scale_k) rs *= a.kv.scale_k[it.h];
             float m_used = -INFINITY, l = 0.f;
-            auto page_bad = [&](int st) -> bool {
-                const int key = (it.s0 + st) * kStep + lane * p.box;
-                if (st >= n || lane >= p.boxes || key >= it.kv_len) return false;
-                const int pg = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
-                return (unsigned)pg >= (unsigned)a.kv.num_pages;
+            // boxes (runs of p.box keys that no page border cuts) of step st
+            // whose page is out of range: bit i of this lane = box lane + 32 i
+            constexpr int kWords = L::gather ? 4 : 1;
+            auto page_bad = [&](int st) -> unsigned {
+                unsigned bits = 0;
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                    const int box = lane + 32 * i, key = (it.s0 + st) * kStep + box * p.box;
+                    if (st >= n || box >= p.boxes || key >= it.kv_len) continue;
+                    const int pg = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
+                    if ((unsigned)pg >= (unsigned)a.kv.num_pages) bits |= 1u << i;
+                }
+                return bits;
             };
-            bool bad = false;
+            unsigned bad = 0;
             if constexpr (PAGED) bad = page_bad(0);
             for (int st = 0; st < n; ++st) {
-                unsigned missing = 0;
+                unsigned bad_now = 0;
                 if constexpr (PAGED) {
-                    missing = __ballot_sync(0xffffffffu, bad);
+                    bad_now = bad;
                     bad = page_bad(st + 1);
                 }
+                const bool missing = PAGED && __any_sync(0xffffffffu, bad_now != 0);
                 ok = mbar_wait(bar(B_S + t), steps & 1, err, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
@@ -439,6 +657,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
                 ++steps;
                 tc_fence_after();
+                if constexpr (kScaledQ)
+                    if (st == 0) {
+                        // 2^expo[row] takes q's scaling out of the scores
+                        rs *= __uint_as_float((uint32_t)(127 + expo[t * kTileM + r]) << 23);
+                        mbar_arrive(bar(B_EXPO + t));
+                    }
                 uint32_t sv[128];
                 tmem_ld128_sync(lane_base, sv);
                 const int key0 = (it.s0 + st) * kStep;
@@ -448,9 +672,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     for (int j = 0; j < 128; ++j)
                         if (j >= rel) sv[j] = __float_as_uint(-INFINITY);
                     if (PAGED && missing) {
+                        // 128 bits, one a key: the words' bits spread over their boxes
+                        unsigned gone[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int i = 0; i < kWords; ++i) {
+                            const unsigned w = __ballot_sync(0xffffffffu, (bad_now >> i) & 1u);
+                            for (unsigned x = w; x; x &= x - 1) {
+                                const int key = (__ffs(x) - 1 + 32 * i) << p.box_shift;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int lo = max(key - 32 * q, 0), hi = min(key + p.box - 32 * q, 32);
+                                    if (lo < hi) gone[q] |= (hi - lo == 32 ? 0xffffffffu : ((1u << (hi - lo)) - 1u)) << lo;
+                                }
+                            }
+                        }
 #pragma unroll
                         for (int j = 0; j < 128; ++j)
-                            if ((missing >> (j >> p.box_shift)) & 1u) sv[j] = __float_as_uint(-INFINITY);
+                            if ((gone[j >> 5] >> (j & 31)) & 1u) sv[j] = __float_as_uint(-INFINITY);
                     }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -481,7 +719,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     const float p0 = fast_exp2(fmaf(__uint_as_float(sv[2 * k]), rs, -sub));
                     const float p1 = fast_exp2(fmaf(__uint_as_float(sv[2 * k + 1]), rs, -sub));
                     ls[k & 3] += p0 + p1;
-                    sv[k] = E::pack2(p0, p1);
+                    sv[k] = M::pack2(p0, p1);
                 }
                 l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 tmem_st32(lane_base, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
@@ -503,7 +741,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
             const bool none = l == 0.f;          // no visible key (a NaN sum is not that)
             const int64_t row = (int64_t)(it.q_row + tok) * a.Hq + head;
-            const float inv = it.whole ? (none ? 0.f : 1.f / l) : 1.f;
+            const float vs = F8 && a.kv.scale_v ? a.kv.scale_v[it.h] : 1.f;
+            const float inv = none ? 0.f : vs / l;
             float* part = p.ws_o + ((int64_t)it.split * a.tokens * a.Hq + row) * D;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -553,7 +792,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 template <class E, int D>
 __global__ void __launch_bounds__(256) attn_tc_merge(const TcParams p) {
     const SeqAttn& a = p.a;
-    constexpr float kPShift = std::is_same<E, BF16>::value ? 0.f : 7.f;
+    const float kPShift = std::is_same<E, BF16>::value && a.kv.f8 == 0 ? 0.f : 7.f;
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     grid_dependency_wait();
@@ -595,7 +834,8 @@ __global__ void __launch_bounds__(256) attn_tc_merge(const TcParams p) {
         for (int i = 0; i < W; ++i) acc[i] += f * src[i];
     }
     const bool none = l == 0.f;
-    const float inv = none ? 0.f : 1.f / l;
+    const float vs = a.kv.f8 && a.kv.scale_v ? a.kv.scale_v[(int)(row % a.Hq) / a.G] : 1.f;
+    const float inv = none ? 0.f : vs / l;
     typename E::T* out = static_cast<typename E::T*>(a.out) + row * D + lane * W;
 #pragma unroll
     for (int i = 0; i < W; i += 2)
@@ -632,18 +872,21 @@ bool pool_map(CUtensorMap* m, const void* base, bool bf16, const SeqKV& kv, bool
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class E, int D, bool PAGED>
+template <class E, int D, int SRC>
 cudaError_t launch_tc_t(const TcParams& p, int64_t items, int num_sms, cudaStream_t stream) {
-    using L = TcSmem<D>;
+    using L = TcSmem<D, SRC>;
     const SeqAttn& a = p.a;
     const bool bf16 = std::is_same<E, BF16>::value;
     CUtensorMap mq, mk, mv;
     if (!rows_map(&mq, a.q, bf16, D, a.Hq, a.tokens, a.q_stride, a.G, p.TR)) return cudaErrorInvalidValue;
-    if (PAGED ? (!pool_map(&mk, a.kv.k, bf16, a.kv, p.hnd, p.box) || !pool_map(&mv, a.kv.v, bf16, a.kv, p.hnd, p.box))
+    if (L::gather) {
+        mk = mv = mq;              // K and V are gathered without maps
+    } else if (SRC == SRC_PAGES ? (!pool_map(&mk, a.kv.k, bf16, a.kv, p.hnd, p.box) || !pool_map(&mv, a.kv.v, bf16, a.kv, p.hnd, p.box))
               : (!rows_map(&mk, a.kv.k, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.s_tok, 1, kStep) ||
-                 !rows_map(&mv, a.kv.v, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.sv_tok, 1, kStep)))
+                 !rows_map(&mv, a.kv.v, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.sv_tok, 1, kStep))) {
         return cudaErrorInvalidValue;
-    auto kern = attn_tc_kernel<E, D, PAGED>;
+    }
+    auto kern = attn_tc_kernel<E, D, SRC>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::alloc);
     if (err != cudaSuccess) return err;
     // the register split assumes a launch with kRegsLaunch registers a thread
@@ -686,9 +929,9 @@ int splits_for(int num_seqs, int tokens, int Hkv, int TR, int num_sms) {
 }  // namespace
 
 bool attn_tc_supported(const SeqKV& kv, int G) {
-    if (G > kTileM) return false;
-    if (!kv.page_table) return true;
-    return kv.f8 == 0 && kv.page_size % 16 == 0;
+    // (a gathered row is named by a 32-bit number)
+    return G <= kTileM &&
+           (!kv.page_table || (int64_t)kv.num_pages * kv.page_size * kv.Hkv < 0xffffffffLL);
 }
 
 size_t attn_tc_ws_bytes(int num_seqs, int tokens, int Hq, int Hkv, int D, int num_sms) {
@@ -713,16 +956,24 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
     p.ws_ml = p.ws_o + (int64_t)p.splits * a.tokens * a.Hq * a.kv.D;
     const int64_t items = items_bound(a.kv.num_seqs, a.tokens, a.kv.Hkv, p.TR) * p.splits;
     const bool bf16 = dtype == SFA_DTYPE_BF16;
-#define SFA_ATTN_TC(D_, PAGED_)                                                      \
-    return bf16 ? launch_tc_t<BF16, D_, PAGED_>(p, items, num_sms, stream)           \
-                : launch_tc_t<F16, D_, PAGED_>(p, items, num_sms, stream);
-    if (a.kv.D == 128) {
-        if (a.kv.page_table) { SFA_ATTN_TC(128, true) }
-        SFA_ATTN_TC(128, false)
-    }
-    if (a.kv.page_table) { SFA_ATTN_TC(64, true) }
-    SFA_ATTN_TC(64, false)
+    const int src = !a.kv.page_table ? SRC_PACKED
+                    : a.kv.f8        ? (a.kv.f8 == 1 ? SRC_E4M3 : SRC_E5M2)
+                                     : (a.kv.page_size % 16 == 0 ? SRC_PAGES : SRC_G16);
+#define SFA_ATTN_TC(D_, SRC_)                                                        \
+    if (a.kv.D == D_ && src == SRC_)                                                 \
+        return bf16 ? launch_tc_t<BF16, D_, SRC_>(p, items, num_sms, stream)         \
+                    : launch_tc_t<F16, D_, SRC_>(p, items, num_sms, stream);
+#define SFA_ATTN_TC_D(D_)                                                            \
+    SFA_ATTN_TC(D_, SRC_PACKED)                                                      \
+    SFA_ATTN_TC(D_, SRC_PAGES)                                                       \
+    SFA_ATTN_TC(D_, SRC_G16)                                                         \
+    SFA_ATTN_TC(D_, SRC_E4M3)                                                        \
+    SFA_ATTN_TC(D_, SRC_E5M2)
+    SFA_ATTN_TC_D(128)
+    SFA_ATTN_TC_D(64)
+#undef SFA_ATTN_TC_D
 #undef SFA_ATTN_TC
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace sfa
