@@ -6,12 +6,14 @@
 //
 // A work item is one kv head and 2 x TR query tokens of a sequence, TR =
 // 128 / G: two M-tiles of 128 rows (row r of a tile: token r / G, head r % G,
-// so a K / V tile serves all G heads), against all its visible keys in steps
-// of 128, or against one of `splits` equal shares of them (parts merged by
-// attn_tc_merge in order of their keys) when there are too few items for the
-// SMs.  CTAs are persistent (one per SM) and walk the items, longest first
-// within a sequence, in boustrophedon order, so that a CTA's long and short
-// ones even out.
+// so a K / V tile serves all G heads), against its visible keys in steps of
+// 128.  CTAs are persistent, one per SM.  All items lie on one line, each as
+// long as its visible keys plus a fixed charge for what an item costs besides,
+// and the line is cut into equal ranges, one per CTA, whatever the mix of
+// lengths: a cut inside an item falls on a step (never within kMinShare steps
+// of an item's end) and leaves the item in parts, fp32 in the workspace, at
+// most two of them from a CTA (the item it ends and the one it begins), which
+// attn_tc_merge joins in order of their keys.
 //
 // Warp roles, 384 threads:
 //   - softmax warpgroups 0, 1: tile t, thread = row = TMEM lane.  Read the
@@ -67,7 +69,11 @@ static_assert(kRegsSoftmax * kSoftWarps * 32 + kRegsControl * 128 <= kRegsLaunch
               "the register split fits what the block was launched with");
 constexpr int kTmemCols = 512, kTileCols = 256, kOCol = 128;
 constexpr float kRescale = 8.0f;            // log2 units
-constexpr int kMinSplitSteps = 4;           // steps below which a share is not cut further
+constexpr int kItemRows = 2 * kTileM;
+constexpr int kCharge = 256;                // an item's fixed cost, in keys
+constexpr int kMinShare = 3;                // fewest steps of a part
+constexpr int kMinRange = 6 * kStep;        // shortest range of a CTA, in keys
+constexpr int kMaxCtas = 160;               // ranges (the workspace's size goes by it)
 
 // Where K and V come from: packed rows, or pages by TMA; or gathered rows of
 // 16-bit, E4M3 or E5M2 pages.
@@ -86,7 +92,8 @@ struct TcSmem {
     static constexpr int rows = staging + (f8 ? 2 * kStep * D : 0);   // row numbers of two steps
     static constexpr int expo = rows + (gather ? 2 * kStep * 4 : 0);  // exponents of q's rows
     static constexpr int bars = expo + (f8 ? 2 * kTileM : 0);
-    static constexpr int abort = bars + 8 * 32;
+    static constexpr int items = bars + 8 * 34;            // the two items being worked on
+    static constexpr int abort = items + 2 * 48;
     static constexpr int tmem_slot = abort + 4;
     static constexpr int total = abort + 16;
     static constexpr int alloc = total + 1024;             // room to align the base to 1024
@@ -104,103 +111,218 @@ enum {
     B_EXPO = 10,        // + t: the softmax has read the exponents of tile t's rows
     B_FULL = 12,        // + slot
     B_FREE = 20,        // + slot
-    B_ROWS = 28         // row numbers of a step written
+    B_ROWS = 28,        // row numbers of a step written
+    B_ITEM = 29,        // + i: item slot i written
+    B_ITEM_FREE = 31    // + i: item slot i read by the MMA thread and the softmax warps
 };
 
 struct TcParams {
     SeqAttn a;
-    int TR, splits, hnd;
+    int TR, hnd;
     int box, box_shift, boxes;          // keys of a TMA box (and its log2), boxes of a step
-    float* ws_o;                        // [splits][tokens * Hq][D]
-    float* ws_ml;                       // [splits][tokens * Hq][2]
+    float* ws_o;                        // [2 * kMaxCtas][kItemRows][D] parts
+    float* ws_ml;                       // [2 * kMaxCtas][kItemRows][2] (m, sum)
 };
 
-// What an item is; the same in every thread of a warp.
+// A sequence on the line.  Tile j holds tokens [j U, (j + 1) U), U = 2 TR, and
+// sees max(0, min((j + 1) U, n_q) + off) keys, off = kv_len - n_q, when causal,
+// else kv_len.
+struct Seq {
+    int q_row, n_q, k_row, kv_len, tiles;
+};
+
+__device__ __forceinline__ Seq seq_of(const TcParams& p, int b) {
+    const int2 q = seq_rows(p.a.cu_q, b, p.a.tokens);
+    const int2 k = seq_keys(p.a.kv, b);
+    Seq s;
+    s.q_row = q.x;
+    s.n_q = q.y - q.x;
+    s.k_row = k.x;
+    s.kv_len = k.y;
+    s.tiles = (s.n_q + 2 * p.TR - 1) / (2 * p.TR);
+    return s;
+}
+
+// Keys visible to the last of the tokens before tok_end.
+__device__ __forceinline__ int visible(const TcParams& p, const Seq& s, int tok_end) {
+    if (!p.a.causal) return s.kv_len;
+    return max(0, min(tok_end, s.n_q) + s.kv_len - s.n_q);
+}
+
+__device__ __forceinline__ int cost(const TcParams& p, const Seq& s, int j) {
+    return visible(p, s, (j + 1) * 2 * p.TR) + kCharge;
+}
+
+// Cost of one kv head's tiles before tile j.
+__device__ __forceinline__ int64_t cost_before(const TcParams& p, const Seq& s, int j) {
+    int64_t sum = (int64_t)j * kCharge;
+    if (!p.a.causal) return sum + (int64_t)j * s.kv_len;
+    const int64_t U = 2 * p.TR, off = s.kv_len - s.n_q;
+    int64_t full = j;                                  // tiles of U tokens among them
+    if (j == s.tiles && j > 0) {
+        sum += s.kv_len;                               // the last one ends at n_q
+        --full;
+    }
+    const int64_t first = off < 0 ? min(full, -off / U) : 0;    // tiles that see no key
+    return sum + (full - first) * off + U * (full * (full + 1) - first * (first + 1)) / 2;
+}
+
+// Steps of an item of N steps before point x of its length c.
+__device__ __forceinline__ int cut(int64_t x, int c, int N) {
+    if (x <= 0) return 0;
+    if (x >= c) return N;
+    const int st = (int)(x * N / c);
+    return st < kMinShare ? 0 : (st > N - kMinShare ? N : st);
+}
+
+// The line: its length, the length of a range, and the sequence (and its first
+// point) that holds point (blockIdx.x + shift) * per.  Whole block; every
+// thread gets the answer.
+struct Line {
+    int64_t total, per, at, start;
+    int b;
+};
+
+template <int THREADS>
+__device__ __forceinline__ Line line_at(const TcParams& p, int ctas, int shift, int64_t* red) {
+    constexpr int W = THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = p.a.kv.num_seqs;
+    auto length = [&](int b) -> int64_t {
+        if (b >= B) return 0;
+        const Seq s = seq_of(p, b);
+        return cost_before(p, s, s.tiles) * p.a.kv.Hkv;
+    };
+    Line l;
+    int64_t mine = length(threadIdx.x);
+    int64_t sum = mine;
+    for (int b = threadIdx.x + THREADS; b < B; b += THREADS) sum += length(b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    l.total = 0;
+    for (int w = 0; w < W; ++w) l.total += red[w];
+    l.per = max((l.total + ctas - 1) / ctas, (int64_t)kMinRange);
+    l.at = ((int64_t)blockIdx.x + shift) * l.per;
+    l.b = B;
+    l.start = 0;
+    if (l.at >= l.total) return l;
+    int64_t base = 0;
+    for (int b0 = 0;; b0 += THREADS) {
+        __syncthreads();
+        int64_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) red[warp] = inc;
+        __syncthreads();
+        int64_t before = base, all = base;
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) before += red[w];
+            all += red[w];
+        }
+        const int64_t first = before + inc - mine;
+        __syncthreads();
+        if (first <= l.at && l.at < first + mine) {
+            red[0] = b0 + threadIdx.x;
+            red[1] = first;
+        }
+        __syncthreads();
+        if (l.at < all) {
+            l.b = (int)red[0];
+            l.start = red[1];
+            return l;
+        }
+        base = all;
+        mine = length(b0 + THREADS + threadIdx.x);
+    }
+}
+
+// Tile and kv head that hold point `rel` of a sequence (tile by tile, its
+// heads one after the other), and the point within the item.
+__device__ __forceinline__ void find_item(const TcParams& p, const Seq& s, int64_t rel, int& j, int& h, int64_t& x) {
+    const int H = p.a.kv.Hkv;
+    int lo = 0, hi = s.tiles - 1;                      // last tile that begins at or before rel
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cost_before(p, s, mid) * H <= rel) lo = mid;
+        else hi = mid - 1;
+    }
+    j = lo;
+    rel -= cost_before(p, s, lo) * H;
+    const int c = cost(p, s, lo);
+    h = (int)(rel / c);
+    x = rel - (int64_t)h * c;
+}
+
+// A share of an item.
 struct Item {
-    int b, h, split;
+    int b, h;                   // b < 0: the end of the range
     int q_row, n_q, tok0;       // packed row of the sequence's first token, its rows, the item's first token
     int k_row, kv_len;
     int s0, n[2];               // first step, steps of each tile
-    bool whole;                 // the first share holds all the keys
-    bool skip;                  // a share behind the last
+    int whole;                  // all of the item's keys
+    int pad;
 };
+static_assert(sizeof(Item) == 48, "TcSmem::items");
 
-// Keys visible to the last of tokens [0, tok_end) of a sequence.
-__device__ __forceinline__ int visible(const SeqAttn& a, int kv_len, int n_q, int tok_end) {
-    if (!a.causal) return kv_len;
-    return max(0, min(kv_len, tok_end + kv_len - n_q));
-}
-
-// Steps of share `split` of N: first, count, and whether the first share holds all.
-__device__ __forceinline__ void share(int N, int splits, int split, int& first, int& count, bool& whole) {
-    int per = max((N + splits - 1) / splits, kMinSplitSteps);
-    if (splits == 1) per = max(N, 1);
-    first = min(split * per, N);
-    count = min(N - first, per);
-    whole = N <= per;
-}
-
-// Walks the items of this CTA: item numbers run over (sequence, tile from the
-// last, kv head, split), the split fastest.  Every warp walks on its own.
+// Walks the shares of this CTA's range: the producer does, and hands each item
+// to the MMA thread and the softmax through two slots in shared memory.
 struct Walk {
-    int round = 0;
-    int b = 0;
-    int64_t base = 0;          // first item of sequence b
+    int64_t left;               // of the range
+    int64_t x;                  // point within the item (j, h)
+    int b, j, h;
+    Seq s;
+
+    __device__ __forceinline__ Walk(const TcParams& p, const Line& l) : left(0), x(0), b(l.b), j(0), h(0) {
+        if (b >= p.a.kv.num_seqs) return;
+        left = min(l.per, l.total - l.at);
+        s = seq_of(p, b);
+        find_item(p, s, l.at - l.start, j, h, x);
+    }
 
     __device__ __forceinline__ bool next(const TcParams& p, Item& it) {
-        const SeqAttn& a = p.a;
-        const int rnd = round++;
-        const int64_t i = (int64_t)rnd * gridDim.x +
-                          ((rnd & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        const int lane = threadIdx.x & 31;
-        const int per_tile = a.kv.Hkv * p.splits;
-        while (b < a.kv.num_seqs) {
-            // 32 sequences at a time
-            const int x = b + lane;
-            int64_t items = 0;
-            if (x < a.kv.num_seqs) {
-                const int2 r = seq_rows(a.cu_q, x, a.tokens);
-                items = (int64_t)((r.y - r.x + 2 * p.TR - 1) / (2 * p.TR)) * per_tile;
+        const int U = 2 * p.TR;
+        while (left > 0) {
+            if (j == s.tiles) {                        // on to the next sequence with rows
+                do {
+                    if (++b >= p.a.kv.num_seqs) return false;
+                    s = seq_of(p, b);
+                } while (s.tiles == 0);
+                j = h = 0;
             }
-            int64_t inc = items;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
+            const int c = cost(p, s, j);
+            const int64_t x0 = x, x1 = min((int64_t)c, x + left);
+            const int v1 = visible(p, s, (j + 1) * U), N = (v1 + kStep - 1) / kStep;
+            const int s0 = cut(x0, c, N), s1 = cut(x1, c, N);
+            it.b = b;
+            it.h = h;
+            it.q_row = s.q_row;
+            it.n_q = s.n_q;
+            it.tok0 = j * U;
+            it.k_row = s.k_row;
+            it.kv_len = s.kv_len;
+            it.s0 = s0;
+            it.whole = s0 == 0 && s1 == N;
+            const bool two = it.tok0 + p.TR < s.n_q;   // the second tile has rows
+            const int v0 = two ? visible(p, s, it.tok0 + p.TR) : v1;
+            it.n[0] = max(0, min((v0 + kStep - 1) / kStep, s1) - s0);
+            it.n[1] = two ? s1 - s0 : 0;
+            left -= x1 - x0;
+            x = x1;
+            if (x1 == c) {
+                x = 0;
+                if (++h == p.a.kv.Hkv) {
+                    h = 0;
+                    ++j;
+                }
             }
-            const unsigned above = __ballot_sync(0xffffffffu, base + inc > i);
-            if (!above) {
-                base += __shfl_sync(0xffffffffu, inc, 31);
-                b += 32;
-                continue;
-            }
-            const int w = __ffs(above) - 1;
-            base += __shfl_sync(0xffffffffu, inc - items, w);
-            b += w;
-            break;
+            // (an item without keys belongs to the range it begins in)
+            if (s1 > s0 || (N == 0 && x0 == 0)) return true;
         }
-        if (b >= a.kv.num_seqs) return false;
-        const int2 qr = seq_rows(a.cu_q, b, a.tokens);
-        const int2 kr = seq_keys(a.kv, b);
-        const int rel = (int)(i - base);
-        it.b = b;
-        it.split = rel % p.splits;
-        it.h = (rel / p.splits) % a.kv.Hkv;
-        it.q_row = qr.x;
-        it.n_q = qr.y - qr.x;
-        const int tiles = (it.n_q + 2 * p.TR - 1) / (2 * p.TR);
-        it.tok0 = (tiles - 1 - rel / per_tile) * 2 * p.TR;
-        it.k_row = kr.x;
-        it.kv_len = kr.y;
-        const int mid = it.tok0 + p.TR;
-        const int v0 = visible(a, it.kv_len, it.n_q, min(mid, it.n_q));
-        const int v1 = mid < it.n_q ? visible(a, it.kv_len, it.n_q, min(mid + p.TR, it.n_q)) : 0;
-        int count;
-        share((max(v0, v1) + kStep - 1) / kStep, p.splits, it.split, it.s0, count, it.whole);
-        it.skip = it.split > 0 && count == 0;
-        it.n[0] = max(0, min((v0 + kStep - 1) / kStep - it.s0, count));
-        it.n[1] = max(0, min((v1 + kStep - 1) / kStep - it.s0, count));
-        return true;
+        return false;
     }
 };
 
@@ -214,11 +336,34 @@ __device__ __forceinline__ uint32_t codes_h2(uint32_t x) {
     return h;
 }
 
+// Hands item number i (counting from 0) on; the end of the range as b < 0.  One thread.
+template <class L>
+__device__ __forceinline__ bool put_item(unsigned char* smem, uint32_t sbase, int i, const Item& it, int* err,
+                                         volatile int* abort_flag) {
+    const uint32_t bars = sbase + L::bars;
+    if (i >= 2 && !mbar_wait(bars + 8 * (B_ITEM_FREE + (i & 1)), ((i >> 1) - 1) & 1, err, abort_flag)) return false;
+    reinterpret_cast<Item*>(smem + L::items)[i & 1] = it;
+    mbar_arrive(bars + 8 * (B_ITEM + (i & 1)));
+    return true;
+}
+// Waits for item i; false if the wait gave up.
+template <class L>
+__device__ __forceinline__ bool get_item(unsigned char* smem, uint32_t sbase, int i, Item& it, int* err,
+                                         volatile int* abort_flag) {
+    if (!mbar_wait(sbase + L::bars + 8 * (B_ITEM + (i & 1)), (i >> 1) & 1, err, abort_flag)) return false;
+    const int4* src = reinterpret_cast<const int4*>(smem + L::items + (i & 1) * sizeof(Item));
+    int4* dst = reinterpret_cast<int4*>(&it);
+    dst[0] = src[0];
+    dst[1] = src[1];
+    dst[2] = src[2];
+    return true;
+}
+
 // The gathering producer: three warps, thread x of kGather.  Tile y of an item
 // (K of step y / 2, then its V) is copied while tile y - 1 is finished.
 template <class E, int D, int SRC>
 __device__ __forceinline__ void gather_rows(const TcParams& p, const CUtensorMap& mq, unsigned char* smem,
-                                            uint32_t sbase, int x) {
+                                            uint32_t sbase, int x, const Line& line) {
     using L = TcSmem<D, SRC>;
     constexpr bool F8 = L::f8, E5 = SRC == SRC_E5M2;
     constexpr bool kScaledQ = F8 && std::is_same<E, BF16>::value;
@@ -231,12 +376,19 @@ __device__ __forceinline__ void gather_rows(const TcParams& p, const CUtensorMap
     auto bar = [&](int i) { return sbase + L::bars + 8 * i; };
     uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::rows);
     const bool hnd = p.hnd != 0;
-    Walk walk;
+    Walk walk(p, line);
     Item it;
-    int items = 0, loads = 0, tables = 0;
+    int number = 0, items = 0, loads = 0, tables = 0;
     int read[2] = {0, 0};            // items whose tile t had keys
     bool ok = true;
-    while (ok && walk.next(p, it)) {
+    for (;;) {
+        const bool more = walk.next(p, it);
+        if (!more) it.b = -1;
+        if (x == 0) ok = put_item<L>(smem, sbase, number, it, err, abort_flag);
+        ++number;
+        if (!more) break;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         const int n = max(it.n[0], it.n[1]);
         if (n == 0) continue;
         // row numbers (in units of D elements) of step st's keys.  (The table
@@ -376,6 +528,7 @@ __device__ __forceinline__ void gather_rows(const TcParams& p, const CUtensorMap
             mbar_arrive(bar(B_FULL + loads % L::slots));
             ++loads;
         }
+        if (!ok) break;
     }
     cp_async_wait<0>();
     if (!ok && !kScaledQ && x == 0 && items > 0)
@@ -385,7 +538,8 @@ __device__ __forceinline__ void gather_rows(const TcParams& p, const CUtensorMap
 template <class E, int D, int SRC>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-               const __grid_constant__ CUtensorMap mv, const TcParams p) {
+               const __grid_constant__ CUtensorMap mv, const TcParams p, int ctas) {
+    __shared__ int64_t red[kThreads / 32];
     using L = TcSmem<D, SRC>;
     constexpr bool PAGED = SRC != SRC_PACKED, F8 = L::f8;
     constexpr bool kScaledQ = F8 && std::is_same<E, BF16>::value;    // q's rows go to fp16
@@ -410,6 +564,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         *abort_flag = 0;
         mbar_init(bar(B_Q), kScaledQ ? kGather : 1);
         mbar_init(bar(B_ROWS), kGather);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_ITEM + i), 1);
+            mbar_init(bar(B_ITEM_FREE + i), kSoftWarps + 1);
+        }
         mbar_init(bar(B_Q_FREE), 1);
         mbar_init(bar(B_TAIL), 1);
         mbar_init(bar(B_DRAIN), 1);
@@ -433,12 +591,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     grid_dependency_wait();
     grid_launch_dependents();
 
-    Walk walk;
-    Item it;
+    const Line line = line_at<kThreads>(p, ctas, 0, red);
     if (warp >= kSoftWarps) {
         regs_release<kRegsControl>();
         if (L::gather && warp >= kLoadWarp) {
-            if constexpr (L::gather) gather_rows<E, D, SRC>(p, mq, smem, sbase, tid - kLoadWarp * 32);
+            if constexpr (L::gather) gather_rows<E, D, SRC>(p, mq, smem, sbase, tid - kLoadWarp * 32, line);
         } else if (warp == kLoadWarp) {
             // ============================ producer (TMA) ============================
             if (lane == 0) {
@@ -446,9 +603,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 tma_prefetch_map(&mk);
                 tma_prefetch_map(&mv);
             }
+            Walk walk(p, line);
+            Item it;
+            int number = 0;
             int items = 0, loads = 0, tails = 0;   // items with keys, tiles loaded, tiles cleared
             bool ok = true;
-            while (ok && walk.next(p, it)) {
+            while (ok) {
+                const bool more = walk.next(p, it);
+                if (!more) it.b = -1;
+                if (lane == 0) ok = put_item<L>(smem, sbase, number, it, err, abort_flag);
+                ++number;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!more || !ok) break;
                 const int n = max(it.n[0], it.n[1]);
                 if (n == 0) continue;
                 if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
@@ -530,10 +696,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
         } else if (warp == kMmaWarp) {
             // ============================ MMA ============================
+            Item it;
             int items = 0, base = 0;        // items with keys; ring index of the item's first tile
             int done[2] = {0, 0};           // P tiles consumed
             bool ok = true;
-            while (ok && walk.next(p, it)) {
+            for (int number = 0; ok && lane == 0; ++number) {
+                ok = get_item<L>(smem, sbase, number, it, err, abort_flag);
+                if (!ok) break;
+                mbar_arrive(bar(B_ITEM_FREE + (number & 1)));
+                if (it.b < 0) break;
                 const int n = max(it.n[0], it.n[1]);
                 if (n == 0) continue;
                 auto full = [&](int x) {
@@ -558,7 +729,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                                       sdesc_sw128(vb + kk * 16 * 128, L::panel, 1024), kIdescPV,
                                       first && kk == 0 ? 0u : 1u);
                 };
-                if (lane == 0) {
+                {
                     ok = mbar_wait(bar(B_Q), items & 1, err, abort_flag) && full(base);
                     if (ok) {
                         tc_fence_after();
@@ -597,14 +768,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         if (i + 2 == n) tc_commit(bar(B_Q_FREE));
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
                 base += 2 * n;
                 ++items;
             }
-            if (!ok && lane == 0) {
+            if (!ok) {
                 tc_commit(bar(B_DRAIN));
                 mbar_wait(bar(B_DRAIN), 0, nullptr, nullptr, 100000000ull);
             }
+            __syncwarp();
         }
     } else {
         // ============================ softmax ============================
@@ -614,10 +785,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + t * kTileCols;
         int steps = 0, outs = 0;                            // barrier phases of this tile so far
         const signed char* expo = reinterpret_cast<const signed char*>(smem + L::expo);
+        Item it;
         bool ok = true;
-        while (ok && walk.next(p, it)) {
-            const int n = it.n[t];
-            if (it.skip) continue;
+        for (int number = 0; ok; ++number) {
+            ok = get_item<L>(smem, sbase, number, it, err, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_ITEM_FREE + (number & 1)));
+            if (it.b < 0) break;
+            const int n = t ? it.n[1] : it.n[0];
             const int tok = it.tok0 + t * p.TR + r / G, head = it.h * G + r % G;
             const bool valid = r < p.TR * G && tok < it.n_q;
             // keys this row sees (a row of no token: all, its result is dropped)
@@ -743,7 +920,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             const int64_t row = (int64_t)(it.q_row + tok) * a.Hq + head;
             const float vs = F8 && a.kv.scale_v ? a.kv.scale_v[it.h] : 1.f;
             const float inv = none ? 0.f : vs / l;
-            float* part = p.ws_o + ((int64_t)it.split * a.tokens * a.Hq + row) * D;
+            const int64_t slot = (int64_t)(2 * blockIdx.x + (it.s0 == 0 ? 1 : 0)) * kItemRows + t * kTileM + r;
+            float* part = p.ws_o + slot * D;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t ov[32];
@@ -773,8 +951,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             tc_fence_before();
             if (valid) {
                 if (!it.whole)
-                    *reinterpret_cast<float2*>(p.ws_ml + ((int64_t)it.split * a.tokens * a.Hq + row) * 2) =
-                        make_float2(m_used, l);
+                    *reinterpret_cast<float2*>(p.ws_ml + slot * 2) = make_float2(m_used, l);
                 else if (a.lse)
                     a.lse[row] = none ? -INFINITY : (m_used + __log2f(l) - kPShift) * kLn2;
             }
@@ -788,59 +965,84 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     }
 }
 
-// Joins the shares of every row whose keys were cut: one warp per row.
+// Block (x, y) joins rows 32 y .. of the parts of the item that border x
+// (between the ranges of CTAs x and x + 1) cuts first: a warp per row, four
+// rows each.
+constexpr int kMergeThreads = 256;
+
 template <class E, int D>
-__global__ void __launch_bounds__(256) attn_tc_merge(const TcParams p) {
+__global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p, int ctas) {
+    __shared__ int64_t red[kMergeThreads / 32];
     const SeqAttn& a = p.a;
     const float kPShift = std::is_same<E, BF16>::value && a.kv.f8 == 0 ? 0.f : 7.f;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
-    if (row >= (int64_t)a.tokens * a.Hq) return;
-    const int t = (int)(row / a.Hq);
-    // the sequence of token t: the number of list entries behind the first that are <= t
-    int b = 0;
-    for (int x0 = 0; x0 < a.kv.num_seqs; x0 += 32) {
-        const int x = x0 + lane;
-        const int c = __popc(__ballot_sync(0xffffffffu, x < a.kv.num_seqs && a.cu_q[1 + x] <= t));
-        b += c;
-        if (c < 32) break;
-    }
-    if (b >= a.kv.num_seqs) return;
-    const int2 qr = seq_rows(a.cu_q, b, a.tokens);
-    if (t < qr.x || t >= qr.y) return;
-    const int n_q = qr.y - qr.x, kv_len = seq_keys(a.kv, b).y;
-    const int tok0 = (t - qr.x) / (2 * p.TR) * (2 * p.TR);
-    const int N = (visible(a, kv_len, n_q, min(tok0 + 2 * p.TR, n_q)) + kStep - 1) / kStep;
-    int first, count;
-    bool whole;
-    share(N, p.splits, 0, first, count, whole);
-    if (whole) return;
-    const int per = count, parts = (N + per - 1) / per;
-    const int64_t rows = (int64_t)a.tokens * a.Hq;
+    const Line line = line_at<kMergeThreads>(p, ctas, 1, red);
+    if (line.b >= a.kv.num_seqs) return;
+    const Seq s = seq_of(p, line.b);
+    int j, h;
+    int64_t x;
+    find_item(p, s, line.at - line.start, j, h, x);
+    const int c = cost(p, s, j), N = (visible(p, s, (j + 1) * 2 * p.TR) + kStep - 1) / kStep;
+    const int first = cut(x, c, N);
+    // not cut here, or cut before
+    if (first == 0 || first == N || cut(x - line.per, c, N) > 0) return;
+    const int parts = 1 + (int)((c - x + line.per - 1) / line.per);
+    // part i is empty where two borders were moved to the same step
+    auto empty = [&](int i) { return i > 0 && cut(x + (i - 1) * line.per, c, N) == cut(x + i * line.per, c, N); };
+    auto slot_of = [&](int i) {
+        return (int64_t)(i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i)) * kItemRows;
+    };
     constexpr int W = D / 32;
-    float M = -INFINITY;
-    for (int s = 0; s < parts; ++s) M = fmaxf(M, p.ws_ml[(s * rows + row) * 2]);
-    float l = 0.f, acc[W];
+    for (int k = 0; k < 4; ++k) {
+        const int r = blockIdx.y * 32 + k * 8 + warp;             // row of the item
+        const int rr = r % kTileM, tok = j * 2 * p.TR + r / kTileM * p.TR + rr / a.G;
+        if (rr >= p.TR * a.G || tok >= s.n_q) continue;
+        float M = -INFINITY, l = 0.f, acc[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) acc[i] = 0.f;
+        for (int i = 0; i < W; ++i) acc[i] = 0.f;
+        // 32 parts at a time, their (m, sum) a lane each
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (i0 + lane < parts && !empty(i0 + lane))
+                ml = *reinterpret_cast<const float2*>(p.ws_ml + (slot_of(i0 + lane) + r) * 2);
+            const float m_new = fmaxf(M, warp_max(ml.x));
+            const float old = rescale_factor(M, m_new);
+            const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m_new);
+            M = m_new;
+            l = l * old + warp_sum(ml.y * f);
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] *= old;
+            const unsigned used = __ballot_sync(0xffffffffu, ml.x != -INFINITY || ml.y != 0.f);
+            const int n = min(32, parts - i0);
 #pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-        const float2 x = *reinterpret_cast<const float2*>(p.ws_ml + (s * rows + row) * 2);
-        const float f = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);
-        l += f * x.y;
-        const float* src = p.ws_o + (s * rows + row) * D + lane * W;
+            for (int i = 0; i < n; ++i) {
+                const float g = __shfl_sync(0xffffffffu, f, i);
+                if (!((used >> i) & 1u)) continue;
+                const float* src = p.ws_o + (slot_of(i0 + i) + r) * D + lane * W;
+                if constexpr (W == 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(src);
+                    acc[0] += g * v.x;
+                    acc[1] += g * v.y;
+                    acc[2] += g * v.z;
+                    acc[3] += g * v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2*>(src);
+                    acc[0] += g * v.x;
+                    acc[1] += g * v.y;
+                }
+            }
+        }
+        const bool none = l == 0.f;
+        const float vs = a.kv.f8 && a.kv.scale_v ? a.kv.scale_v[h] : 1.f;
+        const float inv = none ? 0.f : vs / l;
+        const int64_t row = (int64_t)(s.q_row + tok) * a.Hq + h * a.G + rr % a.G;
+        typename E::T* out = static_cast<typename E::T*>(a.out) + row * D + lane * W;
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] += f * src[i];
+        for (int i = 0; i < W; i += 2)
+            *reinterpret_cast<uint32_t*>(out + i) = none ? 0u : E::pack2(acc[i] * inv, acc[i + 1] * inv);
+        if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (M + __log2f(l) - kPShift) * kLn2;
     }
-    const bool none = l == 0.f;
-    const float vs = a.kv.f8 && a.kv.scale_v ? a.kv.scale_v[(int)(row % a.Hq) / a.G] : 1.f;
-    const float inv = none ? 0.f : vs / l;
-    typename E::T* out = static_cast<typename E::T*>(a.out) + row * D + lane * W;
-#pragma unroll
-    for (int i = 0; i < W; i += 2)
-        *reinterpret_cast<uint32_t*>(out + i) = none ? 0u : E::pack2(acc[i] * inv, acc[i + 1] * inv);
-    if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (M + __log2f(l) - kPShift) * kLn2;
 }
 
 // q, or packed k / v: [rows][heads][D] with rows `stride` elements apart; box
@@ -873,7 +1075,7 @@ bool pool_map(CUtensorMap* m, const void* base, bool bf16, const SeqKV& kv, bool
 }
 
 template <class E, int D, int SRC>
-cudaError_t launch_tc_t(const TcParams& p, int64_t items, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStream_t stream) {
     using L = TcSmem<D, SRC>;
     const SeqAttn& a = p.a;
     const bool bf16 = std::is_same<E, BF16>::value;
@@ -898,32 +1100,16 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t items, int num_sms, cudaStrea
         regs_ok = fa.numRegs == kRegsLaunch ? 1 : 0;
     }
     if (!regs_ok) return cudaErrorInvalidConfiguration;
-    const int grid = (int)(items < num_sms ? items : num_sms);
-    err = launch_pdl(kern, dim3(grid), dim3(kThreads), L::alloc, stream, mq, mk, mv, p);
+    const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+    err = launch_pdl(kern, dim3(ctas), dim3(kThreads), L::alloc, stream, mq, mk, mv, p, ctas);
     if (err != cudaSuccess) return err;
     count_launches(1);
-    if (p.splits > 1) {
-        const int64_t rows = (int64_t)a.tokens * a.Hq;
-        err = launch_pdl(attn_tc_merge<E, D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p);
+    // items of fewer than 2 kMinShare steps are never cut
+    if (longest >= 2 * kMinShare * kStep - kStep + 1) {
+        err = launch_pdl(attn_tc_merge<E, D>, dim3(ctas - 1, kItemRows / 32), dim3(kMergeThreads), 0, stream, p, ctas);
         if (err == cudaSuccess) count_launches(1);
     }
     return err;
-}
-
-// Items of the call at most: every sequence may end in a part tile.
-int64_t items_bound(int num_seqs, int tokens, int Hkv, int TR) {
-    const int64_t tiles = (int64_t)tokens / (2 * TR) + (num_seqs < tokens ? num_seqs : tokens);
-    return (tiles > 0 ? tiles : 1) * Hkv;
-}
-
-// Shares the keys of an item are cut into: enough for every SM to have one
-// when the items are fewer (counting one item per 2 TR rows, at least one a
-// sequence with rows).
-int splits_for(int num_seqs, int tokens, int Hkv, int TR, int num_sms) {
-    const int64_t tiles = (tokens + 2 * TR - 1) / (2 * TR);
-    const int64_t items = (tiles > num_seqs ? tiles : (num_seqs < tokens ? num_seqs : tokens)) * Hkv;
-    const int64_t s = items > 0 ? num_sms / items : 1;
-    return (int)(s < 1 ? 1 : s);
 }
 
 }  // namespace
@@ -934,18 +1120,12 @@ bool attn_tc_supported(const SeqKV& kv, int G) {
            (!kv.page_table || (int64_t)kv.num_pages * kv.page_size * kv.Hkv < 0xffffffffLL);
 }
 
-size_t attn_tc_ws_bytes(int num_seqs, int tokens, int Hq, int Hkv, int D, int num_sms) {
-    const int G = Hq / Hkv;
-    if (G > kTileM || tokens < 1) return 0;
-    const int s = splits_for(num_seqs, tokens, Hkv, kTileM / G, num_sms);
-    return s > 1 ? (size_t)s * tokens * Hq * (D + 2) * 4 : 0;
-}
+size_t attn_tc_ws_bytes(int G, int D) { return G <= kTileM ? (size_t)2 * kMaxCtas * kItemRows * (D + 2) * 4 : 0; }
 
 cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaStream_t stream) {
     TcParams p{};
     p.a = a;
     p.TR = kTileM / a.G;
-    p.splits = splits_for(a.kv.num_seqs, a.tokens, a.kv.Hkv, p.TR, num_sms);
     p.hnd = a.kv.s_tok == a.kv.D && a.kv.Hkv > 1 ? 1 : 0;
     p.box = kStep;
     if (a.kv.page_table)
@@ -953,16 +1133,17 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
     p.boxes = kStep / p.box;
     while ((1 << p.box_shift) < p.box) ++p.box_shift;
     p.ws_o = static_cast<float*>(a.ws);
-    p.ws_ml = p.ws_o + (int64_t)p.splits * a.tokens * a.Hq * a.kv.D;
-    const int64_t items = items_bound(a.kv.num_seqs, a.tokens, a.kv.Hkv, p.TR) * p.splits;
+    p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;
+    // no sequence has more keys than this
+    const int64_t longest = a.kv.page_table ? (int64_t)a.kv.max_pages * a.kv.page_size : a.kv.rows;
     const bool bf16 = dtype == SFA_DTYPE_BF16;
     const int src = !a.kv.page_table ? SRC_PACKED
                     : a.kv.f8        ? (a.kv.f8 == 1 ? SRC_E4M3 : SRC_E5M2)
                                      : (a.kv.page_size % 16 == 0 ? SRC_PAGES : SRC_G16);
 #define SFA_ATTN_TC(D_, SRC_)                                                        \
     if (a.kv.D == D_ && src == SRC_)                                                 \
-        return bf16 ? launch_tc_t<BF16, D_, SRC_>(p, items, num_sms, stream)         \
-                    : launch_tc_t<F16, D_, SRC_>(p, items, num_sms, stream);
+        return bf16 ? launch_tc_t<BF16, D_, SRC_>(p, longest, num_sms, stream)         \
+                    : launch_tc_t<F16, D_, SRC_>(p, longest, num_sms, stream);
 #define SFA_ATTN_TC_D(D_)                                                            \
     SFA_ATTN_TC(D_, SRC_PACKED)                                                      \
     SFA_ATTN_TC(D_, SRC_PAGES)                                                       \

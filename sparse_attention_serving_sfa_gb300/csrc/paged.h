@@ -54,7 +54,7 @@ cudaError_t launch_attn_rows(const SeqAttn& p, sfa_dtype dtype, int num_sms, cud
 // Tensor-core path (two tiles of 128 rows of one kv head per CTA): groups of
 // up to 128 heads; packed rows, or 16-bit pages of a multiple of 16 tokens.
 bool attn_tc_supported(const SeqKV& kv, int G);
-size_t attn_tc_ws_bytes(int num_seqs, int tokens, int Hq, int Hkv, int D, int num_sms);
+size_t attn_tc_ws_bytes(int G, int D);
 cudaError_t launch_attn_tc(const SeqAttn& p, sfa_dtype dtype, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_paged_append(const SeqKV& kv, const void* k_new, const void* v_new,

@@ -63,9 +63,8 @@ bool bad_stride(int64_t stride, int heads, int D) {
 constexpr int kFewRows = 16;
 
 // Workspace of either path.
-size_t attention_ws_bytes(int num_seqs, int tokens, int Hq, int Hkv, int D) {
-    const size_t r = attn_rows_ws_bytes(D);
-    const size_t t = attn_tc_ws_bytes(num_seqs, tokens, Hq, Hkv, D, num_sms());
+size_t attention_ws_bytes(int Hq, int Hkv, int D) {
+    const size_t r = attn_rows_ws_bytes(D), t = attn_tc_ws_bytes(Hq / Hkv, D);
     return r > t ? r : t;
 }
 
@@ -81,7 +80,7 @@ sfa_status run_attention(SeqAttn& p, int num_tokens, int num_qo_heads, int max_q
     if ((int64_t)num_tokens * num_qo_heads > 0x7fffffffLL / 2) return SFA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return SFA_OK;
     if (!q || !out || !al(q, 16) || !al(out, 16) || !al(lse, 4)) return SFA_ERR_INVALID_ARG;
-    const size_t need = attention_ws_bytes(p.kv.num_seqs, num_tokens, num_qo_heads, p.kv.Hkv, p.kv.D);
+    const size_t need = attention_ws_bytes(num_qo_heads, p.kv.Hkv, p.kv.D);
     if (!ws || ws_bytes < need) return SFA_ERR_WORKSPACE;
     if (!al(ws, 16)) return SFA_ERR_INVALID_ARG;
     p.q = q; p.out = out; p.lse = lse; p.cu_q = cu_q;
@@ -147,7 +146,7 @@ sfa_status varlen_workspace_size(int num_seqs, int num_tokens, int num_qo_heads,
     if (!bytes || num_seqs < 1 || num_tokens < 0) return SFA_ERR_INVALID_ARG;
     sfa_status st = check_heads(num_qo_heads, num_kv_heads, head_dim);
     if (st != SFA_OK) return st;
-    *bytes = attention_ws_bytes(num_seqs, num_tokens, num_qo_heads, num_kv_heads, head_dim);
+    *bytes = attention_ws_bytes(num_qo_heads, num_kv_heads, head_dim);
     return SFA_OK;
 }
 
