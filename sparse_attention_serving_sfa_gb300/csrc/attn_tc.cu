@@ -359,6 +359,35 @@ __device__ __forceinline__ bool get_item(unsigned char* smem, uint32_t sbase, in
     return true;
 }
 
+// MMA issue by a whole converged warp, one lane elected in the instruction:
+// with every operand the same in all lanes the descriptors stay in uniform
+// registers.  Issued from one lane's branch instead, 16 MMAs took twice as long
+// next to busy softmax warps.  Descriptors as low words (address in 16-byte units
+// and leading offset) over a constant high word.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p, q;\n.reg .b64 a, b;\nsetp.ne.b32 p, %5, 0;\nelect.sync _|q, 0xffffffff;\n"
+        "mov.b64 a, {%1, %3};\nmov.b64 b, {%2, %3};\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p, q;\n.reg .b64 b;\nsetp.ne.b32 p, %5, 0;\nelect.sync _|q, 0xffffffff;\n"
+        "mov.b64 b, {%2, %3};\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Arrive on `bar` when every MMA the elected lane issued so far has completed.
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+        : "memory");
+}
+
 // The gathering producer: three warps, thread x of kGather.  Tile y of an item
 // (K of step y / 2, then its V) is copied while tile y - 1 is finished.
 template <class E, int D, int SRC>
@@ -696,83 +725,87 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
         } else if (warp == kMmaWarp) {
             // ============================ MMA ============================
+            constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);    // stride 1024, version 1, 128-byte swizzle
+            const uint32_t k_lo = ((sbase + L::ring) >> 4) | (1u << 16);
+            const uint32_t v_lo = ((sbase + L::ring) >> 4) | ((uint32_t)(L::panel >> 4) << 16);
+            const uint32_t q_lo = ((sbase + L::q) >> 4) | (1u << 16);
             Item it;
-            int items = 0, base = 0;        // items with keys; ring index of the item's first tile
-            int done[2] = {0, 0};           // P tiles consumed
+            int items = 0, x = 0;           // items with keys; tiles of the ring used so far
+            int slot = 0;                   // x % slots
+            int done0 = 0, done1 = 0;       // P tiles consumed
             bool ok = true;
-            for (int number = 0; ok && lane == 0; ++number) {
-                ok = get_item<L>(smem, sbase, number, it, err, abort_flag);
-                if (!ok) break;
-                mbar_arrive(bar(B_ITEM_FREE + (number & 1)));
-                if (it.b < 0) break;
-                const int n = max(it.n[0], it.n[1]);
-                if (n == 0) continue;
-                auto full = [&](int x) {
-                    return mbar_wait(bar(B_FULL + x % L::slots), (x / L::slots) & 1, err, abort_flag);
-                };
-                auto qk = [&](int t, int x) {
-                    const uint32_t kb = sbase + L::ring + (x % L::slots) * L::tile;
-                    const uint32_t qb = sbase + L::q + t * L::tile;
+            auto full = [&](int sl, int tile) {
+                return __all_sync(0xffffffffu, mbar_wait(bar(B_FULL + sl), (tile / L::slots) & 1, err, abort_flag)) != 0;
+            };
+            auto after = [&](int sl) { return sl + 1 == L::slots ? 0 : sl + 1; };
+            auto qk = [&](int t, int sl) {
+                const uint32_t kb = k_lo + sl * (L::tile >> 4), qb = q_lo + t * (L::tile >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * L::panel + (kk & 3) * 32;
-                        tc_mma_f16(tmem + t * kTileCols, sdesc_sw128(qb + off, 16, 1024),
-                                   sdesc_sw128(kb + off, 16, 1024), kIdescQK, kk > 0 ? 1u : 0u);
-                    }
-                    tc_commit(bar(B_S + t));
-                };
-                auto pv = [&](int t, int x, bool first) {
-                    const uint32_t vb = sbase + L::ring + (x % L::slots) * L::tile;
-#pragma unroll
-                    for (int kk = 0; kk < kStep / 16; ++kk)
-                        tc_mma_f16_ts(tmem + t * kTileCols + kOCol, tmem + t * kTileCols + 8 * kk,
-                                      sdesc_sw128(vb + kk * 16 * 128, L::panel, 1024), kIdescPV,
-                                      first && kk == 0 ? 0u : 1u);
-                };
-                {
-                    ok = mbar_wait(bar(B_Q), items & 1, err, abort_flag) && full(base);
-                    if (ok) {
-                        tc_fence_after();
-                        for (int t = 0; t < 2; ++t)
-                            if (it.n[t] > 0) qk(t, base);
-                        tc_commit(bar(B_FREE + base % L::slots));
-                        if (n == 1) tc_commit(bar(B_Q_FREE));
-                    }
-                    for (int i = 0; i < n && ok; ++i) {
-                        const int vx = base + 2 * i + 1, kx = vx + 1;
-                        ok = full(vx);
-                        bool have_k = false;
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (!ok || i >= it.n[t]) continue;
-                            ok = mbar_wait(bar(B_P + t), done[t] & 1, err, abort_flag);
-                            if (!ok) continue;
-                            ++done[t];
-                            tc_fence_after();
-                            pv(t, vx, i == 0);
-                            if (i == it.n[t] - 1) {
-                                tc_commit(bar(B_O + t));
-                            } else {
-                                if (!have_k) {
-                                    ok = full(kx);
-                                    if (!ok) continue;
-                                    tc_fence_after();
-                                    have_k = true;
-                                }
-                                qk(t, kx);
-                            }
-                        }
-                        if (!ok) break;
-                        tc_commit(bar(B_FREE + vx % L::slots));
-                        if (i + 1 < n) tc_commit(bar(B_FREE + kx % L::slots));
-                        if (i + 2 == n) tc_commit(bar(B_Q_FREE));
-                    }
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * L::panel + (kk & 3) * 32) >> 4;
+                    mma_ss(tmem + t * kTileCols, qb + off, kb + off, kHi, kIdescQK, kk > 0 ? 1u : 0u);
                 }
-                base += 2 * n;
+                commit(bar(B_S + t));
+            };
+            auto pv = [&](int t, int sl, bool first) {
+                const uint32_t vb = v_lo + sl * (L::tile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kStep / 16; ++kk)
+                    mma_ts(tmem + t * kTileCols + kOCol, tmem + t * kTileCols + 8 * kk, vb + kk * (16 * 128 >> 4), kHi,
+                           kIdescPV, first && kk == 0 ? 0u : 1u);
+            };
+            for (int number = 0; ok; ++number) {
+                ok = __all_sync(0xffffffffu, get_item<L>(smem, sbase, number, it, err, abort_flag)) != 0;
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_ITEM_FREE + (number & 1)));
+                __syncwarp();
+                if (__shfl_sync(0xffffffffu, it.b, 0) < 0) break;
+                const int n0 = __shfl_sync(0xffffffffu, it.n[0], 0), n1 = __shfl_sync(0xffffffffu, it.n[1], 0);
+                const int n = max(n0, n1);
+                if (n == 0) continue;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_Q), items & 1, err, abort_flag)) && full(slot, x);
+                if (!ok) break;
                 ++items;
+                tc_fence_after();
+                if (n0 > 0) qk(0, slot);
+                if (n1 > 0) qk(1, slot);
+                for (int i = 0; i < n; ++i) {
+                    // V of step i, K of step i + 1
+                    const int vs = after(slot), ks = after(vs);
+                    ok = full(vs, x + 1);
+                    if (!ok) break;
+                    bool have_k = false;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int nt = t ? n1 : n0;
+                        if (i >= nt) continue;
+                        int& done = t ? done1 : done0;
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_P + t), done & 1, err, abort_flag)) != 0;
+                        if (!ok) break;
+                        ++done;
+                        tc_fence_after();
+                        pv(t, vs, i == 0);
+                        if (i == nt - 1) {
+                            commit(bar(B_O + t));
+                        } else {
+                            if (!have_k) {
+                                ok = full(ks, x + 2);
+                                if (!ok) break;
+                                tc_fence_after();
+                                have_k = true;
+                            }
+                            qk(t, ks);
+                        }
+                    }
+                    if (!ok) break;
+                    slot = ks;
+                    x += 2;
+                }
             }
             if (!ok) {
-                tc_commit(bar(B_DRAIN));
+                __syncwarp();
+                commit(bar(B_DRAIN));
                 mbar_wait(bar(B_DRAIN), 0, nullptr, nullptr, 100000000ull);
             }
             __syncwarp();
@@ -784,6 +817,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int r = tid & 127;                            // row of the tile = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + t * kTileCols;
         int steps = 0, outs = 0;                            // barrier phases of this tile so far
+        int base = 0;                                       // ring index of the item's first tile
         const signed char* expo = reinterpret_cast<const signed char*>(smem + L::expo);
         Item it;
         bool ok = true;
@@ -794,7 +828,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_ITEM_FREE + (number & 1)));
             if (it.b < 0) break;
-            const int n = t ? it.n[1] : it.n[0];
+            const int n = t ? it.n[1] : it.n[0], n_all = max(it.n[0], it.n[1]);
+            // The last tile issued sees every step; when its S of a step (or
+            // its O) is there, everything issued before is done too, and its
+            // thread 0 gives the tiles read by that back to the producer.
+            // (A commit on the MMA side for each of them cost ~500 cycles of
+            // the issuing thread.)
+            const bool frees = n == n_all && (t == 1 || it.n[1] == 0) && r == 0;
             const int tok = it.tok0 + t * p.TR + r / G, head = it.h * G + r % G;
             const bool valid = r < p.TR * G && tok < it.n_q;
             // keys this row sees (a row of no token: all, its result is dropped)
@@ -833,6 +873,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     break;
                 }
                 ++steps;
+                if (frees) {
+                    mbar_arrive(bar(B_FREE + (base + 2 * st) % L::slots));                    // K of this step
+                    if (st > 0) mbar_arrive(bar(B_FREE + (base + 2 * st - 1) % L::slots));    // V of the one before
+                    if (st == n - 1) mbar_arrive(bar(B_Q_FREE));
+                }
                 tc_fence_after();
                 if constexpr (kScaledQ)
                     if (st == 0) {
@@ -914,8 +959,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     break;
                 }
                 ++outs;
+                if (frees) mbar_arrive(bar(B_FREE + (base + 2 * n - 1) % L::slots));
                 tc_fence_after();
             }
+            base += 2 * n_all;
             const bool none = l == 0.f;          // no visible key (a NaN sum is not that)
             const int64_t row = (int64_t)(it.q_row + tok) * a.Hq + head;
             const float vs = F8 && a.kv.scale_v ? a.kv.scale_v[it.h] : 1.f;
