@@ -72,7 +72,7 @@ constexpr float kRescale = 8.0f;            // log2 units
 constexpr int kItemRows = 2 * kTileM;
 constexpr int kCharge = 256;                // an item's fixed cost, in keys
 constexpr int kMinShare = 3;                // fewest steps of a part
-constexpr int kMinRange = 6 * kStep;        // shortest range of a CTA, in keys
+constexpr int kMinRange = kStep;            // shortest range of a CTA, in keys
 constexpr int kMaxCtas = 160;               // ranges (the workspace's size goes by it)
 
 // Where K and V come from: packed rows, or pages by TMA; or gathered rows of
@@ -92,7 +92,7 @@ struct TcSmem {
     static constexpr int rows = staging + (f8 ? 2 * kStep * D : 0);   // row numbers of two steps
     static constexpr int expo = rows + (gather ? 2 * kStep * 4 : 0);  // exponents of q's rows
     static constexpr int bars = expo + (f8 ? 2 * kTileM : 0);
-    static constexpr int items = bars + 8 * 34;            // the two items being worked on
+    static constexpr int items = bars + 8 * 36;            // the two items being worked on
     static constexpr int abort = items + 2 * 48;
     static constexpr int tmem_slot = abort + 4;
     static constexpr int total = abort + 16;
@@ -104,23 +104,25 @@ enum {
     B_Q = 0,            // Q tiles of the item landed
     B_Q_FREE = 1,       // every Q.K^T of the item done
     B_S = 2,            // + t: S_t written (and the P.V before it done)
-    B_P = 4,            // + t: P_t written
-    B_O = 6,            // + t: O_t of the item complete
-    B_TAIL = 8,         // V tile landed whose tail is still to be cleared
-    B_DRAIN = 9,
-    B_EXPO = 10,        // + t: the softmax has read the exponents of tile t's rows
-    B_FULL = 12,        // + slot
-    B_FREE = 20,        // + slot
-    B_ROWS = 28,        // row numbers of a step written
-    B_ITEM = 29,        // + i: item slot i written
-    B_ITEM_FREE = 31    // + i: item slot i read by the MMA thread and the softmax warps
+    B_P = 4,            // + t: all of P_t written (one arrival a warp)
+    B_PH = 6,           // + t: P_t of keys 0..63 written
+    B_O = 8,            // + t: O_t of the item complete
+    B_TAIL = 10,        // V tile landed whose tail is still to be cleared
+    B_DRAIN = 11,
+    B_EXPO = 12,        // + t: the softmax has read the exponents of tile t's rows
+    B_FULL = 14,        // + slot
+    B_FREE = 22,        // + slot
+    B_ROWS = 30,        // row numbers of a step written
+    B_ITEM = 31,        // + i: item slot i written
+    B_ITEM_FREE = 33    // + i: item slot i read by the MMA warp and the softmax warps
 };
 
 struct TcParams {
     SeqAttn a;
     int TR, hnd;
+    int out32;                          // out is 32-byte aligned
     int box, box_shift, boxes;          // keys of a TMA box (and its log2), boxes of a step
-    float* ws_o;                        // [2 * kMaxCtas][kItemRows][D] parts
+    float* ws_o;                        // [2 * kMaxCtas][D / 4][kItemRows][4] parts
     float* ws_ml;                       // [2 * kMaxCtas][kItemRows][2] (m, sum)
 };
 
@@ -175,85 +177,70 @@ __device__ __forceinline__ int cut(int64_t x, int c, int N) {
     return st < kMinShare ? 0 : (st > N - kMinShare ? N : st);
 }
 
-// The line: its length, the length of a range, and the sequence (and its first
-// point) that holds point (blockIdx.x + shift) * per.  Whole block; every
-// thread gets the answer.
+// The line: its length, the length of a range, the point range (blockIdx.x +
+// shift) begins at, and the sequence (and its first point) that holds it.  One
+// warp; every lane gets the answer.
 struct Line {
     int64_t total, per, at, start;
     int b;
 };
 
-template <int THREADS>
-__device__ __forceinline__ Line line_at(const TcParams& p, int ctas, int shift, int64_t* red) {
-    constexpr int W = THREADS / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = p.a.kv.num_seqs;
+__device__ __forceinline__ Line line_at(const TcParams& p, int ctas, int shift) {
+    const int lane = threadIdx.x & 31, B = p.a.kv.num_seqs;
     auto length = [&](int b) -> int64_t {
         if (b >= B) return 0;
         const Seq s = seq_of(p, b);
         return cost_before(p, s, s.tiles) * p.a.kv.Hkv;
     };
     Line l;
-    int64_t mine = length(threadIdx.x);
-    int64_t sum = mine;
-    for (int b = threadIdx.x + THREADS; b < B; b += THREADS) sum += length(b);
+    const int64_t first = length(lane);
+    int64_t sum = first;
+    for (int b = lane + 32; b < B; b += 32) sum += length(b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) red[warp] = sum;
-    __syncthreads();
-    l.total = 0;
-    for (int w = 0; w < W; ++w) l.total += red[w];
+    l.total = sum;
     l.per = max((l.total + ctas - 1) / ctas, (int64_t)kMinRange);
     l.at = ((int64_t)blockIdx.x + shift) * l.per;
     l.b = B;
     l.start = 0;
     if (l.at >= l.total) return l;
-    int64_t base = 0;
-    for (int b0 = 0;; b0 += THREADS) {
-        __syncthreads();
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int64_t mine = b0 == 0 ? first : length(b0 + lane);
         int64_t inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
-        if (lane == 31) red[warp] = inc;
-        __syncthreads();
-        int64_t before = base, all = base;
-        for (int w = 0; w < W; ++w) {
-            if (w < warp) before += red[w];
-            all += red[w];
-        }
-        const int64_t first = before + inc - mine;
-        __syncthreads();
-        if (first <= l.at && l.at < first + mine) {
-            red[0] = b0 + threadIdx.x;
-            red[1] = first;
-        }
-        __syncthreads();
-        if (l.at < all) {
-            l.b = (int)red[0];
-            l.start = red[1];
+        const unsigned above = __ballot_sync(0xffffffffu, l.start + inc > l.at);
+        if (above) {
+            const int w = __ffs(above) - 1;
+            l.start += __shfl_sync(0xffffffffu, inc - mine, w);
+            l.b = b0 + w;
             return l;
         }
-        base = all;
-        mine = length(b0 + THREADS + threadIdx.x);
+        l.start += __shfl_sync(0xffffffffu, inc, 31);
     }
+    return l;
 }
 
 // Tile and kv head that hold point `rel` of a sequence (tile by tile, its
-// heads one after the other), and the point within the item.
+// heads one after the other), and the point within the item.  One warp.
 __device__ __forceinline__ void find_item(const TcParams& p, const Seq& s, int64_t rel, int& j, int& h, int64_t& x) {
-    const int H = p.a.kv.Hkv;
-    int lo = 0, hi = s.tiles - 1;                      // last tile that begins at or before rel
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cost_before(p, s, mid) * H <= rel) lo = mid;
-        else hi = mid - 1;
+    const int lane = threadIdx.x & 31, H = p.a.kv.Hkv;
+    // the last of tiles j .. j + n that begins at or before rel, 32 tried at a time
+    j = 0;
+    for (int n = s.tiles - 1; n > 0;) {
+        const int step = (n + 31) / 32, i = j + (lane + 1) * step;
+        const bool below = (lane + 1) * step <= n && cost_before(p, s, i) * H <= rel;
+        const int c = __popc(__ballot_sync(0xffffffffu, below));
+        j += c * step;
+        n = min(step - 1, n - c * step);
     }
-    j = lo;
-    rel -= cost_before(p, s, lo) * H;
-    const int c = cost(p, s, lo);
-    h = (int)(rel / c);
+    rel -= cost_before(p, s, j) * H;
+    const int c = cost(p, s, j);
+    h = 0;
+    if (rel >= c) h = rel < 0x7fffffff ? (int)((uint32_t)rel / (uint32_t)c) : (int)(rel / c);
     x = rel - (int64_t)h * c;
 }
 
@@ -359,6 +346,31 @@ __device__ __forceinline__ bool get_item(unsigned char* smem, uint32_t sbase, in
     return true;
 }
 
+// Two fp32 in a register pair: packed arithmetic, each half rounded as alone.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float high(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// 32 bytes at once (a full sector a thread).
+__device__ __forceinline__ void st_32(void* to, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // MMA issue by a whole converged warp, one lane elected in the instruction:
 // with every operand the same in all lanes the descriptors stay in uniform
 // registers.  Issued from one lane's branch instead, 16 MMAs took twice as long
@@ -392,7 +404,7 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 // (K of step y / 2, then its V) is copied while tile y - 1 is finished.
 template <class E, int D, int SRC>
 __device__ __forceinline__ void gather_rows(const TcParams& p, const CUtensorMap& mq, unsigned char* smem,
-                                            uint32_t sbase, int x, const Line& line) {
+                                            uint32_t sbase, int x, int ctas) {
     using L = TcSmem<D, SRC>;
     constexpr bool F8 = L::f8, E5 = SRC == SRC_E5M2;
     constexpr bool kScaledQ = F8 && std::is_same<E, BF16>::value;
@@ -405,7 +417,7 @@ __device__ __forceinline__ void gather_rows(const TcParams& p, const CUtensorMap
     auto bar = [&](int i) { return sbase + L::bars + 8 * i; };
     uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::rows);
     const bool hnd = p.hnd != 0;
-    Walk walk(p, line);
+    Walk walk(p, line_at(p, ctas, 0));
     Item it;
     int number = 0, items = 0, loads = 0, tables = 0;
     int read[2] = {0, 0};            // items whose tile t had keys
@@ -568,7 +580,6 @@ template <class E, int D, int SRC>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const TcParams p, int ctas) {
-    __shared__ int64_t red[kThreads / 32];
     using L = TcSmem<D, SRC>;
     constexpr bool PAGED = SRC != SRC_PACKED, F8 = L::f8;
     constexpr bool kScaledQ = F8 && std::is_same<E, BF16>::value;    // q's rows go to fp16
@@ -602,7 +613,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         mbar_init(bar(B_DRAIN), 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(B_S + t), 1);
-            mbar_init(bar(B_P + t), 128);
+            mbar_init(bar(B_P + t), 4);
+            mbar_init(bar(B_PH + t), 4);
             mbar_init(bar(B_O + t), 1);
             mbar_init(bar(B_EXPO + t), kTileM);
         }
@@ -620,11 +632,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     grid_dependency_wait();
     grid_launch_dependents();
 
-    const Line line = line_at<kThreads>(p, ctas, 0, red);
     if (warp >= kSoftWarps) {
         regs_release<kRegsControl>();
         if (L::gather && warp >= kLoadWarp) {
-            if constexpr (L::gather) gather_rows<E, D, SRC>(p, mq, smem, sbase, tid - kLoadWarp * 32, line);
+            if constexpr (L::gather) gather_rows<E, D, SRC>(p, mq, smem, sbase, tid - kLoadWarp * 32, ctas);
         } else if (warp == kLoadWarp) {
             // ============================ producer (TMA) ============================
             if (lane == 0) {
@@ -632,7 +643,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 tma_prefetch_map(&mk);
                 tma_prefetch_map(&mv);
             }
-            Walk walk(p, line);
+            Walk walk(p, line_at(p, ctas, 0));
             Item it;
             int number = 0;
             int items = 0, loads = 0, tails = 0;   // items with keys, tiles loaded, tiles cleared
@@ -747,10 +758,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
                 commit(bar(B_S + t));
             };
-            auto pv = [&](int t, int sl, bool first) {
+            // keys 64 half .. + 63
+            auto pv = [&](int t, int sl, int half, bool first) {
                 const uint32_t vb = v_lo + sl * (L::tile >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kStep / 16; ++kk)
+                for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
                     mma_ts(tmem + t * kTileCols + kOCol, tmem + t * kTileCols + 8 * kk, vb + kk * (16 * 128 >> 4), kHi,
                            kIdescPV, first && kk == 0 ? 0u : 1u);
             };
@@ -781,11 +793,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         const int nt = t ? n1 : n0;
                         if (i >= nt) continue;
                         int& done = t ? done1 : done0;
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PH + t), done & 1, err, abort_flag)) != 0;
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(t, vs, 0, i == 0);
                         ok = __all_sync(0xffffffffu, mbar_wait(bar(B_P + t), done & 1, err, abort_flag)) != 0;
                         if (!ok) break;
                         ++done;
                         tc_fence_after();
-                        pv(t, vs, i == 0);
+                        pv(t, vs, 1, false);
                         if (i == nt - 1) {
                             commit(bar(B_O + t));
                         } else {
@@ -915,7 +931,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int j = 0; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sv[j]));
+                for (int j = 0; j < 128; j += 2)
+                    mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], __uint_as_float(sv[j])), __uint_as_float(sv[j + 1]));
                 // the scale is positive and rounding monotonic: max of scaled = scaled max
                 const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rs);
                 const bool need = m_new > m_used + kRescale;
@@ -935,20 +952,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 if (need) m_used = m_new;
                 // (a row that has seen no key has only -inf scores: subtracting 0 gives P = 0)
                 const float sub = m_used == -INFINITY ? 0.f : m_used - kPShift;
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < 64; ++k) {
-                    const float p0 = fast_exp2(fmaf(__uint_as_float(sv[2 * k]), rs, -sub));
-                    const float p1 = fast_exp2(fmaf(__uint_as_float(sv[2 * k + 1]), rs, -sub));
-                    ls[k & 3] += p0 + p1;
+                const uint64_t rs2 = pair(rs, rs), sub2 = pair(-sub, -sub);
+                uint64_t ls[2] = {0, 0};
+                auto weights = [&](int k) {              // keys 2 k, 2 k + 1
+                    const uint64_t u = fma2(pair(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), rs2, sub2);
+                    const float p0 = fast_exp2(low(u)), p1 = fast_exp2(high(u));
+                    ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
                     sv[k] = M::pack2(p0, p1);
-                }
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                };
+#pragma unroll
+                for (int k = 0; k < 32; ++k) weights(k);
                 tmem_st32(lane_base, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                tmem_st32(lane_base + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                // (the first half's store completes under the next weights)
+#pragma unroll
+                for (int k = 32; k < 44; ++k) weights(k);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(B_P + t));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_PH + t));
+#pragma unroll
+                for (int k = 44; k < 64; ++k) weights(k);
+                tmem_st32(lane_base + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                const uint64_t l2 = add2(ls[0], ls[1]);
+                l += low(l2) + high(l2);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_P + t));
             }
             if (!ok) break;
             // ---- epilogue ----
@@ -967,8 +997,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             const int64_t row = (int64_t)(it.q_row + tok) * a.Hq + head;
             const float vs = F8 && a.kv.scale_v ? a.kv.scale_v[it.h] : 1.f;
             const float inv = none ? 0.f : vs / l;
-            const int64_t slot = (int64_t)(2 * blockIdx.x + (it.s0 == 0 ? 1 : 0)) * kItemRows + t * kTileM + r;
-            float* part = p.ws_o + slot * D;
+            // parts: [D / 4][row][4], so that the lanes (rows) write side by side
+            const int64_t slot = 2 * blockIdx.x + (it.s0 == 0 ? 1 : 0);
+            float* part = p.ws_o + slot * kItemRows * D + (t * kTileM + r) * 4;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t ov[32];
@@ -980,25 +1011,31 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
                 if (!valid) continue;
                 if (it.whole) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<typename E::T*>(a.out) + row * D + 32 * c);
+                    typename E::T* dst = static_cast<typename E::T*>(a.out) + row * D + 32 * c;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        auto two = [&](int x) {
-                            return none ? 0u : E::pack2(__uint_as_float(ov[x]) * inv, __uint_as_float(ov[x + 1]) * inv);
-                        };
-                        dst[j / 8] = make_uint4(two(j), two(j + 2), two(j + 4), two(j + 6));
+                    for (int j = 0; j < 32; j += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            w[i] = none ? 0u : E::pack2(__uint_as_float(ov[j + 2 * i]) * inv, __uint_as_float(ov[j + 2 * i + 1]) * inv);
+                        if (p.out32) {
+                            st_32(dst + j, w);
+                        } else {
+                            reinterpret_cast<uint4*>(dst + j)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(dst + j)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(part + 32 * c);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) dst[j / 4] = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<uint4*>(part + (32 * c + j) * kItemRows) = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
                 }
             }
             // O has been read: the MMAs of the next item may overwrite it (they wait for its P)
             tc_fence_before();
             if (valid) {
                 if (!it.whole)
-                    *reinterpret_cast<float2*>(p.ws_ml + slot * 2) = make_float2(m_used, l);
+                    *reinterpret_cast<float2*>(p.ws_ml + (slot * kItemRows + t * kTileM + r) * 2) = make_float2(m_used, l);
                 else if (a.lse)
                     a.lse[row] = none ? -INFINITY : (m_used + __log2f(l) - kPShift) * kLn2;
             }
@@ -1012,19 +1049,22 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     }
 }
 
-// Block (x, y) joins rows 32 y .. of the parts of the item that border x
-// (between the ranges of CTAs x and x + 1) cuts first: a warp per row, four
-// rows each.
+// Block (x, y) joins rows 32 y .. 32 y + 31 of the parts of the item that
+// border x (between the ranges of CTAs x and x + 1) cuts first: lane = row,
+// each warp some of the dims; the result crosses over in shared memory to be
+// written row by row.
 constexpr int kMergeThreads = 256;
 
 template <class E, int D>
 __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p, int ctas) {
-    __shared__ int64_t red[kMergeThreads / 32];
+    constexpr int kWarps = kMergeThreads / 32;
+    constexpr int Q = D / 4 / kWarps;                    // 4-dim groups of a warp
+    __shared__ uint2 turn[32][D / 4 + 1];
     const SeqAttn& a = p.a;
     const float kPShift = std::is_same<E, BF16>::value && a.kv.f8 == 0 ? 0.f : 7.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
-    const Line line = line_at<kMergeThreads>(p, ctas, 1, red);
+    const Line line = line_at(p, ctas, 1);
     if (line.b >= a.kv.num_seqs) return;
     const Seq s = seq_of(p, line.b);
     int j, h;
@@ -1035,60 +1075,56 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p,
     // not cut here, or cut before
     if (first == 0 || first == N || cut(x - line.per, c, N) > 0) return;
     const int parts = 1 + (int)((c - x + line.per - 1) / line.per);
-    // part i is empty where two borders were moved to the same step
-    auto empty = [&](int i) { return i > 0 && cut(x + (i - 1) * line.per, c, N) == cut(x + i * line.per, c, N); };
-    auto slot_of = [&](int i) {
-        return (int64_t)(i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i)) * kItemRows;
-    };
-    constexpr int W = D / 32;
-    for (int k = 0; k < 4; ++k) {
-        const int r = blockIdx.y * 32 + k * 8 + warp;             // row of the item
-        const int rr = r % kTileM, tok = j * 2 * p.TR + r / kTileM * p.TR + rr / a.G;
-        if (rr >= p.TR * a.G || tok >= s.n_q) continue;
-        float M = -INFINITY, l = 0.f, acc[W];
+    const int r = blockIdx.y * 32 + lane, rr = r % kTileM, tok = j * 2 * p.TR + r / kTileM * p.TR + rr / a.G;
+    const bool valid = rr < p.TR * a.G && tok < s.n_q;
+    if (!__any_sync(0xffffffffu, valid)) return;         // (the same in every warp)
+    float M = -INFINITY, l = 0.f;
+    float4 acc[Q];
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] = 0.f;
-        // 32 parts at a time, their (m, sum) a lane each
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (i0 + lane < parts && !empty(i0 + lane))
-                ml = *reinterpret_cast<const float2*>(p.ws_ml + (slot_of(i0 + lane) + r) * 2);
-            const float m_new = fmaxf(M, warp_max(ml.x));
-            const float old = rescale_factor(M, m_new);
-            const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m_new);
-            M = m_new;
-            l = l * old + warp_sum(ml.y * f);
+    for (int q = 0; q < Q; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    int last = 0;                                        // steps before part i
+    for (int i = 0; i < parts; ++i) {
+        const int end = cut(x + i * line.per, c, N);
+        const bool empty = end == last;                  // two borders moved to the same step
+        last = end;
+        if (empty) continue;
+        const int64_t slot = i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (valid) ml = *reinterpret_cast<const float2*>(p.ws_ml + (slot * kItemRows + r) * 2);
+        float4 v[Q];
 #pragma unroll
-            for (int i = 0; i < W; ++i) acc[i] *= old;
-            const unsigned used = __ballot_sync(0xffffffffu, ml.x != -INFINITY || ml.y != 0.f);
-            const int n = min(32, parts - i0);
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const float g = __shfl_sync(0xffffffffu, f, i);
-                if (!((used >> i) & 1u)) continue;
-                const float* src = p.ws_o + (slot_of(i0 + i) + r) * D + lane * W;
-                if constexpr (W == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(src);
-                    acc[0] += g * v.x;
-                    acc[1] += g * v.y;
-                    acc[2] += g * v.z;
-                    acc[3] += g * v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(src);
-                    acc[0] += g * v.x;
-                    acc[1] += g * v.y;
-                }
-            }
+        for (int q = 0; q < Q; ++q)
+            v[q] = valid ? *reinterpret_cast<const float4*>(p.ws_o + slot * kItemRows * D + ((q * kWarps + warp) * kItemRows + r) * 4)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        // (a part without a visible key: m = -inf, everything else 0)
+        const float m_new = fmaxf(M, ml.x);
+        const float old = rescale_factor(M, m_new), f = rescale_factor(ml.x, m_new);
+        M = m_new;
+        l = l * old + ml.y * f;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            acc[q].x = acc[q].x * old + v[q].x * f;
+            acc[q].y = acc[q].y * old + v[q].y * f;
+            acc[q].z = acc[q].z * old + v[q].z * f;
+            acc[q].w = acc[q].w * old + v[q].w * f;
         }
-        const bool none = l == 0.f;
-        const float vs = a.kv.f8 && a.kv.scale_v ? a.kv.scale_v[h] : 1.f;
-        const float inv = none ? 0.f : vs / l;
-        const int64_t row = (int64_t)(s.q_row + tok) * a.Hq + h * a.G + rr % a.G;
-        typename E::T* out = static_cast<typename E::T*>(a.out) + row * D + lane * W;
+    }
+    const bool none = l == 0.f;
+    const float vs = a.kv.f8 && a.kv.scale_v ? a.kv.scale_v[h] : 1.f;
+    const float inv = none ? 0.f : vs / l;
+    const int64_t row = (int64_t)(s.q_row + tok) * a.Hq + h * a.G + rr % a.G;
 #pragma unroll
-        for (int i = 0; i < W; i += 2)
-            *reinterpret_cast<uint32_t*>(out + i) = none ? 0u : E::pack2(acc[i] * inv, acc[i + 1] * inv);
-        if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (M + __log2f(l) - kPShift) * kLn2;
+    for (int q = 0; q < Q; ++q)
+        turn[lane][q * kWarps + warp] = none ? make_uint2(0u, 0u)
+                                             : make_uint2(E::pack2(acc[q].x * inv, acc[q].y * inv),
+                                                          E::pack2(acc[q].z * inv, acc[q].w * inv));
+    if (warp == 0 && valid && a.lse) a.lse[row] = none ? -INFINITY : (M + __log2f(l) - kPShift) * kLn2;
+    __syncthreads();
+    // D / 4 threads a row
+    for (int i = warp; i < 32; i += kWarps) {
+        const int64_t to = __shfl_sync(0xffffffffu, row, i);
+        if (!__shfl_sync(0xffffffffu, (int)valid, i)) continue;
+        if (lane < D / 4) *reinterpret_cast<uint2*>(static_cast<typename E::T*>(a.out) + to * D + lane * 4) = turn[i][lane];
     }
 }
 
@@ -1179,6 +1215,7 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
         while (a.kv.page_size % p.box != 0) p.box /= 2;
     p.boxes = kStep / p.box;
     while ((1 << p.box_shift) < p.box) ++p.box_shift;
+    p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.ws_o = static_cast<float*>(a.ws);
     p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;
     // no sequence has more keys than this
