@@ -120,6 +120,9 @@ enum {
 struct TcParams {
     SeqAttn a;
     int TR, hnd;
+    uint32_t unit_mul;                  // x / (2 TR) = x * unit_mul >> unit_shift for 0 <= x < 2^31
+    int unit_shift;
+    uint64_t ctas_mul;                  // x / ctas = high word of x * ctas_mul for x < 2^56
     int out32;                          // out is 32-byte aligned
     int box, box_shift, boxes;          // keys of a TMA box (and its log2), boxes of a step
     float* ws_o;                        // [2 * kMaxCtas][D / 4][kItemRows][4] parts
@@ -133,6 +136,11 @@ struct Seq {
     int q_row, n_q, k_row, kv_len, tiles;
 };
 
+// x / (2 TR)
+__device__ __forceinline__ int units(const TcParams& p, int x) {
+    return (int)(((uint64_t)(uint32_t)x * p.unit_mul) >> p.unit_shift);
+}
+
 __device__ __forceinline__ Seq seq_of(const TcParams& p, int b) {
     const int2 q = seq_rows(p.a.cu_q, b, p.a.tokens);
     const int2 k = seq_keys(p.a.kv, b);
@@ -141,7 +149,7 @@ __device__ __forceinline__ Seq seq_of(const TcParams& p, int b) {
     s.n_q = q.y - q.x;
     s.k_row = k.x;
     s.kv_len = k.y;
-    s.tiles = (s.n_q + 2 * p.TR - 1) / (2 * p.TR);
+    s.tiles = units(p, s.n_q + 2 * p.TR - 1);
     return s;
 }
 
@@ -165,7 +173,7 @@ __device__ __forceinline__ int64_t cost_before(const TcParams& p, const Seq& s, 
         sum += s.kv_len;                               // the last one ends at n_q
         --full;
     }
-    const int64_t first = off < 0 ? min(full, -off / U) : 0;    // tiles that see no key
+    const int64_t first = off < 0 ? min(full, (int64_t)units(p, (int)-off)) : 0;    // tiles that see no key
     return sum + (full - first) * off + U * (full * (full + 1) - first * (first + 1)) / 2;
 }
 
@@ -173,7 +181,8 @@ __device__ __forceinline__ int64_t cost_before(const TcParams& p, const Seq& s, 
 __device__ __forceinline__ int cut(int64_t x, int c, int N) {
     if (x <= 0) return 0;
     if (x >= c) return N;
-    const int st = (int)(x * N / c);
+    // (fp32: monotonic in x, and the same wherever a border is looked at)
+    const int st = (int)__fdividef(__ll2float_rn(x) * (float)N, (float)c);
     return st < kMinShare ? 0 : (st > N - kMinShare ? N : st);
 }
 
@@ -199,7 +208,7 @@ __device__ __forceinline__ Line line_at(const TcParams& p, int ctas, int shift) 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     l.total = sum;
-    l.per = max((l.total + ctas - 1) / ctas, (int64_t)kMinRange);
+    l.per = max((int64_t)__umul64hi((uint64_t)l.total, p.ctas_mul) + 1, (int64_t)kMinRange);
     l.at = ((int64_t)blockIdx.x + shift) * l.per;
     l.b = B;
     l.start = 0;
@@ -239,8 +248,9 @@ __device__ __forceinline__ void find_item(const TcParams& p, const Seq& s, int64
     }
     rel -= cost_before(p, s, j) * H;
     const int c = cost(p, s, j);
-    h = 0;
-    if (rel >= c) h = rel < 0x7fffffff ? (int)((uint32_t)rel / (uint32_t)c) : (int)(rel / c);
+    h = min(H - 1, (int)__fdividef(__ll2float_rn(rel), (float)c));     // within one of the quotient
+    if ((int64_t)h * c > rel) --h;
+    if (h + 1 < H && (int64_t)(h + 1) * c <= rel) ++h;
     x = rel - (int64_t)h * c;
 }
 
@@ -905,10 +915,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 tmem_ld128_sync(lane_base, sv);
                 const int key0 = (it.s0 + st) * kStep;
                 if (lim_min < key0 + kStep || missing) {
-                    const int rel = lim - key0;
+                    const int rel = lim - key0, rel_min = lim_min - key0;
+                    // 32 keys at a time, where a row of this warp ends before or in them
 #pragma unroll
-                    for (int j = 0; j < 128; ++j)
-                        if (j >= rel) sv[j] = __float_as_uint(-INFINITY);
+                    for (int q = 0; q < 4; ++q)
+                        if (rel_min < 32 * (q + 1)) {
+#pragma unroll
+                            for (int j = 32 * q; j < 32 * (q + 1); ++j)
+                                if (j >= rel) sv[j] = __float_as_uint(-INFINITY);
+                        }
                     if (PAGED && missing) {
                         // 128 bits, one a key: the words' bits spread over their boxes
                         unsigned gone[4] = {0, 0, 0, 0};
@@ -1215,6 +1230,13 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
         while (a.kv.page_size % p.box != 0) p.box /= 2;
     p.boxes = kStep / p.box;
     while ((1 << p.box_shift) < p.box) ++p.box_shift;
+    // for x < 2^31: multiplier rounded up at 2^(31 + ceil(log2 d))
+    const uint32_t unit = 2 * p.TR;
+    int up = 0;
+    while ((1u << up) < unit) ++up;
+    p.unit_shift = 31 + up;
+    p.unit_mul = (uint32_t)((((uint64_t)1 << p.unit_shift) + unit - 1) / unit);
+    p.ctas_mul = ~uint64_t(0) / (uint64_t)(num_sms < kMaxCtas ? num_sms : kMaxCtas) + 1;
     p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.ws_o = static_cast<float*>(a.ws);
     p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;
