@@ -27,11 +27,10 @@
 //   - producer: Q tiles and a ring of 128-key K and V tiles in the order the
 //     MMAs use them, running ahead across items.  Packed rows and 16-bit pages
 //     of a multiple of 16 tokens come by TMA (one warp; a page is a box of a
-//     4-D map).  8-bit pages, and 16-bit pages of other sizes, come row by row
-//     through three warps' 16-byte cp.async: 8-bit rows into a staging tile,
-//     from which the thread that copied a piece writes it out as fp16 (exact)
-//     into the 128-byte-swizzled tile the MMA reads.  Rows without a key are
-//     zeros.
+//     4-D map).  8-bit pages come by TMA into two swizzled staging tiles, from
+//     which two mover warps write them out as fp16 (exact) into the tiles the
+//     MMA reads.  Pages of other sizes come row by row through the movers'
+//     16-byte cp.async.  Rows without a key are zeros.
 // TMEM: tile t at column 256 t: S / P in [0, 128), O in [128, 128 + D).
 //
 // With an 8-bit cache both products run in fp16.  bf16 rows of q are scaled to
@@ -62,7 +61,7 @@ constexpr int kTileM = 128;
 constexpr int kStep = 128;                  // keys of a step
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kGather = 96;                 // threads of the gathering producer (warps 9, 10, 11)
+constexpr int kMoveWarp = 10, kMovers = 64; // the movers: warps 10 and 11
 constexpr int kThreads = 384;
 constexpr int kRegsLaunch = 168, kRegsControl = 80, kRegsSoftmax = 208;
 static_assert(kRegsSoftmax * kSoftWarps * 32 + kRegsControl * 128 <= kRegsLaunch * kThreads,
@@ -90,9 +89,8 @@ struct TcSmem {
     static constexpr int ring = 2 * tile;
     static constexpr int staging = ring + slots * tile;    // two tiles of 8-bit rows
     static constexpr int rows = staging + (f8 ? 2 * kStep * D : 0);   // row numbers of two steps
-    static constexpr int expo = rows + (gather ? 2 * kStep * 4 : 0);  // exponents of q's rows
-    static constexpr int bars = expo + (f8 ? 2 * kTileM : 0);
-    static constexpr int items = bars + 8 * 36;            // the two items being worked on
+    static constexpr int bars = rows + (gather ? 2 * kStep * 4 : 0);
+    static constexpr int items = bars + 8 * 38;            // the two items being worked on
     static constexpr int abort = items + 2 * 48;
     static constexpr int tmem_slot = abort + 4;
     static constexpr int total = abort + 16;
@@ -101,20 +99,21 @@ struct TcSmem {
 };
 
 enum {
-    B_Q = 0,            // Q tiles of the item landed
-    B_Q_FREE = 1,       // every Q.K^T of the item done
-    B_S = 2,            // + t: S_t written (and the P.V before it done)
-    B_P = 4,            // + t: all of P_t written (one arrival a warp)
-    B_PH = 6,           // + t: P_t of keys 0..63 written
-    B_O = 8,            // + t: O_t of the item complete
-    B_TAIL = 10,        // V tile landed whose tail is still to be cleared
-    B_DRAIN = 11,
-    B_EXPO = 12,        // + t: the softmax has read the exponents of tile t's rows
-    B_FULL = 14,        // + slot
+    B_Q = 0,            // + t: Q tile t of the item there
+    B_Q_FREE = 2,       // every Q.K^T of the item done
+    B_S = 3,            // + t: S_t written (and the P.V before it done)
+    B_P = 5,            // + t: all of P_t written (one arrival a warp)
+    B_PH = 7,           // + t: P_t of keys 0..63 written
+    B_O = 9,            // + t: O_t of the item complete
+    B_TAIL = 11,        // V tile landed whose tail is still to be cleared
+    B_DRAIN = 12,
+    B_ROWS = 13,        // the movers met (one arrival a warp)
+    B_FULL = 14,        // + slot (gathered: one arrival a mover warp)
     B_FREE = 22,        // + slot
-    B_ROWS = 30,        // row numbers of a step written
-    B_ITEM = 31,        // + i: item slot i written
-    B_ITEM_FREE = 33    // + i: item slot i read by the MMA warp and the softmax warps
+    B_ITEM = 30,        // + i: item slot i written
+    B_ITEM_FREE = 32,   // + i: item slot i read by the MMA, softmax and mover warps
+    B_STAGE = 34,       // + i: staging tile i landed
+    B_STAGE_FREE = 36   // + i: staging tile i read (one arrival a mover warp)
 };
 
 struct TcParams {
@@ -410,71 +409,98 @@ __device__ __forceinline__ void commit(uint32_t bar) {
         : "memory");
 }
 
-// The gathering producer: three warps, thread x of kGather.  Tile y of an item
-// (K of step y / 2, then its V) is copied while tile y - 1 is finished.
-template <class E, int D, int SRC>
-__device__ __forceinline__ void gather_rows(const TcParams& p, const CUtensorMap& mq, unsigned char* smem,
-                                            uint32_t sbase, int x, int ctas) {
+// 16-byte piece `ch` of 8-bit row r in a staging tile: TMA's swizzle for rows
+// of 128 or 64 bytes.
+template <int D>
+__device__ __forceinline__ int staged(int r, int ch) {
+    return r * D + ((ch ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+}
+
+// The movers, thread x of kMovers: K and V tiles that TMA does not bring into
+// the ring by itself.  A thread works on rows x and x + 64.
+template <int D, int SRC>
+__device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem, uint32_t sbase, int x) {
     using L = TcSmem<D, SRC>;
     constexpr bool F8 = L::f8, E5 = SRC == SRC_E5M2;
-    constexpr bool kScaledQ = F8 && std::is_same<E, BF16>::value;
     constexpr int EB = F8 ? 1 : 2, RB = D * EB;
     constexpr int PR = RB / 16;                              // 16-byte pieces of a row
-    constexpr int kPieces = kStep * PR;
     const SeqAttn& a = p.a;
     int* err = a.err_word;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort);
     auto bar = [&](int i) { return sbase + L::bars + 8 * i; };
+    auto all = [](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+    // one arrival for this warp, behind what all its lanes did
+    auto arrive = [&](int b) {
+        __syncwarp();
+        if ((x & 31) == 0) mbar_arrive(bar(b));
+    };
     uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::rows);
-    const bool hnd = p.hnd != 0;
-    Walk walk(p, line_at(p, ctas, 0));
-    Item it;
-    int number = 0, items = 0, loads = 0, tables = 0;
-    int read[2] = {0, 0};            // items whose tile t had keys
+    const bool tma = F8 && p.box >= 16;                      // staging tiles filled by the loader's TMA
+    int loads = 0, tables = 0;
     bool ok = true;
-    for (;;) {
-        const bool more = walk.next(p, it);
-        if (!more) it.b = -1;
-        if (x == 0) ok = put_item<L>(smem, sbase, number, it, err, abort_flag);
-        ++number;
-        if (!more) break;
-        ok = __all_sync(0xffffffffu, ok);
+    // both movers are here (with what they wrote to shared memory)
+    auto together = [&]() -> bool {
+        arrive(B_ROWS);
+        return all(mbar_wait(bar(B_ROWS), tables++ & 1, err, abort_flag));
+    };
+    for (int number = 0; ok; ++number) {
+        Item it;
+        ok = all(get_item<L>(smem, sbase, number, it, err, abort_flag));
         if (!ok) break;
-        const int n = max(it.n[0], it.n[1]);
-        if (n == 0) continue;
-        // row numbers (in units of D elements) of step st's keys.  (The table
+        arrive(B_ITEM_FREE + (number & 1));
+        if (it.b < 0) break;
+        const int n = max(it.n[0], it.n[1]), s0 = it.s0, kv_len = it.kv_len, h = it.h;
+        const int32_t* table = a.kv.page_table + (int64_t)it.b * a.kv.max_pages;
+        // pages of this thread's two keys of a step, looked up a step ahead
+        // (left as loaded, so that nothing waits for the load)
+        int ahead[2];
+        auto look_up = [&](int st) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int key = (s0 + st) * kStep + x + i * kMovers;
+                ahead[i] = st < n && key < kv_len ? table[key / a.kv.page_size] : -1;
+            }
+        };
+        // Row numbers (in units of D elements) of step st's keys.  (The table
         // of a step is written over two steps later: by then every thread
         // has passed the barrier of the step between, after its last read.)
         auto find_rows = [&](int st) -> bool {
-            for (int i = x; i < kStep; i += kGather) {
-                const int key = (it.s0 + st) * kStep + i;
-                uint32_t row = 0xffffffffu;
-                if (key < it.kv_len) {
-                    const int slot = key / a.kv.page_size, place = key - slot * a.kv.page_size;
-                    const int pg = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + slot];
-                    if ((unsigned)pg < (unsigned)a.kv.num_pages)
-                        row = hnd ? ((uint32_t)pg * a.kv.Hkv + it.h) * a.kv.page_size + place
-                                  : ((uint32_t)pg * a.kv.page_size + place) * a.kv.Hkv + it.h;
-                }
-                rows[(st & 1) * kStep + i] = row;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = x + i * kMovers, place = ((s0 + st) * kStep + k) % a.kv.page_size;
+                const uint32_t pg = (uint32_t)ahead[i];
+                rows[(st & 1) * kStep + k] = pg >= (uint32_t)a.kv.num_pages ? 0xffffffffu
+                                             : p.hnd ? (pg * a.kv.Hkv + h) * a.kv.page_size + place
+                                                     : (pg * a.kv.page_size + place) * a.kv.Hkv + h;
             }
-            mbar_arrive(bar(B_ROWS));
-            return mbar_wait(bar(B_ROWS), tables++ & 1, err, abort_flag);
+            return together();
         };
-        // tile y, ring index `load`
+        auto wait_free = [&](int load) {
+            return load < L::slots ||
+                   all(mbar_wait(bar(B_FREE + load % L::slots), (load / L::slots - 1) & 1, err, abort_flag));
+        };
+        // starts the copy of tile y, ring index `load`, row by row
         auto copy = [&](int y, int load) -> bool {
             if (y < 2 * n) {
                 const int st = y >> 1;
-                if (!(y & 1) && !__all_sync(0xffffffffu, find_rows(st))) return false;
+                // (here, too: both have read what the staging tile held)
+                if (!(y & 1)) {
+                    if (!find_rows(st)) return false;
+                    look_up(st + 1);
+                } else if (F8) {
+                    if (!together()) return false;
+                }
+                if (!F8 && !wait_free(load)) return false;
                 const char* src = static_cast<const char*>((y & 1) ? a.kv.v : a.kv.k);
-                unsigned char* stage = smem + L::staging + (y & 1) * kStep * D;
+                unsigned char* stage = smem + L::staging + (load & 1) * kStep * D;
                 unsigned char* slot = smem + L::ring + (load % L::slots) * L::tile;
-#pragma unroll 4
-                for (int id = x; id < kPieces; id += kGather) {
-                    const int r = id / PR, ch = id % PR;
+                const int ch = x % PR;
+                // kMovers / PR rows at a time, a row's pieces side by side
+#pragma unroll 8
+                for (int r = x / PR; r < kStep; r += kMovers / PR) {
                     const uint32_t row = rows[(st & 1) * kStep + r];
                     const bool in = row != 0xffffffffu;
-                    unsigned char* dst = F8 ? stage + id * 16
+                    unsigned char* dst = F8 ? stage + staged<D>(r, ch)
                                             : slot + (ch >> 3) * L::panel + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
                     cp_async_16_zfill(dst, src + (in ? (int64_t)row * RB + ch * 16 : 0), in ? 16 : 0);
                 }
@@ -482,108 +508,58 @@ __device__ __forceinline__ void gather_rows(const TcParams& p, const CUtensorMap
             cp_async_commit();
             return true;
         };
-        auto wait_free = [&](int load) {
-            return load < L::slots || mbar_wait(bar(B_FREE + load % L::slots), (load / L::slots - 1) & 1, err, abort_flag);
-        };
-        auto all = [](bool v) { return __all_sync(0xffffffffu, v) != 0; };
-
-        // ---- Q ----
-        if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
-        if constexpr (kScaledQ) {
-            for (int t = 0; t < 2; ++t) {
-                if (ok && read[t] > 0) ok = mbar_wait(bar(B_EXPO + t), (read[t] - 1) & 1, err, abort_flag);
-                if (it.n[t] > 0) ++read[t];
-            }
-            ok = all(ok);
-            if (ok) {
-                constexpr int PQ = D / 8;                    // pieces of a q row, one lane each
-                signed char* expo = reinterpret_cast<signed char*>(smem + L::expo);
-                const int ch = x % PQ, tr = p.TR * a.G;
-#pragma unroll 8
-                for (int id = x; id < 2 * kTileM * PQ; id += kGather) {
-                    const int r = id / PQ, t = r / kTileM, rr = r % kTileM;
-                    const int tok = it.tok0 + t * p.TR + rr / a.G;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (rr < tr && tok < it.n_q)
-                        w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                            (int64_t)(it.q_row + tok) * a.q_stride +
-                                                            (it.h * a.G + rr % a.G) * D + ch * 8);
-                    uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                    float top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = BF16::unpack2(v[i]);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
-#pragma unroll
-                    for (int o = 1; o < PQ; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int e8 = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
-                    const int e = (top == 0.f || e8 > 127) ? 0 : min(max(e8 - 3, -120), 120);
-                    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 y = BF16::unpack2(v[i]);
-                        v[i] = F16::pack2(y.x * f, y.y * f);
-                    }
-                    *reinterpret_cast<uint4*>(smem + L::q + t * L::tile + (ch >> 3) * L::panel + rr * 128 +
-                                              (((ch & 7) ^ (rr & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                    if (ch == 0) expo[r] = (signed char)e;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(bar(B_Q));
-            }
-        } else if (ok && x == 0) {
-            const int tiles = it.tok0 + p.TR < it.n_q ? 2 : 1;
-            mbar_arrive_expect_tx(bar(B_Q), tiles * L::panels * p.TR * a.G * 128);
-            for (int t = 0; t < tiles; ++t)
-                for (int pn = 0; pn < L::panels; ++pn)
-                    tma_load_3d(sbase + L::q + t * L::tile + pn * L::panel, &mq, pn * 64, it.h * a.G,
-                                it.q_row + it.tok0 + t * p.TR, bar(B_Q));
+        if (!tma && n > 0) {
+            look_up(0);
+            ok = copy(0, loads);
         }
-        ok = all(ok);
-        ++items;
-
-        // ---- K and V ----
-        if (!F8 && ok) ok = all(wait_free(loads));
-        if (ok) ok = copy(0, loads);
         for (int y = 0; y < 2 * n && ok; ++y) {
-            // tile y + 1 on its way: 8-bit into the other staging tile (this
-            // thread has finished what it held there), 16-bit into its slot
-            if (!F8 && y + 1 < 2 * n) {
-                ok = all(wait_free(loads + 1));
-                if (!ok) break;
+            if (tma) {
+                ok = all(mbar_wait(bar(B_STAGE + (loads & 1)), (loads >> 1) & 1, err, abort_flag));
+            } else {
+                // the next tile on its way, this one landed
+                ok = copy(y + 1, loads + 1);
+                cp_async_wait<1>();
+                // (8-bit pieces are read by other threads of both warps than copied them)
+                if (F8 && ok) ok = together();
             }
-            ok = copy(y + 1, loads + 1);
+            if (F8 && ok) ok = wait_free(loads);
             if (!ok) break;
-            cp_async_wait<1>();
             if constexpr (F8) {
-                ok = all(wait_free(loads));
-                if (!ok) break;
-                const unsigned char* stage = smem + L::staging + (y & 1) * kStep * D;
+                const unsigned char* stage = smem + L::staging + (loads & 1) * kStep * D;
                 unsigned char* slot = smem + L::ring + (loads % L::slots) * L::tile;
-#pragma unroll 2
-                for (int id = x; id < kPieces; id += kGather) {
-                    const int r = id / PR, ch = id % PR;
-                    const uint4 c = *reinterpret_cast<const uint4*>(stage + id * 16);
-                    const uint4 lo = make_uint4(codes_h2<E5>(c.x), codes_h2<E5>(c.x >> 16), codes_h2<E5>(c.y),
-                                                codes_h2<E5>(c.y >> 16));
-                    const uint4 hi = make_uint4(codes_h2<E5>(c.z), codes_h2<E5>(c.z >> 16), codes_h2<E5>(c.w),
-                                                codes_h2<E5>(c.w >> 16));
-                    unsigned char* to = slot + (ch >> 2) * L::panel + r * 128;
-                    const int c0 = (ch & 3) * 2, first = ch >> 2;     // panels start on opposite halves: no bank twice
-                    *reinterpret_cast<uint4*>(to + (((c0 + first) ^ (r & 7)) << 4)) = first ? hi : lo;
-                    *reinterpret_cast<uint4*>(to + (((c0 + 1 - first) ^ (r & 7)) << 4)) = first ? lo : hi;
+                // (a page goes on behind the last token: rows from there on are written as zeros)
+                const int real = kv_len - (s0 + (y >> 1)) * kStep;
+                auto widen = [&](int r, int ch, uint4 c) {
+                    // lanes = rows: the swizzle puts neighbours on different banks, here and in the staging tile
+                    unsigned char* to = slot + (ch >> 2) * L::panel + r * 128 + ((((ch & 3) * 2) ^ (r & 7)) << 4);
+                    *reinterpret_cast<uint4*>(to) = make_uint4(codes_h2<E5>(c.x), codes_h2<E5>(c.x >> 16),
+                                                               codes_h2<E5>(c.y), codes_h2<E5>(c.y >> 16));
+                    *reinterpret_cast<uint4*>(slot + ((to - slot) ^ 16)) = make_uint4(codes_h2<E5>(c.z), codes_h2<E5>(c.z >> 16),
+                                                                                      codes_h2<E5>(c.w), codes_h2<E5>(c.w >> 16));
+                };
+#pragma unroll 1
+                for (int r = x; r < kStep; r += kMovers) {
+#pragma unroll
+                    for (int c0 = 0; c0 < PR; c0 += 4) {
+                        uint4 c[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4*>(stage + staged<D>(r, c0 + i));
+                        if (r >= real) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) c[i] = make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) widen(r, c0 + i, c[i]);
+                    }
                 }
+                if (tma) arrive(B_STAGE_FREE + (loads & 1));
             }
             fence_proxy_async_smem();
-            mbar_arrive(bar(B_FULL + loads % L::slots));
+            arrive(B_FULL + loads % L::slots);
             ++loads;
         }
-        if (!ok) break;
     }
     cp_async_wait<0>();
-    if (!ok && !kScaledQ && x == 0 && items > 0)
-        mbar_wait(bar(B_Q), (items - 1) & 1, nullptr, nullptr, 100000000ull);   // the copy in flight lands
 }
 
 template <class E, int D, int SRC>
@@ -612,11 +588,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort);
     if (tid == 0) {
         *abort_flag = 0;
-        mbar_init(bar(B_Q), kScaledQ ? kGather : 1);
-        mbar_init(bar(B_ROWS), kGather);
+        mbar_init(bar(B_ROWS), kMovers / 32);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_ITEM + i), 1);
-            mbar_init(bar(B_ITEM_FREE + i), kSoftWarps + 1);
+            mbar_init(bar(B_ITEM_FREE + i), kSoftWarps + 1 + (L::gather ? kMovers / 32 : 0));
+            mbar_init(bar(B_STAGE + i), 1);
+            mbar_init(bar(B_STAGE_FREE + i), kMovers / 32);
         }
         mbar_init(bar(B_Q_FREE), 1);
         mbar_init(bar(B_TAIL), 1);
@@ -626,10 +603,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(bar(B_P + t), 4);
             mbar_init(bar(B_PH + t), 4);
             mbar_init(bar(B_O + t), 1);
-            mbar_init(bar(B_EXPO + t), kTileM);
+            mbar_init(bar(B_Q + t), kScaledQ ? 4 : 1);
         }
         for (int s = 0; s < L::slots; ++s) {
-            mbar_init(bar(B_FULL + s), L::gather ? kGather : 1);
+            mbar_init(bar(B_FULL + s), L::gather ? kMovers / 32 : 1);
             mbar_init(bar(B_FREE + s), 1);
         }
         fence_barrier_init();
@@ -644,10 +621,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 
     if (warp >= kSoftWarps) {
         regs_release<kRegsControl>();
-        if (L::gather && warp >= kLoadWarp) {
-            if constexpr (L::gather) gather_rows<E, D, SRC>(p, mq, smem, sbase, tid - kLoadWarp * 32, ctas);
+        if (L::gather && warp >= kMoveWarp) {
+            if constexpr (L::gather) move_rows<D, SRC>(p, smem, sbase, tid - kMoveWarp * 32);
         } else if (warp == kLoadWarp) {
-            // ============================ producer (TMA) ============================
+            // ============================ loader ============================
             if (lane == 0) {
                 tma_prefetch_map(&mq);
                 tma_prefetch_map(&mk);
@@ -657,6 +634,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             Item it;
             int number = 0;
             int items = 0, loads = 0, tails = 0;   // items with keys, tiles loaded, tiles cleared
+            int qs[2] = {0, 0};                    // Q tiles loaded
+            const bool tma = !L::gather || (L::f8 && p.box >= 16);
             bool ok = true;
             while (ok) {
                 const bool more = walk.next(p, it);
@@ -667,18 +646,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 if (!more || !ok) break;
                 const int n = max(it.n[0], it.n[1]);
                 if (n == 0) continue;
-                if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    const int tiles = it.tok0 + p.TR < it.n_q ? 2 : 1;
-                    mbar_arrive_expect_tx(bar(B_Q), tiles * L::panels * p.TR * G * 128);
-                    for (int t = 0; t < tiles; ++t)
+                if constexpr (!kScaledQ) {
+                    if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (it.n[t] == 0) continue;
+                        ++qs[t];
+                        if (lane != 0) continue;
+                        mbar_arrive_expect_tx(bar(B_Q + t), L::panels * p.TR * G * 128);
                         for (int pn = 0; pn < L::panels; ++pn)
                             tma_load_3d(sbase + L::q + t * L::tile + pn * L::panel, &mq, pn * 64, it.h * G,
-                                        it.q_row + it.tok0 + t * p.TR, bar(B_Q));
+                                        it.q_row + it.tok0 + t * p.TR, bar(B_Q + t));
+                    }
                 }
                 ++items;
+                if (!tma) continue;
                 // page of this lane's box of a step, -1 if there is none to read
                 auto page_of = [&](int st) -> int {
                     const int key = (it.s0 + st) * kStep + lane * p.box;
@@ -693,25 +677,28 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     const int pg = page;
                     if constexpr (PAGED) page = page_of(st + 1);
                     for (int kv = 0; kv < 2 && ok; ++kv) {
-                        const int s = loads % L::slots;
-                        if (loads >= L::slots)
-                            ok = mbar_wait(bar(B_FREE + s), (loads / L::slots - 1) & 1, err, abort_flag);
+                        // 16-bit tiles go into the ring, 8-bit ones into the staging tiles
+                        constexpr int kDepth = L::gather ? 2 : L::slots;
+                        const int s = loads % kDepth;
+                        if (loads >= kDepth)
+                            ok = mbar_wait(bar((L::gather ? B_STAGE_FREE : B_FREE) + s), (loads / kDepth - 1) & 1, err, abort_flag);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
-                        const uint32_t dst = sbase + L::ring + s * L::tile;
+                        const uint32_t dst = sbase + (L::gather ? L::staging + s * kStep * D : L::ring + s * L::tile);
                         const int real = it.kv_len - key0;             // keys of this tile that exist
-                        const bool tail = kv == 1 && real < kStep;
-                        const uint32_t b = bar(tail ? B_TAIL : B_FULL + s);
+                        const bool tail = !L::gather && kv == 1 && real < kStep;
+                        const uint32_t b = bar(tail ? B_TAIL : (L::gather ? B_STAGE : B_FULL) + s);
                         const CUtensorMap* map = kv ? &mv : &mk;
-                        if (lane == 0) mbar_arrive_expect_tx(b, L::tile);
+                        if (lane == 0) mbar_arrive_expect_tx(b, L::gather ? kStep * D : L::tile);
                         __syncwarp();
                         if constexpr (PAGED) {
                             if (lane < p.boxes) {
                                 // a box without a page reads page num_pages: outside, zeros
                                 const int at = pg < 0 ? a.kv.num_pages : pg;
                                 const int place = pg < 0 ? 0 : (key0 + lane * p.box) % a.kv.page_size;
-                                for (int pn = 0; pn < L::panels; ++pn) {
-                                    const uint32_t to = dst + pn * L::panel + lane * p.box * 128;
+                                constexpr int kRow = L::gather ? D : 128;          // bytes of a box's row
+                                for (int pn = 0; pn < (L::gather ? 1 : L::panels); ++pn) {
+                                    const uint32_t to = dst + pn * L::panel + lane * p.box * kRow;
                                     if (p.hnd) tma_load_4d(to, map, pn * 64, place, it.h, at, b);
                                     else tma_load_4d(to, map, pn * 64, it.h, place, at, b);
                                 }
@@ -740,9 +727,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
             if (!ok && lane == 0) {
                 // a wait gave up: let the copies in flight land (bounded) before leaving
-                if (items > 0) mbar_wait(bar(B_Q), (items - 1) & 1, nullptr, nullptr, 100000000ull);
-                for (int x = max(0, loads - L::slots); x < loads; ++x)
-                    mbar_wait(bar(B_FULL + x % L::slots), (x / L::slots) & 1, nullptr, nullptr, 100000000ull);
+                for (int t = 0; t < 2; ++t)
+                    if (qs[t] > 0) mbar_wait(bar(B_Q + t), (qs[t] - 1) & 1, nullptr, nullptr, 100000000ull);
+                constexpr int kDepth = L::gather ? 2 : L::slots;
+                for (int x = max(0, loads - kDepth); x < loads; ++x)
+                    mbar_wait(bar((L::gather ? B_STAGE : B_FULL) + x % kDepth), (x / kDepth) & 1, nullptr, nullptr, 100000000ull);
             }
         } else if (warp == kMmaWarp) {
             // ============================ MMA ============================
@@ -751,7 +740,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             const uint32_t v_lo = ((sbase + L::ring) >> 4) | ((uint32_t)(L::panel >> 4) << 16);
             const uint32_t q_lo = ((sbase + L::q) >> 4) | (1u << 16);
             Item it;
-            int items = 0, x = 0;           // items with keys; tiles of the ring used so far
+            int x = 0;                      // tiles of the ring used so far
+            int qs0 = 0, qs1 = 0;           // Q tiles used
             int slot = 0;                   // x % slots
             int done0 = 0, done1 = 0;       // P tiles consumed
             bool ok = true;
@@ -786,12 +776,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 const int n0 = __shfl_sync(0xffffffffu, it.n[0], 0), n1 = __shfl_sync(0xffffffffu, it.n[1], 0);
                 const int n = max(n0, n1);
                 if (n == 0) continue;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_Q), items & 1, err, abort_flag)) && full(slot, x);
+                ok = full(slot, x);
+                if (ok && n0 > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_Q), qs0++ & 1, err, abort_flag)) != 0;
+                    tc_fence_after();
+                    if (ok) qk(0, slot);
+                }
+                if (ok && n1 > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_Q + 1), qs1++ & 1, err, abort_flag)) != 0;
+                    tc_fence_after();
+                    if (ok) qk(1, slot);
+                }
                 if (!ok) break;
-                ++items;
-                tc_fence_after();
-                if (n0 > 0) qk(0, slot);
-                if (n1 > 0) qk(1, slot);
                 for (int i = 0; i < n; ++i) {
                     // V of step i, K of step i + 1
                     const int vs = after(slot), ks = after(vs);
@@ -844,7 +840,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + t * kTileCols;
         int steps = 0, outs = 0;                            // barrier phases of this tile so far
         int base = 0;                                       // ring index of the item's first tile
-        const signed char* expo = reinterpret_cast<const signed char*>(smem + L::expo);
         Item it;
         bool ok = true;
         for (int number = 0; ok; ++number) {
@@ -869,6 +864,42 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             float rs = a.scale_log2;
             if constexpr (F8)
                 if (a.kv.scale_k) rs *= a.kv.scale_k[it.h];
+            if constexpr (kScaledQ) {
+                // This thread's row of q as fp16, scaled by 2^-e.  (The last
+                // Q.K^T that read the tile was done before the S of the item
+                // before was there.)
+                if (n > 0) {
+                    uint32_t w[D / 2];
+                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                                      (int64_t)(it.q_row + tok) * a.q_stride + head * D);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        reinterpret_cast<uint4*>(w)[c] = valid ? src[c] : make_uint4(0, 0, 0, 0);
+                    float top = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 2; ++c) {
+                        const float2 f = BF16::unpack2(w[c]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                    const int e8 = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
+                    const int e = (top == 0.f || e8 > 127) ? 0 : min(max(e8 - 3, -120), 120);
+                    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                    for (int c = 0; c < D / 2; ++c) {
+                        const float2 y = BF16::unpack2(w[c]);
+                        w[c] = F16::pack2(y.x * f, y.y * f);
+                    }
+                    unsigned char* to = smem + L::q + t * L::tile + r * 128;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        *reinterpret_cast<uint4*>(to + (c >> 3) * L::panel + (((c & 7) ^ (r & 7)) << 4)) =
+                            reinterpret_cast<const uint4*>(w)[c];
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_Q + t));
+                    rs *= __uint_as_float((uint32_t)(127 + e) << 23);
+                }
+            }
             float m_used = -INFINITY, l = 0.f;
             // boxes (runs of p.box keys that no page border cuts) of step st
             // whose page is out of range: bit i of this lane = box lane + 32 i
@@ -905,12 +936,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     if (st == n - 1) mbar_arrive(bar(B_Q_FREE));
                 }
                 tc_fence_after();
-                if constexpr (kScaledQ)
-                    if (st == 0) {
-                        // 2^expo[row] takes q's scaling out of the scores
-                        rs *= __uint_as_float((uint32_t)(127 + expo[t * kTileM + r]) << 23);
-                        mbar_arrive(bar(B_EXPO + t));
-                    }
                 uint32_t sv[128];
                 tmem_ld128_sync(lane_base, sv);
                 const int key0 = (it.s0 + st) * kStep;
@@ -1172,6 +1197,19 @@ bool pool_map(CUtensorMap* m, const void* base, bool bf16, const SeqKV& kv, bool
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A pool of 8-bit codes likewise; box D bytes x `box_rows` places, swizzled over a row (see staged()).
+bool codes_map(CUtensorMap* m, const void* base, const SeqKV& kv, bool hnd, int box_rows) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t D = kv.D, H = kv.Hkv, P = kv.page_size;
+    const cuuint64_t dim[4] = {D, hnd ? P : H, hnd ? H : P, (cuuint64_t)kv.num_pages};
+    const cuuint64_t st[3] = {D, (hnd ? P : H) * D, H * P * D};
+    const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(hnd ? box_rows : 1), (cuuint32_t)(hnd ? 1 : box_rows), 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dim, st, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              kv.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class E, int D, int SRC>
 cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStream_t stream) {
     using L = TcSmem<D, SRC>;
@@ -1180,7 +1218,9 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStr
     CUtensorMap mq, mk, mv;
     if (!rows_map(&mq, a.q, bf16, D, a.Hq, a.tokens, a.q_stride, a.G, p.TR)) return cudaErrorInvalidValue;
     if (L::gather) {
-        mk = mv = mq;              // K and V are gathered without maps
+        mk = mv = mq;              // (unused where rows are gathered without maps)
+        if (L::f8 && p.box >= 16 && (!codes_map(&mk, a.kv.k, a.kv, p.hnd, p.box) || !codes_map(&mv, a.kv.v, a.kv, p.hnd, p.box)))
+            return cudaErrorInvalidValue;
     } else if (SRC == SRC_PAGES ? (!pool_map(&mk, a.kv.k, bf16, a.kv, p.hnd, p.box) || !pool_map(&mv, a.kv.v, bf16, a.kv, p.hnd, p.box))
               : (!rows_map(&mk, a.kv.k, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.s_tok, 1, kStep) ||
                  !rows_map(&mv, a.kv.v, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.sv_tok, 1, kStep))) {
