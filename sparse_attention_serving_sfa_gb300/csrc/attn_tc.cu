@@ -15,7 +15,7 @@
 // most two of them from a CTA (the item it ends and the one it begins), which
 // attn_tc_merge joins in order of their keys.
 //
-// Warp roles, 384 threads:
+// Warp roles, 384 threads (512 with movers):
 //   - softmax warpgroups 0, 1: tile t, thread = row = TMEM lane.  Read the
 //     128 scores of a step, mask them (only where a row's limit or a missing
 //     page falls into the step), update m (O is rescaled only when m grows by
@@ -28,7 +28,7 @@
 //     MMAs use them, running ahead across items.  Packed rows and 16-bit pages
 //     of a multiple of 16 tokens come by TMA (one warp; a page is a box of a
 //     4-D map).  8-bit pages come by TMA into two swizzled staging tiles, from
-//     which two mover warps write them out as fp16 (exact) into the tiles the
+//     which four mover warps write them out as fp16 (exact) into the tiles the
 //     MMA reads.  Pages of other sizes come row by row through the movers'
 //     16-byte cp.async.  Rows without a key are zeros.
 // TMEM: tile t at column 256 t: S / P in [0, 128), O in [128, 128 + D).
@@ -61,11 +61,7 @@ constexpr int kTileM = 128;
 constexpr int kStep = 128;                  // keys of a step
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kMoveWarp = 10, kMovers = 64; // the movers: warps 10 and 11
-constexpr int kThreads = 384;
-constexpr int kRegsLaunch = 168, kRegsControl = 80, kRegsSoftmax = 208;
-static_assert(kRegsSoftmax * kSoftWarps * 32 + kRegsControl * 128 <= kRegsLaunch * kThreads,
-              "the register split fits what the block was launched with");
+constexpr int kMoveWarp = 12, kMovers = 128; // the movers: warps 12 to 15
 constexpr int kTmemCols = 512, kTileCols = 256, kOCol = 128;
 constexpr float kRescale = 8.0f;            // log2 units
 constexpr int kItemRows = 2 * kTileM;
@@ -77,6 +73,17 @@ constexpr int kMaxCtas = 160;               // ranges (the workspace's size goes
 // Where K and V come from: packed rows, or pages by TMA; or gathered rows of
 // 16-bit, E4M3 or E5M2 pages.
 enum { SRC_PACKED = 0, SRC_PAGES = 1, SRC_G16 = 2, SRC_E4M3 = 3, SRC_E5M2 = 4 };
+
+// Block size and registers a thread: at launch, then of the control warps and
+// of the softmax warps.  The movers come as a warpgroup of their own.
+template <int SRC>
+struct TcBlock {
+    static constexpr bool movers = SRC >= SRC_G16;
+    static constexpr int threads = movers ? 512 : 384;
+    static constexpr int launch = movers ? 128 : 168, control = movers ? 64 : 80, softmax = movers ? 192 : 208;
+    static_assert(softmax * kSoftWarps * 32 + control * (threads - kSoftWarps * 32) <= launch * threads,
+                  "the register split fits what the block was launched with");
+};
 
 template <int D, int SRC>
 struct TcSmem {
@@ -417,7 +424,7 @@ __device__ __forceinline__ int staged(int r, int ch) {
 }
 
 // The movers, thread x of kMovers: K and V tiles that TMA does not bring into
-// the ring by itself.  A thread works on rows x and x + 64.
+// the ring by itself.  A thread widens one row.
 template <int D, int SRC>
 __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem, uint32_t sbase, int x) {
     using L = TcSmem<D, SRC>;
@@ -434,6 +441,7 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
         __syncwarp();
         if ((x & 31) == 0) mbar_arrive(bar(b));
     };
+    static_assert(kMovers == kStep, "a thread a row");
     uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::rows);
     const bool tma = F8 && p.box >= 16;                      // staging tiles filled by the loader's TMA
     int loads = 0, tables = 0;
@@ -451,28 +459,22 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
         if (it.b < 0) break;
         const int n = max(it.n[0], it.n[1]), s0 = it.s0, kv_len = it.kv_len, h = it.h;
         const int32_t* table = a.kv.page_table + (int64_t)it.b * a.kv.max_pages;
-        // pages of this thread's two keys of a step, looked up a step ahead
-        // (left as loaded, so that nothing waits for the load)
-        int ahead[2];
+        // page of this thread's key of a step, looked up a step ahead (left as
+        // loaded, so that nothing waits for the load)
+        int ahead;
         auto look_up = [&](int st) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int key = (s0 + st) * kStep + x + i * kMovers;
-                ahead[i] = st < n && key < kv_len ? table[key / a.kv.page_size] : -1;
-            }
+            const int key = (s0 + st) * kStep + x;
+            ahead = st < n && key < kv_len ? table[key / a.kv.page_size] : -1;
         };
         // Row numbers (in units of D elements) of step st's keys.  (The table
         // of a step is written over two steps later: by then every thread
         // has passed the barrier of the step between, after its last read.)
         auto find_rows = [&](int st) -> bool {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int k = x + i * kMovers, place = ((s0 + st) * kStep + k) % a.kv.page_size;
-                const uint32_t pg = (uint32_t)ahead[i];
-                rows[(st & 1) * kStep + k] = pg >= (uint32_t)a.kv.num_pages ? 0xffffffffu
-                                             : p.hnd ? (pg * a.kv.Hkv + h) * a.kv.page_size + place
-                                                     : (pg * a.kv.page_size + place) * a.kv.Hkv + h;
-            }
+            const int place = ((s0 + st) * kStep + x) % a.kv.page_size;
+            const uint32_t pg = (uint32_t)ahead;
+            rows[(st & 1) * kStep + x] = pg >= (uint32_t)a.kv.num_pages ? 0xffffffffu
+                                         : p.hnd ? (pg * a.kv.Hkv + h) * a.kv.page_size + place
+                                                 : (pg * a.kv.page_size + place) * a.kv.Hkv + h;
             return together();
         };
         auto wait_free = [&](int load) {
@@ -537,21 +539,15 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
                     *reinterpret_cast<uint4*>(slot + ((to - slot) ^ 16)) = make_uint4(codes_h2<E5>(c.z), codes_h2<E5>(c.z >> 16),
                                                                                       codes_h2<E5>(c.w), codes_h2<E5>(c.w >> 16));
                 };
-#pragma unroll 1
-                for (int r = x; r < kStep; r += kMovers) {
+                uint4 c[PR];
 #pragma unroll
-                    for (int c0 = 0; c0 < PR; c0 += 4) {
-                        uint4 c[4];
+                for (int i = 0; i < PR; ++i) c[i] = *reinterpret_cast<const uint4*>(stage + staged<D>(x, i));
+                if (x >= real) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4*>(stage + staged<D>(r, c0 + i));
-                        if (r >= real) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) c[i] = make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) widen(r, c0 + i, c[i]);
-                    }
+                    for (int i = 0; i < PR; ++i) c[i] = make_uint4(0, 0, 0, 0);
                 }
+#pragma unroll
+                for (int i = 0; i < PR; ++i) widen(x, i, c[i]);
                 if (tma) arrive(B_STAGE_FREE + (loads & 1));
             }
             fence_proxy_async_smem();
@@ -563,7 +559,7 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
 }
 
 template <class E, int D, int SRC>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(TcBlock<SRC>::threads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const TcParams p, int ctas) {
     using L = TcSmem<D, SRC>;
@@ -620,7 +616,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     grid_launch_dependents();
 
     if (warp >= kSoftWarps) {
-        regs_release<kRegsControl>();
+        regs_release<TcBlock<SRC>::control>();
         if (L::gather && warp >= kMoveWarp) {
             if constexpr (L::gather) move_rows<D, SRC>(p, smem, sbase, tid - kMoveWarp * 32);
         } else if (warp == kLoadWarp) {
@@ -834,7 +830,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
     } else {
         // ============================ softmax ============================
-        regs_acquire<kRegsSoftmax>();
+        regs_acquire<TcBlock<SRC>::softmax>();
         const int t = warp >> 2;
         const int r = tid & 127;                            // row of the tile = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + t * kTileCols;
@@ -1229,17 +1225,17 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStr
     auto kern = attn_tc_kernel<E, D, SRC>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::alloc);
     if (err != cudaSuccess) return err;
-    // the register split assumes a launch with kRegsLaunch registers a thread
+    // the register split assumes a launch with that many registers a thread
     static int regs_ok = -1;
     if (regs_ok < 0) {
         cudaFuncAttributes fa;
         err = cudaFuncGetAttributes(&fa, kern);
         if (err != cudaSuccess) return err;
-        regs_ok = fa.numRegs == kRegsLaunch ? 1 : 0;
+        regs_ok = fa.numRegs == TcBlock<SRC>::launch ? 1 : 0;
     }
     if (!regs_ok) return cudaErrorInvalidConfiguration;
     const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-    err = launch_pdl(kern, dim3(ctas), dim3(kThreads), L::alloc, stream, mq, mk, mv, p, ctas);
+    err = launch_pdl(kern, dim3(ctas), dim3(TcBlock<SRC>::threads), L::alloc, stream, mq, mk, mv, p, ctas);
     if (err != cudaSuccess) return err;
     count_launches(1);
     // items of fewer than 2 kMinShare steps are never cut
