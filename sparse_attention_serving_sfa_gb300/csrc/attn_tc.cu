@@ -115,12 +115,12 @@ enum {
     B_TAIL = 11,        // V tile landed whose tail is still to be cleared
     B_DRAIN = 12,
     B_ROWS = 13,        // the movers met (one arrival a warp)
-    B_FULL = 14,        // + slot (gathered: one arrival a mover warp)
+    B_FULL = 14,        // + slot (gathered: one arrival a mover warp that fills it)
     B_FREE = 22,        // + slot
     B_ITEM = 30,        // + i: item slot i written
     B_ITEM_FREE = 32,   // + i: item slot i read by the MMA, softmax and mover warps
     B_STAGE = 34,       // + i: staging tile i landed
-    B_STAGE_FREE = 36   // + i: staging tile i read (one arrival a mover warp)
+    B_STAGE_FREE = 36   // + i: staging tile i read (one arrival a mover warp that does)
 };
 
 struct TcParams {
@@ -424,7 +424,7 @@ __device__ __forceinline__ int staged(int r, int ch) {
 }
 
 // The movers, thread x of kMovers: K and V tiles that TMA does not bring into
-// the ring by itself.  A thread widens one row.
+// the ring by itself.
 template <int D, int SRC>
 __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem, uint32_t sbase, int x) {
     using L = TcSmem<D, SRC>;
@@ -441,7 +441,7 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
         __syncwarp();
         if ((x & 31) == 0) mbar_arrive(bar(b));
     };
-    static_assert(kMovers == kStep, "a thread a row");
+    static_assert(kMovers == kStep, "a thread a row number");
     uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::rows);
     const bool tma = F8 && p.box >= 16;                      // staging tiles filled by the loader's TMA
     int loads = 0, tables = 0;
@@ -514,41 +514,56 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
             look_up(0);
             ok = copy(0, loads);
         }
-        for (int y = 0; y < 2 * n && ok; ++y) {
-            if (tma) {
-                ok = all(mbar_wait(bar(B_STAGE + (loads & 1)), (loads >> 1) & 1, err, abort_flag));
-            } else {
-                // the next tile on its way, this one landed
-                ok = copy(y + 1, loads + 1);
-                cp_async_wait<1>();
-                // (8-bit pieces are read by other threads of both warps than copied them)
-                if (F8 && ok) ok = together();
-            }
-            if (F8 && ok) ok = wait_free(loads);
-            if (!ok) break;
-            if constexpr (F8) {
-                const unsigned char* stage = smem + L::staging + (loads & 1) * kStep * D;
-                unsigned char* slot = smem + L::ring + (loads % L::slots) * L::tile;
-                // (a page goes on behind the last token: rows from there on are written as zeros)
-                const int real = kv_len - (s0 + (y >> 1)) * kStep;
-                auto widen = [&](int r, int ch, uint4 c) {
-                    // lanes = rows: the swizzle puts neighbours on different banks, here and in the staging tile
-                    unsigned char* to = slot + (ch >> 2) * L::panel + r * 128 + ((((ch & 3) * 2) ^ (r & 7)) << 4);
-                    *reinterpret_cast<uint4*>(to) = make_uint4(codes_h2<E5>(c.x), codes_h2<E5>(c.x >> 16),
-                                                               codes_h2<E5>(c.y), codes_h2<E5>(c.y >> 16));
-                    *reinterpret_cast<uint4*>(slot + ((to - slot) ^ 16)) = make_uint4(codes_h2<E5>(c.z), codes_h2<E5>(c.z >> 16),
-                                                                                      codes_h2<E5>(c.w), codes_h2<E5>(c.w >> 16));
-                };
+        // Rows r0, r0 + stride, .. of tile `load`, from its staging tile into its
+        // slot.  A page goes on behind the last token: rows from `real` on are
+        // written as zeros.
+        auto widen = [&](int load, int r0, int stride, int real) {
+            const unsigned char* stage = smem + L::staging + (load & 1) * kStep * D;
+            unsigned char* slot = smem + L::ring + (load % L::slots) * L::tile;
+            for (int r = r0; r < kStep; r += stride) {
+                // lanes = rows: the swizzle puts neighbours on different banks on both sides
                 uint4 c[PR];
 #pragma unroll
-                for (int i = 0; i < PR; ++i) c[i] = *reinterpret_cast<const uint4*>(stage + staged<D>(x, i));
-                if (x >= real) {
+                for (int i = 0; i < PR; ++i) c[i] = *reinterpret_cast<const uint4*>(stage + staged<D>(r, i));
+                if (r >= real) {
 #pragma unroll
                     for (int i = 0; i < PR; ++i) c[i] = make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int i = 0; i < PR; ++i) widen(x, i, c[i]);
-                if (tma) arrive(B_STAGE_FREE + (loads & 1));
+                for (int i = 0; i < PR; ++i) {
+                    const int to = (i >> 2) * L::panel + r * 128 + ((((i & 3) * 2) ^ (r & 7)) << 4);
+                    *reinterpret_cast<uint4*>(slot + to) = make_uint4(codes_h2<E5>(c[i].x), codes_h2<E5>(c[i].x >> 16),
+                                                                      codes_h2<E5>(c[i].y), codes_h2<E5>(c[i].y >> 16));
+                    *reinterpret_cast<uint4*>(slot + (to ^ 16)) = make_uint4(codes_h2<E5>(c[i].z), codes_h2<E5>(c[i].z >> 16),
+                                                                             codes_h2<E5>(c[i].w), codes_h2<E5>(c[i].w >> 16));
+                }
+            }
+        };
+        if (tma) {
+            // Warps 0, 1 do the K tiles, 2, 3 the V tiles: each pair goes at its own pace.
+            const int g = x >> 6;
+            for (int st = 0; st < n && ok; ++st) {
+                const int load = loads + 2 * st + g;
+                ok = all(mbar_wait(bar(B_STAGE + g), (load >> 1) & 1, err, abort_flag)) && wait_free(load);
+                if (!ok) break;
+                widen(load, x & 63, kMovers / 2, kv_len - (s0 + st) * kStep);
+                arrive(B_STAGE_FREE + g);
+                fence_proxy_async_smem();
+                arrive(B_FULL + load % L::slots);
+            }
+            loads += 2 * n;
+            continue;
+        }
+        for (int y = 0; y < 2 * n && ok; ++y) {
+            // the next tile on its way, this one landed
+            ok = copy(y + 1, loads + 1);
+            cp_async_wait<1>();
+            if (!ok) break;
+            if constexpr (F8) {
+                // (pieces are read by other threads than copied them)
+                ok = together() && wait_free(loads);
+                if (!ok) break;
+                widen(loads, x, kMovers, kStep);
             }
             fence_proxy_async_smem();
             arrive(B_FULL + loads % L::slots);
@@ -589,7 +604,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(bar(B_ITEM + i), 1);
             mbar_init(bar(B_ITEM_FREE + i), kSoftWarps + 1 + (L::gather ? kMovers / 32 : 0));
             mbar_init(bar(B_STAGE + i), 1);
-            mbar_init(bar(B_STAGE_FREE + i), kMovers / 32);
+            mbar_init(bar(B_STAGE_FREE + i), kMovers / 64);
         }
         mbar_init(bar(B_Q_FREE), 1);
         mbar_init(bar(B_TAIL), 1);
@@ -602,7 +617,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(bar(B_Q + t), kScaledQ ? 4 : 1);
         }
         for (int s = 0; s < L::slots; ++s) {
-            mbar_init(bar(B_FULL + s), L::gather ? kMovers / 32 : 1);
+            mbar_init(bar(B_FULL + s), !L::gather ? 1 : (L::f8 && p.box >= 16 ? kMovers / 64 : kMovers / 32));
             mbar_init(bar(B_FREE + s), 1);
         }
         fence_barrier_init();
