@@ -44,6 +44,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;            // rows of a tile
 constexpr int kMaxCtas = 320;        // ranges (the workspace's size goes by it)
+constexpr int kMinChunks = 4;        // shortest range: a part costs its way through the workspace
 constexpr float kRescale = 8.f;      // log2 growth of m that rescales O
 
 template <int D, int F8>
@@ -62,84 +63,82 @@ struct RowsCfg {
     static_assert(kRows * D * 4 <= warp_bytes, "a warp's O fits its ring");
 };
 
-struct Line {
-    int64_t total, per;
+// A sequence on the line: its tiles, kv heads and chunks are `tiles * Hkv *
+// chunks` units, the chunks of a tile side by side.
+struct Seq {
+    int q_row, n_q, k_row, kv_len, tiles, chunks;
 };
 
-// Units of sequence b: x = tiles, y = chunks.
-__device__ __forceinline__ int2 units_of(const SeqAttn& p, int b, int chunk) {
-    const int2 r = seq_rows(p.cu_q, b, p.tokens);
-    const int n = r.y - r.x;
-    const int kv = seq_keys(p.kv, b).y;
-    return make_int2((int)(((int64_t)n * p.G + kRows - 1) / kRows), max(1, (kv + chunk - 1) / chunk));
-}
-
-// Total units over all sequences (whole block; result uniform).
-__device__ int64_t total_units(const SeqAttn& p, int chunk, int64_t* red) {
-    int64_t s = 0;
-    for (int b = threadIdx.x; b < p.kv.num_seqs; b += kThreads) {
-        const int2 u = units_of(p, b, chunk);
-        s += (int64_t)u.x * u.y * p.kv.Hkv;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = 0;
-    for (int w = 0; w < kWarps; ++w) s += red[w];
-    __syncthreads();
+__device__ __forceinline__ Seq seq_of(const SeqAttn& p, int b, int chunk) {
+    const int2 q = seq_rows(p.cu_q, b, p.tokens);
+    const int2 k = seq_keys(p.kv, b);
+    Seq s;
+    s.q_row = q.x;
+    s.n_q = q.y - q.x;
+    s.k_row = k.x;
+    s.kv_len = k.y;
+    s.tiles = (s.n_q * p.G + kRows - 1) / kRows;             // (tokens * heads fits 30 bits)
+    s.chunks = max(1, (s.kv_len + chunk - 1) / chunk);
     return s;
 }
 
-// Sequence that holds unit u and the first unit of it (whole block).
-__device__ void locate(const SeqAttn& p, int chunk, int64_t u, int64_t* red, int& b_out, int64_t& start) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t base = 0;
-    b_out = p.kv.num_seqs;
-    start = 0;
-    for (int b0 = 0; b0 < p.kv.num_seqs; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        int64_t w = 0;
-        if (b < p.kv.num_seqs) {
-            const int2 x = units_of(p, b, chunk);
-            w = (int64_t)x.x * x.y * p.kv.Hkv;
-        }
-        int64_t inc = w;
+// The line's length, a range's length, the unit range (blockIdx.x + shift)
+// begins at, and the sequence (and its first unit) that holds it.  One warp;
+// every lane gets the answer.
+struct Line {
+    int64_t total, per, at, start;
+    int b;
+};
+
+__device__ __forceinline__ Line line_at(const SeqAttn& p, int chunk, uint64_t ctas_mul, int shift) {
+    const int lane = threadIdx.x & 31, B = p.kv.num_seqs;
+    auto length = [&](int b) -> int64_t {
+        if (b >= B) return 0;
+        const Seq s = seq_of(p, b, chunk);
+        return (int64_t)s.tiles * s.chunks * p.kv.Hkv;
+    };
+    Line l;
+    const int64_t first = length(lane);
+    int64_t sum = first;
+    for (int b = lane + 32; b < B; b += 32) sum += length(b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l.total = sum;
+    l.per = max((int64_t)__umul64hi((uint64_t)l.total, ctas_mul) + 1, (int64_t)kMinChunks);
+    l.at = ((int64_t)blockIdx.x + shift) * l.per;
+    l.b = B;
+    l.start = 0;
+    if (l.at >= l.total) return l;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int64_t mine = b0 == 0 ? first : length(b0 + lane);
+        int64_t inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
-        if (lane == 31) red[warp] = inc;
-        __syncthreads();
-        int64_t before = base;
-        for (int i = 0; i < warp; ++i) before += red[i];
-        int64_t all = 0;
-        for (int i = 0; i < kWarps; ++i) all += red[i];
-        const int64_t mine = before + inc - w;
-        __syncthreads();
-        if (w > 0 && mine <= u && u < mine + w) {
-            red[0] = b;
-            red[1] = mine;
+        const unsigned above = __ballot_sync(0xffffffffu, l.start + inc > l.at);
+        if (above) {
+            const int w = __ffs(above) - 1;
+            l.start += __shfl_sync(0xffffffffu, inc - mine, w);
+            l.b = b0 + w;
+            return l;
         }
-        __syncthreads();
-        const bool found = u < base + all;
-        if (found) {
-            b_out = (int)red[0];
-            start = red[1];
-        }
-        __syncthreads();
-        if (found) return;
-        base += all;
+        l.start += __shfl_sync(0xffffffffu, inc, 31);
     }
+    return l;
 }
 
-__device__ __forceinline__ Line line_of(const SeqAttn& p, int chunk, int ctas, int64_t* red) {
-    Line l;
-    l.total = total_units(p, chunk, red);
-    l.per = (l.total + ctas - 1) / ctas;
-    if (l.per < 1) l.per = 1;
-    return l;
+// Chunk and tile-and-head number of unit `rel` of a sequence.
+__device__ __forceinline__ void split_unit(int64_t rel, int chunks, int& c, int64_t& th) {
+    if ((rel >> 32) == 0) {
+        const uint32_t q = (uint32_t)rel / (uint32_t)chunks;
+        th = q;
+        c = (int)((uint32_t)rel - q * (uint32_t)chunks);
+    } else {
+        th = rel / chunks;
+        c = (int)(rel - th * chunks);
+    }
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -196,7 +195,7 @@ __device__ __forceinline__ int piece_at(int key, int ch) {
 }
 
 template <class E, int D, int F8, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p, int ctas) {
+__global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p, uint64_t ctas_mul) {
     using C = RowsCfg<D, F8>;
     constexpr int KS = C::KS, RB = C::RB, NS = C::NS;
     constexpr bool BF = std::is_same<E, BF16>::value && F8 == 0;    // MMA element type
@@ -204,7 +203,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
     constexpr int KK = D / 16;                                      // k-steps of Q.K^T
     constexpr int ND = D / 8;                                       // dim n-tiles
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int64_t red[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     unsigned char* ring = smem + warp * C::warp_bytes;
@@ -214,43 +212,40 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
     grid_dependency_wait();
     grid_launch_dependents();
 
-    const Line line = line_of(p, C::chunk, ctas, red);
-    int64_t u = (int64_t)blockIdx.x * line.per;
+    const Line line = line_at(p, C::chunk, ctas_mul, 0);
+    int64_t u = line.at;
     const int64_t u_end = min(line.total, u + line.per);
     if (u >= u_end) return;
-    int b;
-    int64_t seq_start;
-    locate(p, C::chunk, u, red, b, seq_start);
+    int b = line.b;
+    int64_t seq_start = line.start;
+    Seq sq = seq_of(p, b, C::chunk);
 
     float* ws_o = static_cast<float*>(p.ws);
     float* ws_ml = ws_o + (int64_t)2 * kMaxCtas * kRows * D;
 
-    while (u < u_end && b < p.kv.num_seqs) {
+    while (u < u_end) {
         // ---- the tile ----
-        const int2 nu = units_of(p, b, C::chunk);
-        const int64_t seq_units = (int64_t)nu.x * nu.y * p.kv.Hkv;
+        const int64_t seq_units = (int64_t)sq.tiles * sq.chunks * p.kv.Hkv;
         if (u >= seq_start + seq_units) {
             seq_start += seq_units;
-            ++b;
+            if (++b >= p.kv.num_seqs) return;
+            sq = seq_of(p, b, C::chunk);
             continue;
         }
-        const int64_t rel = u - seq_start;
-        const int c0 = (int)(rel % nu.y);
-        const int64_t th = rel / nu.y;
-        const int h = (int)(th % p.kv.Hkv), tile = (int)(th / p.kv.Hkv);
-        const int c1 = (int)min((int64_t)nu.y, c0 + (u_end - u));
-        const int2 qr = seq_rows(p.cu_q, b, p.tokens);
-        const int2 kr = seq_keys(p.kv, b);
-        const int n_q = qr.y - qr.x, kv_len = kr.y;
-        const int64_t rows = (int64_t)n_q * p.G;
-        const int64_t row_base = (int64_t)tile * kRows;
+        int c0;
+        int64_t th;
+        split_unit(u - seq_start, sq.chunks, c0, th);
+        const int tile = (int)((uint32_t)th / (uint32_t)p.kv.Hkv), h = (int)((uint32_t)th - (uint32_t)tile * p.kv.Hkv);
+        const int c1 = (int)min((int64_t)sq.chunks, c0 + (u_end - u));
+        const int n_q = sq.n_q, kv_len = sq.kv_len;
+        const int rows = n_q * p.G, row_base = tile * kRows;
         // number of visible keys of a row (rows past the tile: all, unused)
         auto limit = [&](int r) -> int {
             if (!p.causal || row_base + r >= rows) return kv_len;
-            const int i = (int)((row_base + r) / p.G);
+            const int i = (row_base + r) / p.G;
             return max(0, min(kv_len, i + kv_len - n_q + 1));
         };
-        const int last_row = (int)min((int64_t)kRows, rows - row_base) - 1;
+        const int last_row = min(kRows, rows - row_base) - 1;
         const int tile_lim = limit(last_row);
         const int lim0 = limit(g), lim1 = limit(g + 8);
 
@@ -276,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                     if constexpr (PAGED) {
                         ko = (int64_t)page * p.kv.s_page + (int64_t)(key % p.kv.page_size) * p.kv.s_tok;
                     } else {
-                        ko = (int64_t)(kr.x + key) * p.kv.s_tok;
-                        vo = (int64_t)(kr.x + key) * p.kv.sv_tok;
+                        ko = (int64_t)(sq.k_row + key) * p.kv.s_tok;
+                        vo = (int64_t)(sq.k_row + key) * p.kv.sv_tok;
                     }
                 }
                 const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
@@ -312,8 +307,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             const uint16_t* qb = static_cast<const uint16_t*>(p.q);
             auto q_row = [&](int r) -> const uint16_t* {
                 if (row_base + r >= rows) return nullptr;
-                const int64_t i = (row_base + r) / p.G;
-                return qb + (qr.x + i) * p.q_stride + (int64_t)(h * p.G + (row_base + r) % p.G) * D;
+                const int i = (row_base + r) / p.G;
+                return qb + (sq.q_row + i) * p.q_stride + (h * p.G + (row_base + r) - i * p.G) * D;
             };
             const uint16_t* q0 = q_row(g);
             const uint16_t* q1 = q_row(g + 8);
@@ -570,12 +565,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                     acc[4 * i + 3] += f * t.w;
                 }
             }
-            if (c0 == 0 && c1 == nu.y) {
+            if (c0 == 0 && c1 == sq.chunks) {
                 if (row_base + r < rows) {
                     const float vs = F8 && p.kv.scale_v ? p.kv.scale_v[h] : 1.f;
                     const bool none = L == 0.f;        // no visible key (a NaN sum is not that)
                     const float inv = none ? 0.f : vs / L;
-                    const int64_t row = (qr.x + (row_base + r) / p.G) * p.Hq + h * p.G + (row_base + r) % p.G;
+                    const int i = (row_base + r) / p.G;
+                    const int64_t row = (int64_t)(sq.q_row + i) * p.Hq + h * p.G + (row_base + r) - i * p.G;
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<typename E::T*>(p.out) + row * D + d0);
 #pragma unroll
                     for (int i = 0; i < W / 8; ++i) {
@@ -604,60 +600,79 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
 }
 
 // Block x joins the parts of the tile that border x (between the ranges of
-// CTAs x and x + 1) cuts first.
+// CTAs x and x + 1) cuts first: a warp per row, the parts' (m, sum) a lane
+// each, eight parts of O in flight.
 template <class E, int D, int F8>
-__global__ void __launch_bounds__(kThreads) attn_rows_merge(const SeqAttn p, int ctas) {
+__global__ void __launch_bounds__(kThreads) attn_rows_merge(const SeqAttn p, uint64_t ctas_mul) {
     constexpr int chunk = RowsCfg<D, F8>::chunk;
-    __shared__ int64_t red[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // The lists are older than the main kernel, which waited for them before
+    // this one could start; its parts are not.  (Every block waits, also those
+    // with nothing to do: this grid must not be over before the main one.)
+    const Line line = line_at(p, chunk, ctas_mul, 1);
+    int c = 0;
+    int64_t th = 0;
+    Seq sq{};
+    if (line.b < p.kv.num_seqs) {
+        sq = seq_of(p, line.b, chunk);
+        split_unit(line.at - line.start, sq.chunks, c, th);
+    }
     grid_dependency_wait();
-    const Line line = line_of(p, chunk, ctas, red);
-    const int64_t cut = (int64_t)(blockIdx.x + 1) * line.per;
-    if (cut >= line.total) return;
-    int b;
-    int64_t start;
-    locate(p, chunk, cut, red, b, start);
-    if (b >= p.kv.num_seqs) return;
-    const int2 nu = units_of(p, b, chunk);
-    const int64_t th = (cut - start) / nu.y;
-    const int64_t first = start + th * nu.y, end = first + nu.y;     // units of the tile
-    if (first == cut || first < cut - line.per) return;              // not cut here, or first cut earlier
-    const int h = (int)(th % p.kv.Hkv), tile = (int)(th / p.kv.Hkv);
-    const int2 qr = seq_rows(p.cu_q, b, p.tokens);
-    const int64_t rows = (int64_t)(qr.y - qr.x) * p.G, row_base = (int64_t)tile * kRows;
-    const int parts = (int)((end - cut + line.per - 1) / line.per) + 1;
+    if (c == 0 || c > line.per) return;                       // not cut here, or first cut earlier
+    const int tile = (int)((uint32_t)th / (uint32_t)p.kv.Hkv), h = (int)((uint32_t)th - (uint32_t)tile * p.kv.Hkv);
+    const int rows = sq.n_q * p.G, row_base = tile * kRows;
+    const int parts = 1 + (int)((uint32_t)(sq.chunks - c + (int)min(line.per, (int64_t)sq.chunks) - 1) /
+                                (uint32_t)min(line.per, (int64_t)sq.chunks));
     const float* ws_o = static_cast<const float*>(p.ws);
     const float* ws_ml = ws_o + (int64_t)2 * kMaxCtas * kRows * D;
     auto slot_of = [&](int i) { return i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i); };
 
-    constexpr int W = 4;                          // dims of a thread
-    constexpr int TR = D / W;                     // threads of a row
-    for (int r = threadIdx.x / TR; r < kRows; r += kThreads / TR) {
+    constexpr int W = D / 32;                     // dims of a lane
+    for (int r = warp; r < kRows; r += kWarps) {
         if (row_base + r >= rows) break;
-        const int d0 = (threadIdx.x % TR) * W;
-        float M = -INFINITY;
-        for (int i = 0; i < parts; ++i) M = fmaxf(M, ws_ml[((int64_t)slot_of(i) * kRows + r) * 2]);
-        float L = 0.f, acc[W] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const int64_t at = (int64_t)slot_of(i) * kRows + r;
-            const float2 x = *reinterpret_cast<const float2*>(ws_ml + at * 2);
-            const float f = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);
-            L += f * x.y;
-            const float4 t = *reinterpret_cast<const float4*>(ws_o + at * D + d0);
-            acc[0] += f * t.x;
-            acc[1] += f * t.y;
-            acc[2] += f * t.z;
-            acc[3] += f * t.w;
+        float M = -INFINITY, L = 0.f, acc[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[i] = 0.f;
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (i0 + lane < parts)
+                ml = *reinterpret_cast<const float2*>(ws_ml + ((int64_t)slot_of(i0 + lane) * kRows + r) * 2);
+            const float m_new = fmaxf(M, warp_max(ml.x));
+            const float old = rescale_factor(M, m_new), f = rescale_factor(ml.x, m_new);
+            M = m_new;
+            L = L * old + warp_sum(ml.y * f);
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] *= old;
+            const int n = min(32, parts - i0);
+            for (int j0 = 0; j0 < n; j0 += 8) {
+                float v[8][W];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float* src = ws_o + ((int64_t)slot_of(i0 + min(j0 + j, n - 1)) * kRows + r) * D + lane * W;
+#pragma unroll
+                    for (int i = 0; i < W; i += 2)
+                        *reinterpret_cast<float2*>(&v[j][i]) = *reinterpret_cast<const float2*>(src + i);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float g = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
+                    if (j0 + j < n) {
+#pragma unroll
+                        for (int i = 0; i < W; ++i) acc[i] += g * v[j][i];
+                    }
+                }
+            }
         }
         const bool none = L == 0.f;
         const float vs = F8 && p.kv.scale_v ? p.kv.scale_v[h] : 1.f;
         const float inv = none ? 0.f : vs / L;
-        const int64_t row = (qr.x + (row_base + r) / p.G) * p.Hq + h * p.G + (row_base + r) % p.G;
-        uint2 w;
-        w.x = none ? 0u : E::pack2(acc[0] * inv, acc[1] * inv);
-        w.y = none ? 0u : E::pack2(acc[2] * inv, acc[3] * inv);
-        *reinterpret_cast<uint2*>(static_cast<typename E::T*>(p.out) + row * D + d0) = w;
-        if (p.lse && d0 == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
+        const int i = (row_base + r) / p.G;
+        const int64_t row = (int64_t)(sq.q_row + i) * p.Hq + h * p.G + (row_base + r) - i * p.G;
+        typename E::T* out = static_cast<typename E::T*>(p.out) + row * D + lane * W;
+#pragma unroll
+        for (int k = 0; k < W; k += 2)
+            *reinterpret_cast<uint32_t*>(out + k) = none ? 0u : E::pack2(acc[k] * inv, acc[k + 1] * inv);
+        if (p.lse && lane == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
     }
 }
 
@@ -668,11 +683,17 @@ cudaError_t launch_rows_t(const SeqAttn& p, int num_sms, cudaStream_t stream) {
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::total);
     if (err != cudaSuccess) return err;
     const int ctas = 2 * num_sms < kMaxCtas ? 2 * num_sms : kMaxCtas;
-    err = launch_pdl(kern, dim3(ctas), dim3(kThreads), C::total, stream, p, ctas);
+    const uint64_t mul = ~uint64_t(0) / (uint64_t)ctas + 1;        // x / ctas = high word of x * mul
+    err = launch_pdl(kern, dim3(ctas), dim3(kThreads), C::total, stream, p, mul);
     if (err != cudaSuccess) return err;
     count_launches(1);
-    err = launch_pdl(attn_rows_merge<E, D, F8>, dim3(ctas - 1), dim3(kThreads), 0, stream, p, ctas);
-    if (err == cudaSuccess) count_launches(1);
+    // tiles of at most a shortest range are cut too where they lie across a
+    // border; only where no tile has a second chunk there is nothing to join
+    const int64_t longest = p.kv.page_table ? (int64_t)p.kv.max_pages * p.kv.page_size : p.kv.rows;
+    if (longest > C::chunk) {
+        err = launch_pdl(attn_rows_merge<E, D, F8>, dim3(ctas - 1), dim3(kThreads), 0, stream, p, mul);
+        if (err == cudaSuccess) count_launches(1);
+    }
     return err;
 }
 

@@ -1114,15 +1114,21 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p,
     const SeqAttn& a = p.a;
     const float kPShift = std::is_same<E, BF16>::value && a.kv.f8 == 0 ? 0.f : 7.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    grid_dependency_wait();
+    // The lists are older than the main kernel, which waited for them before
+    // this one could start; its parts are not.  (Every block waits, also those
+    // with nothing to do: this grid must not be over before the main one.)
     const Line line = line_at(p, ctas, 1);
-    if (line.b >= a.kv.num_seqs) return;
-    const Seq s = seq_of(p, line.b);
-    int j, h;
-    int64_t x;
-    find_item(p, s, line.at - line.start, j, h, x);
-    const int c = cost(p, s, j), N = (visible(p, s, (j + 1) * 2 * p.TR) + kStep - 1) / kStep;
-    const int first = cut(x, c, N);
+    int j = 0, h = 0, c = 1, N = 0, first = 0;
+    int64_t x = 0;
+    Seq s{};
+    if (line.b < a.kv.num_seqs) {
+        s = seq_of(p, line.b);
+        find_item(p, s, line.at - line.start, j, h, x);
+        c = cost(p, s, j);
+        N = (visible(p, s, (j + 1) * 2 * p.TR) + kStep - 1) / kStep;
+        first = cut(x, c, N);
+    }
+    grid_dependency_wait();
     // not cut here, or cut before
     if (first == 0 || first == N || cut(x - line.per, c, N) > 0) return;
     const int parts = 1 + (int)((c - x + line.per - 1) / line.per);
