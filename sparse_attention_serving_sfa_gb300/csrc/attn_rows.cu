@@ -10,9 +10,11 @@
 // warps' states merged at the end of the tile.
 //
 // Bound: HBM, each cached K / V row of a kv head read once per 16-row tile.
-// So the unit of scheduling is a chunk: all (sequence, tile, kv head, chunk)
-// units form one line, cut into equal ranges, one per CTA (two CTAs per SM),
-// whatever the mix of lengths.  A tile cut by a range border leaves its parts
+// All tiles lie on one line, each as long as its chunks plus a fixed charge
+// for what a tile costs besides, and the line is cut into equal ranges, one
+// per CTA (two CTAs per SM), whatever the mix of lengths.  A cut leaves at least
+// kMinPart chunks on both sides (a shorter tile stays whole: a part costs its
+// way through the workspace).  A tile cut by a range border leaves its parts
 // (O unnormalised, m, sum; fp32) in the workspace: a CTA has at most two, the
 // one it ends and the one it begins.  attn_rows_merge, launched behind with
 // programmatic dependent launch, joins them in order of their keys, so results do not
@@ -44,7 +46,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;            // rows of a tile
 constexpr int kMaxCtas = 320;        // ranges (the workspace's size goes by it)
-constexpr int kMinChunks = 4;        // shortest range: a part costs its way through the workspace
+constexpr int kCharge = 2;           // a tile's fixed cost, in chunks
+constexpr int kMinPart = 2;          // fewest chunks of a part
 constexpr float kRescale = 8.f;      // log2 growth of m that rescales O
 
 template <int D, int F8>
@@ -63,8 +66,8 @@ struct RowsCfg {
     static_assert(kRows * D * 4 <= warp_bytes, "a warp's O fits its ring");
 };
 
-// A sequence on the line: its tiles, kv heads and chunks are `tiles * Hkv *
-// chunks` units, the chunks of a tile side by side.
+// A sequence on the line: tiles * Hkv pieces of chunks + kCharge units, a tile's
+// kv heads side by side.
 struct Seq {
     int q_row, n_q, k_row, kv_len, tiles, chunks;
 };
@@ -95,7 +98,7 @@ __device__ __forceinline__ Line line_at(const SeqAttn& p, int chunk, uint64_t ct
     auto length = [&](int b) -> int64_t {
         if (b >= B) return 0;
         const Seq s = seq_of(p, b, chunk);
-        return (int64_t)s.tiles * s.chunks * p.kv.Hkv;
+        return (int64_t)s.tiles * (s.chunks + kCharge) * p.kv.Hkv;
     };
     Line l;
     const int64_t first = length(lane);
@@ -104,7 +107,7 @@ __device__ __forceinline__ Line line_at(const SeqAttn& p, int chunk, uint64_t ct
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     l.total = sum;
-    l.per = max((int64_t)__umul64hi((uint64_t)l.total, ctas_mul) + 1, (int64_t)kMinChunks);
+    l.per = (int64_t)__umul64hi((uint64_t)l.total, ctas_mul) + 1;
     l.at = ((int64_t)blockIdx.x + shift) * l.per;
     l.b = B;
     l.start = 0;
@@ -129,16 +132,23 @@ __device__ __forceinline__ Line line_at(const SeqAttn& p, int chunk, uint64_t ct
     return l;
 }
 
-// Chunk and tile-and-head number of unit `rel` of a sequence.
-__device__ __forceinline__ void split_unit(int64_t rel, int chunks, int& c, int64_t& th) {
+// Tile-and-head number of unit `rel` of a sequence, and the unit within it.
+__device__ __forceinline__ void split_unit(int64_t rel, int len, int& x, int64_t& th) {
     if ((rel >> 32) == 0) {
-        const uint32_t q = (uint32_t)rel / (uint32_t)chunks;
+        const uint32_t q = (uint32_t)rel / (uint32_t)len;
         th = q;
-        c = (int)((uint32_t)rel - q * (uint32_t)chunks);
+        x = (int)((uint32_t)rel - q * (uint32_t)len);
     } else {
-        th = rel / chunks;
-        c = (int)(rel - th * chunks);
+        th = rel / len;
+        x = (int)(rel - th * len);
     }
+}
+
+// Chunks of a tile of n before unit x of its n + kCharge.
+__device__ __forceinline__ int cut(int64_t x, int n) {
+    if (x >= n + kCharge) return n;
+    const int c = (int)min(x - kCharge / 2, (int64_t)n);
+    return c < kMinPart ? 0 : (c > n - kMinPart ? n : c);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -225,18 +235,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
 
     while (u < u_end) {
         // ---- the tile ----
-        const int64_t seq_units = (int64_t)sq.tiles * sq.chunks * p.kv.Hkv;
+        const int64_t seq_units = (int64_t)sq.tiles * (sq.chunks + kCharge) * p.kv.Hkv;
         if (u >= seq_start + seq_units) {
             seq_start += seq_units;
             if (++b >= p.kv.num_seqs) return;
             sq = seq_of(p, b, C::chunk);
             continue;
         }
-        int c0;
+        int x0;
         int64_t th;
-        split_unit(u - seq_start, sq.chunks, c0, th);
+        split_unit(u - seq_start, sq.chunks + kCharge, x0, th);
         const int tile = (int)((uint32_t)th / (uint32_t)p.kv.Hkv), h = (int)((uint32_t)th - (uint32_t)tile * p.kv.Hkv);
-        const int c1 = (int)min((int64_t)sq.chunks, c0 + (u_end - u));
+        const int64_t x1 = min((int64_t)sq.chunks + kCharge, x0 + (u_end - u));
+        const int c0 = cut(x0, sq.chunks), c1 = cut(x1, sq.chunks);
+        u += x1 - x0;
+        if (c0 == c1) continue;
         const int n_q = sq.n_q, kv_len = sq.kv_len;
         const int rows = n_q * p.G, row_base = tile * kRows;
         // number of visible keys of a row (rows past the tile: all, unused)
@@ -595,7 +608,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             }
         }
         __syncthreads();       // the rings are free for the next tile
-        u += c1 - c0;
     }
 }
 
@@ -610,19 +622,21 @@ __global__ void __launch_bounds__(kThreads) attn_rows_merge(const SeqAttn p, uin
     // this one could start; its parts are not.  (Every block waits, also those
     // with nothing to do: this grid must not be over before the main one.)
     const Line line = line_at(p, chunk, ctas_mul, 1);
-    int c = 0;
+    int x = 0;
     int64_t th = 0;
     Seq sq{};
     if (line.b < p.kv.num_seqs) {
         sq = seq_of(p, line.b, chunk);
-        split_unit(line.at - line.start, sq.chunks, c, th);
+        split_unit(line.at - line.start, sq.chunks + kCharge, x, th);
     }
     grid_dependency_wait();
-    if (c == 0 || c > line.per) return;                       // not cut here, or first cut earlier
+    const int n = sq.chunks, c = cut(x, n);
+    // not cut here, or first cut earlier
+    if (c == 0 || c == n || cut(x - line.per, n) > 0) return;
     const int tile = (int)((uint32_t)th / (uint32_t)p.kv.Hkv), h = (int)((uint32_t)th - (uint32_t)tile * p.kv.Hkv);
     const int rows = sq.n_q * p.G, row_base = tile * kRows;
-    const int parts = 1 + (int)((uint32_t)(sq.chunks - c + (int)min(line.per, (int64_t)sq.chunks) - 1) /
-                                (uint32_t)min(line.per, (int64_t)sq.chunks));
+    // one before this border and one behind each border that still cuts
+    const int parts = 2 + (int)((uint32_t)(n - kMinPart + kCharge / 2 - x) / (uint32_t)min(line.per, (int64_t)0x7fffffff));
     const float* ws_o = static_cast<const float*>(p.ws);
     const float* ws_ml = ws_o + (int64_t)2 * kMaxCtas * kRows * D;
     auto slot_of = [&](int i) { return i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i); };
@@ -643,12 +657,12 @@ __global__ void __launch_bounds__(kThreads) attn_rows_merge(const SeqAttn p, uin
             L = L * old + warp_sum(ml.y * f);
 #pragma unroll
             for (int i = 0; i < W; ++i) acc[i] *= old;
-            const int n = min(32, parts - i0);
-            for (int j0 = 0; j0 < n; j0 += 8) {
+            const int m = min(32, parts - i0);
+            for (int j0 = 0; j0 < m; j0 += 8) {
                 float v[8][W];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float* src = ws_o + ((int64_t)slot_of(i0 + min(j0 + j, n - 1)) * kRows + r) * D + lane * W;
+                    const float* src = ws_o + ((int64_t)slot_of(i0 + min(j0 + j, m - 1)) * kRows + r) * D + lane * W;
 #pragma unroll
                     for (int i = 0; i < W; i += 2)
                         *reinterpret_cast<float2*>(&v[j][i]) = *reinterpret_cast<const float2*>(src + i);
@@ -656,7 +670,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_merge(const SeqAttn p, uin
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float g = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
-                    if (j0 + j < n) {
+                    if (j0 + j < m) {
 #pragma unroll
                         for (int i = 0; i < W; ++i) acc[i] += g * v[j][i];
                     }
@@ -687,10 +701,9 @@ cudaError_t launch_rows_t(const SeqAttn& p, int num_sms, cudaStream_t stream) {
     err = launch_pdl(kern, dim3(ctas), dim3(kThreads), C::total, stream, p, mul);
     if (err != cudaSuccess) return err;
     count_launches(1);
-    // tiles of at most a shortest range are cut too where they lie across a
-    // border; only where no tile has a second chunk there is nothing to join
+    // tiles of fewer than 2 kMinPart chunks are never cut
     const int64_t longest = p.kv.page_table ? (int64_t)p.kv.max_pages * p.kv.page_size : p.kv.rows;
-    if (longest > C::chunk) {
+    if (longest > (int64_t)(2 * kMinPart - 1) * C::chunk) {
         err = launch_pdl(attn_rows_merge<E, D, F8>, dim3(ctas - 1), dim3(kThreads), 0, stream, p, mul);
         if (err == cudaSuccess) count_launches(1);
     }
