@@ -91,17 +91,20 @@ __device__ __forceinline__ Seq seq_of(const SeqAttn& p, int b, int chunk) {
 struct Line {
     int64_t total, per, at, start;
     int b;
+    Seq seq;
 };
 
 __device__ __forceinline__ Line line_at(const SeqAttn& p, int chunk, uint64_t ctas_mul, int shift) {
     const int lane = threadIdx.x & 31, B = p.kv.num_seqs;
+    Seq mine_seq{};
     auto length = [&](int b) -> int64_t {
         if (b >= B) return 0;
-        const Seq s = seq_of(p, b, chunk);
-        return (int64_t)s.tiles * (s.chunks + kCharge) * p.kv.Hkv;
+        mine_seq = seq_of(p, b, chunk);
+        return (int64_t)mine_seq.tiles * (mine_seq.chunks + kCharge) * p.kv.Hkv;
     };
     Line l;
     const int64_t first = length(lane);
+    const Seq first_seq = mine_seq;
     int64_t sum = first;
     for (int b = lane + 32; b < B; b += 32) sum += length(b);
 #pragma unroll
@@ -114,6 +117,7 @@ __device__ __forceinline__ Line line_at(const SeqAttn& p, int chunk, uint64_t ct
     if (l.at >= l.total) return l;
     for (int b0 = 0; b0 < B; b0 += 32) {
         const int64_t mine = b0 == 0 ? first : length(b0 + lane);
+        if (b0 == 0) mine_seq = first_seq;
         int64_t inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -125,6 +129,12 @@ __device__ __forceinline__ Line line_at(const SeqAttn& p, int chunk, uint64_t ct
             const int w = __ffs(above) - 1;
             l.start += __shfl_sync(0xffffffffu, inc - mine, w);
             l.b = b0 + w;
+            l.seq.q_row = __shfl_sync(0xffffffffu, mine_seq.q_row, w);
+            l.seq.n_q = __shfl_sync(0xffffffffu, mine_seq.n_q, w);
+            l.seq.k_row = __shfl_sync(0xffffffffu, mine_seq.k_row, w);
+            l.seq.kv_len = __shfl_sync(0xffffffffu, mine_seq.kv_len, w);
+            l.seq.tiles = __shfl_sync(0xffffffffu, mine_seq.tiles, w);
+            l.seq.chunks = __shfl_sync(0xffffffffu, mine_seq.chunks, w);
             return l;
         }
         l.start += __shfl_sync(0xffffffffu, inc, 31);
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
     if (u >= u_end) return;
     int b = line.b;
     int64_t seq_start = line.start;
-    Seq sq = seq_of(p, b, C::chunk);
+    Seq sq = line.seq;
 
     float* ws_o = static_cast<float*>(p.ws);
     float* ws_ml = ws_o + (int64_t)2 * kMaxCtas * kRows * D;
@@ -267,15 +277,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
         auto key0 = [&](int st) { return (c0 + st) * C::chunk + warp * KS; };
         const char* kb = static_cast<const char*>(p.kv.k) + h * p.kv.s_head * C::EB;
         const char* vb = static_cast<const char*>(p.kv.v) + h * (PAGED ? p.kv.s_head : p.kv.sv_head) * C::EB;
-        // page of this lane's key of step st, or -1 (looked up a step early)
+        // page of this lane's key of step st, or -1: looked up a step early, and
+        // left as loaded, so that nothing waits for the load
         auto page_of = [&](int st) -> int {
             const int key = key0(st) + lane;
             if (st >= nsteps || lane >= KS || key >= kv_len) return -1;
             if constexpr (!PAGED) return 0;
-            const int pg = p.kv.page_table[(int64_t)b * p.kv.max_pages + key / p.kv.page_size];
-            return (unsigned)pg < (unsigned)p.kv.num_pages ? pg : -1;
+            return p.kv.page_table[(int64_t)b * p.kv.max_pages + key / p.kv.page_size];
         };
         auto issue = [&](int st, int page) {
+            if (PAGED && (unsigned)page >= (unsigned)p.kv.num_pages) page = -1;
             if (st < nsteps) {
                 const int s = st % NS;
                 const int key = key0(st) + lane;
@@ -626,7 +637,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_merge(const SeqAttn p, uin
     int64_t th = 0;
     Seq sq{};
     if (line.b < p.kv.num_seqs) {
-        sq = seq_of(p, line.b, chunk);
+        sq = line.seq;
         split_unit(line.at - line.start, sq.chunks + kCharge, x, th);
     }
     grid_dependency_wait();

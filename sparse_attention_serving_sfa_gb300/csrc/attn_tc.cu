@@ -675,17 +675,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 ++items;
                 if (!tma) continue;
                 // page of this lane's box of a step, -1 if there is none to read
+                // (left as loaded, so that nothing waits for the load)
                 auto page_of = [&](int st) -> int {
                     const int key = (it.s0 + st) * kStep + lane * p.box;
                     if (st >= n || lane >= p.boxes || key >= it.kv_len) return -1;
-                    const int pg = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
-                    return (unsigned)pg < (unsigned)a.kv.num_pages ? pg : -1;
+                    return a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
                 };
                 int page = 0;
                 if constexpr (PAGED) page = page_of(0);
                 for (int st = 0; st < n && ok; ++st) {
                     const int key0 = (it.s0 + st) * kStep;
-                    const int pg = page;
+                    const int pg = (unsigned)page < (unsigned)a.kv.num_pages ? page : -1;
                     if constexpr (PAGED) page = page_of(st + 1);
                     for (int kv = 0; kv < 2 && ok; ++kv) {
                         // 16-bit tiles go into the ring, 8-bit ones into the staging tiles
@@ -912,29 +912,30 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
             }
             float m_used = -INFINITY, l = 0.f;
-            // boxes (runs of p.box keys that no page border cuts) of step st
-            // whose page is out of range: bit i of this lane = box lane + 32 i
+            // Pages of the boxes (runs of p.box keys that no page border cuts)
+            // lane + 32 i of step st, looked up a step ahead; left as loaded, so
+            // that nothing waits for the load.
             constexpr int kWords = L::gather ? 4 : 1;
-            auto page_bad = [&](int st) -> unsigned {
-                unsigned bits = 0;
+            int ahead[kWords];
+            auto look_up = [&](int st) {
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) {
                     const int box = lane + 32 * i, key = (it.s0 + st) * kStep + box * p.box;
-                    if (st >= n || box >= p.boxes || key >= it.kv_len) continue;
-                    const int pg = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
-                    if ((unsigned)pg >= (unsigned)a.kv.num_pages) bits |= 1u << i;
+                    ahead[i] = 0;
+                    if (st < n && box < p.boxes && key < it.kv_len)
+                        ahead[i] = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
                 }
-                return bits;
             };
-            unsigned bad = 0;
-            if constexpr (PAGED) bad = page_bad(0);
+            if constexpr (PAGED) look_up(0);
             for (int st = 0; st < n; ++st) {
-                unsigned bad_now = 0;
+                unsigned bad = 0;                // bit i: the page of box lane + 32 i is out of range
+                bool missing = false;
                 if constexpr (PAGED) {
-                    bad_now = bad;
-                    bad = page_bad(st + 1);
+#pragma unroll
+                    for (int i = 0; i < kWords; ++i) bad |= ((unsigned)ahead[i] >= (unsigned)a.kv.num_pages ? 1u : 0u) << i;
+                    missing = __any_sync(0xffffffffu, bad != 0);
+                    look_up(st + 1);
                 }
-                const bool missing = PAGED && __any_sync(0xffffffffu, bad_now != 0);
                 ok = mbar_wait(bar(B_S + t), steps & 1, err, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
@@ -965,7 +966,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         unsigned gone[4] = {0, 0, 0, 0};
 #pragma unroll
                         for (int i = 0; i < kWords; ++i) {
-                            const unsigned w = __ballot_sync(0xffffffffu, (bad_now >> i) & 1u);
+                            const unsigned w = __ballot_sync(0xffffffffu, (bad >> i) & 1u);
                             for (unsigned x = w; x; x &= x - 1) {
                                 const int key = (__ffs(x) - 1 + 32 * i) << p.box_shift;
 #pragma unroll
