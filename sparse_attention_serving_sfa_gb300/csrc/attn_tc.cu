@@ -65,7 +65,6 @@ constexpr int kMoveWarp = 12, kMovers = 128; // the movers: warps 12 to 15
 constexpr int kTmemCols = 512, kTileCols = 256, kOCol = 128;
 constexpr float kRescale = 8.0f;            // log2 units
 constexpr int kItemRows = 2 * kTileM;
-constexpr int kCharge = 256;                // an item's fixed cost, in keys
 constexpr int kMinShare = 3;                // fewest steps of a part
 constexpr int kMinRange = kStep;            // shortest range of a CTA, in keys
 constexpr int kMaxCtas = 160;               // ranges (the workspace's size goes by it)
@@ -129,6 +128,7 @@ struct TcParams {
     uint32_t unit_mul;                  // x / (2 TR) = x * unit_mul >> unit_shift for 0 <= x < 2^31
     int unit_shift;
     uint64_t ctas_mul;                  // x / ctas = high word of x * ctas_mul for x < 2^56
+    int charge;                         // an item's fixed cost, in keys
     int out32;                          // out is 32-byte aligned
     int box, box_shift, boxes;          // keys of a TMA box (and its log2), boxes of a step
     float* ws_o;                        // [2 * kMaxCtas][D / 4][kItemRows][4] parts
@@ -166,12 +166,12 @@ __device__ __forceinline__ int visible(const TcParams& p, const Seq& s, int tok_
 }
 
 __device__ __forceinline__ int cost(const TcParams& p, const Seq& s, int j) {
-    return visible(p, s, (j + 1) * 2 * p.TR) + kCharge;
+    return visible(p, s, (j + 1) * 2 * p.TR) + p.charge;
 }
 
 // Cost of one kv head's tiles before tile j.
 __device__ __forceinline__ int64_t cost_before(const TcParams& p, const Seq& s, int j) {
-    int64_t sum = (int64_t)j * kCharge;
+    int64_t sum = (int64_t)j * p.charge;
     if (!p.a.causal) return sum + (int64_t)j * s.kv_len;
     const int64_t U = 2 * p.TR, off = s.kv_len - s.n_q;
     int64_t full = j;                                  // tiles of U tokens among them
@@ -1295,6 +1295,10 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
     p.unit_shift = 31 + up;
     p.unit_mul = (uint32_t)((((uint64_t)1 << p.unit_shift) + unit - 1) / unit);
     p.ctas_mul = ~uint64_t(0) / (uint64_t)(num_sms < kMaxCtas ? num_sms : kMaxCtas) + 1;
+    // measured on CTAs of many short items beside CTAs of few long ones: about
+    // 8,000 cycles an item where a step takes 2,900 (64-dim: 5,000 and 2,400;
+    // 8-bit: 15,000 and 4,000), and half a step that rounding up adds
+    p.charge = a.kv.f8 ? 512 : (a.kv.D == 128 ? 448 : 320);
     p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.ws_o = static_cast<float*>(a.ws);
     p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;
