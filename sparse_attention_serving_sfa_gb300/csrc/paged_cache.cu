@@ -9,16 +9,22 @@
 // of V).  A thread moves 16 consecutive elements of a head's row of K and of V
 // (two 16-byte loads each, and one 16-byte store each for 8-bit codes), so a
 // warp covers 512 elements of a token and the loads of K and V are in flight
-// together.  The sequence of a warp's first token is found by a 32-way search
+// together.  (Two pieces a thread, of one token or of several, and pieces of 8
+// elements measured slower on most calls: 47.4 -> 50.6 and 54.9 us for 261 MB
+// read back.)  The sequence of a warp's first token is found by a 32-way search
 // of cu (one load per factor of 32 in the number of sequences), then each lane
 // walks to its own token's.
 //
-// Rounding to codes: the quotient is rounded to fp32 first.  Only a quotient
-// whose low 19 bits are then zero can sit on a border between two codes
-// (formats with at most 3 fraction bits); there the exact remainder
-// x - q * scale (one fma) tells on which side the true quotient lies, and q is
-// moved off the border by one unit in that direction, so the code is that of
-// the exact quotient.
+// Rounding to codes: x times the scale's rounded reciprocal is within 2 units
+// in the last place of the quotient.  A border between two codes has 19 zero
+// bits at the end (formats of at most 3 fraction bits), so a product whose
+// last 19 bits are further than that from zero has the quotient's code.
+// Where one of a thread's 16 is not, they are divided: the quotient rounded
+// to fp32, and if that has 19 zeros, the exact remainder x - q * scale (one
+// fma) tells on which side the true quotient lies, and q moves off the border
+// by one unit in that direction.  So the code is always that of the exact
+// quotient, for 5 instructions an element instead of about 18 (which took
+// longer than the memory did).  A power of two divides exactly.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -70,15 +76,32 @@ __device__ __forceinline__ float quotient(float x, float s) {
 }
 
 template <class E, bool E5>
-__device__ __forceinline__ uint4 encode16(const uint4 (&x)[2], float s) {
+__device__ __forceinline__ uint4 encode16(const uint4 (&x)[2], float s, float inv) {
     const uint32_t in[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    float q[16];
+    const bool normal = inv >= 1.1754944e-38f && inv < INFINITY;
+    bool near = !normal;                     // (a reciprocal out of the normal range is less exact)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 a = E::unpack2(in[i]);
+        q[2 * i] = a.x * inv;
+        q[2 * i + 1] = a.y * inv;
+        near |= ((__float_as_uint(q[2 * i]) + 2u) & 0x7ffffu) <= 4u;
+        near |= ((__float_as_uint(q[2 * i + 1]) + 2u) & 0x7ffffu) <= 4u;
+    }
+    // an exact reciprocal (a power of two, normal) gives exact quotients
+    if (near && ((__float_as_uint(s) & 0x7fffffu) != 0u || !normal)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 a = E::unpack2(in[i]);
+            q[2 * i] = quotient(a.x, s);
+            q[2 * i + 1] = quotient(a.y, s);
+        }
+    }
     uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 a = E::unpack2(in[2 * i]), b = E::unpack2(in[2 * i + 1]);
-        o[i] = f8_pack2<E5>(quotient(a.x, s), quotient(a.y, s)) |
-               (f8_pack2<E5>(quotient(b.x, s), quotient(b.y, s)) << 16);
-    }
+    for (int i = 0; i < 4; ++i)
+        o[i] = f8_pack2<E5>(q[4 * i], q[4 * i + 1]) | (f8_pack2<E5>(q[4 * i + 2], q[4 * i + 3]) << 16);
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -108,13 +131,28 @@ paged_move_kernel(const SeqKV kv, const void* src_k, const void* src_v, void* ds
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t first = id - (threadIdx.x & 31);
     if (first >= total) return;
-    const int t0 = (int)(first / per_token);
-    int b = find_seq(cu, kv.num_seqs, t0);
-    if (id >= total) return;
-    const int t = (int)(id / per_token), piece = (int)(id % per_token);
+    // (32-bit arithmetic where it reaches: a 64-bit division took longer than the search)
+    const bool small = (total >> 32) == 0;
+    auto token_of = [&](int64_t i) { return small ? (int)((uint32_t)i / (uint32_t)per_token) : (int)(i / per_token); };
+    const int t = id < total ? token_of(id) : tokens;
+    const int piece = (int)(id - (int64_t)t * per_token);
+    const int h = (int)((uint32_t)piece / (uint32_t)per_head), d = (piece - h * per_head) * kVec;
+    uint4 k[2] = {}, v[2] = {};
+    if (!READ && t < tokens) {
+        // new rows are on their way while their place is looked up
+        const uint4* pk = reinterpret_cast<const uint4*>(static_cast<const char*>(src_k) +
+                                                         ((int64_t)t * k_stride + h * kv.D + d) * 2);
+        const uint4* pv = reinterpret_cast<const uint4*>(static_cast<const char*>(src_v) +
+                                                         ((int64_t)t * v_stride + h * kv.D + d) * 2);
+        k[0] = __ldcs(pk);
+        k[1] = __ldcs(pk + 1);
+        v[0] = __ldcs(pv);
+        v[1] = __ldcs(pv + 1);
+    }
+    int b = find_seq(cu, kv.num_seqs, token_of(first));
+    if (t >= tokens) return;
     while (b < kv.num_seqs && cu[b + 1] <= t) ++b;
     const int64_t at = place_of(kv, cu, b, t);
-    const int h = piece / per_head, d = (piece % per_head) * kVec;
     const int64_t cell = at + h * kv.s_head + d;
     const float sk = F8 && kv.scale_k ? kv.scale_k[h] : 1.f;
     const float sv = F8 && kv.scale_v ? kv.scale_v[h] : 1.f;
@@ -122,7 +160,6 @@ paged_move_kernel(const SeqKV kv, const void* src_k, const void* src_v, void* ds
     if constexpr (READ) {
         // rows without a place read as zero; rows past the last sequence are left alone
         if (b >= kv.num_seqs || t < cu[b]) return;
-        uint4 k[2] = {}, v[2] = {};
         if (at >= 0) {
             const uint4* pk = reinterpret_cast<const uint4*>(static_cast<const char*>(src_k) + cell * EB);
             const uint4* pv = reinterpret_cast<const uint4*>(static_cast<const char*>(src_v) + cell * EB);
@@ -141,16 +178,11 @@ paged_move_kernel(const SeqKV kv, const void* src_k, const void* src_v, void* ds
         ov[0] = v[0]; ov[1] = v[1];
     } else {
         if (at < 0) return;
-        const uint4* pk = reinterpret_cast<const uint4*>(static_cast<const char*>(src_k) +
-                                                         ((int64_t)t * k_stride + h * kv.D + d) * 2);
-        const uint4* pv = reinterpret_cast<const uint4*>(static_cast<const char*>(src_v) +
-                                                         ((int64_t)t * v_stride + h * kv.D + d) * 2);
-        const uint4 k[2] = {__ldcs(pk), __ldcs(pk + 1)}, v[2] = {__ldcs(pv), __ldcs(pv + 1)};
         uint4* ok = reinterpret_cast<uint4*>(static_cast<char*>(dst_k) + cell * EB);
         uint4* ov = reinterpret_cast<uint4*>(static_cast<char*>(dst_v) + cell * EB);
         if constexpr (F8) {
-            *ok = encode16<E, F8 == 2>(k, sk);
-            *ov = encode16<E, F8 == 2>(v, sv);
+            *ok = encode16<E, F8 == 2>(k, sk, __frcp_rn(sk));
+            *ov = encode16<E, F8 == 2>(v, sv, __frcp_rn(sv));
         } else {
             ok[0] = k[0]; ok[1] = k[1];
             ov[0] = v[0]; ov[1] = v[1];

@@ -60,8 +60,9 @@ def test_append(q_lens, kv_lens, heads, dim, page, dtype, cache, layout):
         assert torch.equal(raw(got), want)          # every other place as it was
 
 
+@pytest.mark.parametrize("extreme", [False, True])
 @pytest.mark.parametrize("cache", ["e4m3", "e5m2"])
-def test_append_rounds_the_exact_quotient(cache):
+def test_append_rounds_the_exact_quotient(cache, extreme):
     """Every fp16 value, over scales that put many of them on borders between
     two codes, and over one where the quotient rounded to fp32 sits on a border
     that the exact one does not."""
@@ -71,6 +72,8 @@ def test_append_rounds_the_exact_quotient(cache):
     scales = torch.tensor([1.0, 0.25, 3.0, 1 / 3, float(near),
                            float(torch.nextafter(near, torch.tensor(2.0))),
                            float(torch.nextafter(near, torch.tensor(0.0))), 0.7])
+    if extreme:
+        scales = torch.tensor([1e-38, 3e-39, 1e-30, 2.0 ** -120, 1e30, 1.5e38, 3e38, 2.0 ** 127])
     x = every.view(-1, 1, 128).expand(-1, 8, -1).contiguous()      # 512 tokens, 8 heads
     T, H, D = x.shape
     pool = torch.zeros(T // 16, 16, H, D, dtype=P.TORCH[cache], device="cuda")
