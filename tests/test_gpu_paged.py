@@ -85,7 +85,7 @@ def test_append_rounds_the_exact_quotient(cache, extreme):
                      scale_v=scales.flip(0).cuda())
     for got, s in ((pool, scales), (pool2, scales.flip(0))):
         got = raw(got).view(T, H, D)
-        want = P.nearest_code(torch.nan_to_num(x.double(), nan=0.0, posinf=1e30, neginf=-1e30) /
+        want = P.nearest_code(torch.nan_to_num(x.double(), nan=0.0, posinf=math.inf, neginf=-math.inf) /
                               s.double().view(1, -1, 1), cache)
         nan = torch.isnan(x)
         assert torch.equal(got[~nan], want[~nan])
