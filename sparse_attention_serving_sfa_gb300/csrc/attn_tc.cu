@@ -198,17 +198,20 @@ __device__ __forceinline__ int cut(int64_t x, int c, int N) {
 struct Line {
     int64_t total, per, at, start;
     int b;
+    Seq seq;
 };
 
 __device__ __forceinline__ Line line_at(const TcParams& p, int ctas, int shift) {
     const int lane = threadIdx.x & 31, B = p.a.kv.num_seqs;
+    Seq mine_seq{};
     auto length = [&](int b) -> int64_t {
         if (b >= B) return 0;
-        const Seq s = seq_of(p, b);
-        return cost_before(p, s, s.tiles) * p.a.kv.Hkv;
+        mine_seq = seq_of(p, b);
+        return cost_before(p, mine_seq, mine_seq.tiles) * p.a.kv.Hkv;
     };
     Line l;
     const int64_t first = length(lane);
+    const Seq first_seq = mine_seq;
     int64_t sum = first;
     for (int b = lane + 32; b < B; b += 32) sum += length(b);
 #pragma unroll
@@ -221,6 +224,7 @@ __device__ __forceinline__ Line line_at(const TcParams& p, int ctas, int shift) 
     if (l.at >= l.total) return l;
     for (int b0 = 0; b0 < B; b0 += 32) {
         const int64_t mine = b0 == 0 ? first : length(b0 + lane);
+        if (b0 == 0) mine_seq = first_seq;
         int64_t inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -232,6 +236,11 @@ __device__ __forceinline__ Line line_at(const TcParams& p, int ctas, int shift) 
             const int w = __ffs(above) - 1;
             l.start += __shfl_sync(0xffffffffu, inc - mine, w);
             l.b = b0 + w;
+            l.seq.q_row = __shfl_sync(0xffffffffu, mine_seq.q_row, w);
+            l.seq.n_q = __shfl_sync(0xffffffffu, mine_seq.n_q, w);
+            l.seq.k_row = __shfl_sync(0xffffffffu, mine_seq.k_row, w);
+            l.seq.kv_len = __shfl_sync(0xffffffffu, mine_seq.kv_len, w);
+            l.seq.tiles = __shfl_sync(0xffffffffu, mine_seq.tiles, w);
             return l;
         }
         l.start += __shfl_sync(0xffffffffu, inc, 31);
@@ -279,10 +288,13 @@ struct Walk {
     int b, j, h;
     Seq s;
 
-    __device__ __forceinline__ Walk(const TcParams& p, const Line& l) : left(0), x(0), b(l.b), j(0), h(0) {
+    __device__ __forceinline__ void begin(const TcParams& p, const Line& l) {
+        left = x = 0;
+        b = l.b;
+        j = h = 0;
         if (b >= p.a.kv.num_seqs) return;
         left = min(l.per, l.total - l.at);
-        s = seq_of(p, b);
+        s = l.seq;
         find_item(p, s, l.at - l.start, j, h, x);
     }
 
@@ -623,6 +635,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         fence_barrier_init();
     }
     if (warp == 0) tmem_alloc(sbase + L::tmem_slot, kTmemCols);
+    Item next_item;                     // the loader: found while the others set up
+    bool more = false;
+    Walk walk;
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            tma_prefetch_map(&mq);
+            tma_prefetch_map(&mk);
+            tma_prefetch_map(&mv);
+        }
+        grid_dependency_wait();
+        walk.begin(p, line_at(p, ctas, 0));
+        more = walk.next(p, next_item);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -636,25 +661,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             if constexpr (L::gather) move_rows<D, SRC>(p, smem, sbase, tid - kMoveWarp * 32);
         } else if (warp == kLoadWarp) {
             // ============================ loader ============================
-            if (lane == 0) {
-                tma_prefetch_map(&mq);
-                tma_prefetch_map(&mk);
-                tma_prefetch_map(&mv);
-            }
-            Walk walk(p, line_at(p, ctas, 0));
-            Item it;
             int number = 0;
             int items = 0, loads = 0, tails = 0;   // items with keys, tiles loaded, tiles cleared
             int qs[2] = {0, 0};                    // Q tiles loaded
             const bool tma = !L::gather || (L::f8 && p.box >= 16);
             bool ok = true;
-            while (ok) {
-                const bool more = walk.next(p, it);
-                if (!more) it.b = -1;
-                if (lane == 0) ok = put_item<L>(smem, sbase, number, it, err, abort_flag);
+            for (;; more = walk.next(p, next_item)) {
+                if (!more) next_item.b = -1;
+                if (lane == 0) ok = put_item<L>(smem, sbase, number, next_item, err, abort_flag);
                 ++number;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!more || !ok) break;
+                const Item& it = next_item;
                 const int n = max(it.n[0], it.n[1]);
                 if (n == 0) continue;
                 if constexpr (!kScaledQ) {
@@ -735,6 +753,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         ++loads;
                     }
                 }
+                if (!ok) break;
             }
             if (!ok && lane == 0) {
                 // a wait gave up: let the copies in flight land (bounded) before leaving
@@ -1123,7 +1142,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p,
     int64_t x = 0;
     Seq s{};
     if (line.b < a.kv.num_seqs) {
-        s = seq_of(p, line.b);
+        s = line.seq;
         find_item(p, s, line.at - line.start, j, h, x);
         c = cost(p, s, j);
         N = (visible(p, s, (j + 1) * 2 * p.TR) + kStep - 1) / kStep;
