@@ -65,7 +65,7 @@ constexpr int kMoveWarp = 12, kMovers = 128; // the movers: warps 12 to 15
 constexpr int kTmemCols = 512, kTileCols = 256, kOCol = 128;
 constexpr float kRescale = 8.0f;            // log2 units
 constexpr int kItemRows = 2 * kTileM;
-constexpr int kMinShare = 3;                // fewest steps of a part
+constexpr int kMinShare = 2;                // fewest steps of a part
 constexpr int kMinRange = kStep;            // shortest range of a CTA, in keys
 constexpr int kMaxCtas = 160;               // ranges (the workspace's size goes by it)
 
@@ -1314,10 +1314,11 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
     p.unit_shift = 31 + up;
     p.unit_mul = (uint32_t)((((uint64_t)1 << p.unit_shift) + unit - 1) / unit);
     p.ctas_mul = ~uint64_t(0) / (uint64_t)(num_sms < kMaxCtas ? num_sms : kMaxCtas) + 1;
-    // measured on CTAs of many short items beside CTAs of few long ones: about
-    // 8,000 cycles an item where a step takes 2,900 (64-dim: 5,000 and 2,400;
-    // 8-bit: 15,000 and 4,000), and half a step that rounding up adds
-    p.charge = a.kv.f8 ? 512 : (a.kv.D == 128 ? 448 : 320);
+    // Measured (320 / 448 / 576 / 768): chunks of 200 to 1,024 tokens over 16-bit
+    // pages 236 / 223 / 215 / 219 us; 64-dim prompts of up to 700 tokens (192 / 320 /
+    // 448) 38.4 / 36.2 / 36.2 us; chunks over E4M3 pages (384 / 512 / 640) 454 / 448 /
+    // 445 us.  A step of 128 keys takes about 2,700 cycles (64-dim 2,400, 8-bit 3,900).
+    p.charge = a.kv.f8 ? 640 : (a.kv.D == 128 ? 576 : 448);
     p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.ws_o = static_cast<float*>(a.ws);
     p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;
