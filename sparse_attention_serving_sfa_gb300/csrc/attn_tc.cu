@@ -125,8 +125,8 @@ enum {
 struct TcParams {
     SeqAttn a;
     int TR, hnd;
-    uint32_t unit_mul;                  // x / (2 TR) = x * unit_mul >> unit_shift for 0 <= x < 2^31
-    int unit_shift;
+    uint32_t unit_mul, page_mul;        // x / (2 TR) = x * unit_mul >> unit_shift for 0 <= x < 2^31,
+    int unit_shift, page_shift;         // x / page_size likewise
     uint64_t ctas_mul;                  // x / ctas = high word of x * ctas_mul for x < 2^56
     int charge;                         // an item's fixed cost, in keys
     int out32;                          // out is 32-byte aligned
@@ -145,6 +145,11 @@ struct Seq {
 // x / (2 TR)
 __device__ __forceinline__ int units(const TcParams& p, int x) {
     return (int)(((uint64_t)(uint32_t)x * p.unit_mul) >> p.unit_shift);
+}
+
+// x / page_size
+__device__ __forceinline__ int page_slot(const TcParams& p, int x) {
+    return (int)(((uint64_t)(uint32_t)x * p.page_mul) >> p.page_shift);
 }
 
 __device__ __forceinline__ Seq seq_of(const TcParams& p, int b) {
@@ -476,13 +481,13 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
         int ahead;
         auto look_up = [&](int st) {
             const int key = (s0 + st) * kStep + x;
-            ahead = st < n && key < kv_len ? table[key / a.kv.page_size] : -1;
+            ahead = st < n && key < kv_len ? table[page_slot(p, key)] : -1;
         };
         // Row numbers (in units of D elements) of step st's keys.  (The table
         // of a step is written over two steps later: by then every thread
         // has passed the barrier of the step between, after its last read.)
         auto find_rows = [&](int st) -> bool {
-            const int place = ((s0 + st) * kStep + x) % a.kv.page_size;
+            const int key = (s0 + st) * kStep + x, place = key - page_slot(p, key) * a.kv.page_size;
             const uint32_t pg = (uint32_t)ahead;
             rows[(st & 1) * kStep + x] = pg >= (uint32_t)a.kv.num_pages ? 0xffffffffu
                                          : p.hnd ? (pg * a.kv.Hkv + h) * a.kv.page_size + place
@@ -697,7 +702,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 auto page_of = [&](int st) -> int {
                     const int key = (it.s0 + st) * kStep + lane * p.box;
                     if (st >= n || lane >= p.boxes || key >= it.kv_len) return -1;
-                    return a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
+                    return a.kv.page_table[(int64_t)it.b * a.kv.max_pages + page_slot(p, key)];
                 };
                 int page = 0;
                 if constexpr (PAGED) page = page_of(0);
@@ -724,7 +729,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                             if (lane < p.boxes) {
                                 // a box without a page reads page num_pages: outside, zeros
                                 const int at = pg < 0 ? a.kv.num_pages : pg;
-                                const int place = pg < 0 ? 0 : (key0 + lane * p.box) % a.kv.page_size;
+                                const int key = key0 + lane * p.box;
+                                const int place = pg < 0 ? 0 : key - page_slot(p, key) * a.kv.page_size;
                                 constexpr int kRow = L::gather ? D : 128;          // bytes of a box's row
                                 for (int pn = 0; pn < (L::gather ? 1 : L::panels); ++pn) {
                                     const uint32_t to = dst + pn * L::panel + lane * p.box * kRow;
@@ -941,8 +947,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 for (int i = 0; i < kWords; ++i) {
                     const int box = lane + 32 * i, key = (it.s0 + st) * kStep + box * p.box;
                     ahead[i] = 0;
+                    if (i > 0 && 32 * i >= p.boxes) continue;          // (the same for all lanes)
                     if (st < n && box < p.boxes && key < it.kv_len)
-                        ahead[i] = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + key / a.kv.page_size];
+                        ahead[i] = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + page_slot(p, key)];
                 }
             };
             if constexpr (PAGED) look_up(0);
@@ -1308,11 +1315,14 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
     p.boxes = kStep / p.box;
     while ((1 << p.box_shift) < p.box) ++p.box_shift;
     // for x < 2^31: multiplier rounded up at 2^(31 + ceil(log2 d))
-    const uint32_t unit = 2 * p.TR;
-    int up = 0;
-    while ((1u << up) < unit) ++up;
-    p.unit_shift = 31 + up;
-    p.unit_mul = (uint32_t)((((uint64_t)1 << p.unit_shift) + unit - 1) / unit);
+    auto divide_by = [](uint32_t d, uint32_t& mul, int& shift) {
+        int up = 0;
+        while (((uint64_t)1 << up) < d) ++up;
+        shift = 31 + up;
+        mul = (uint32_t)((((uint64_t)1 << shift) + d - 1) / d);
+    };
+    divide_by(2 * p.TR, p.unit_mul, p.unit_shift);
+    if (a.kv.page_table) divide_by(a.kv.page_size, p.page_mul, p.page_shift);
     p.ctas_mul = ~uint64_t(0) / (uint64_t)(num_sms < kMaxCtas ? num_sms : kMaxCtas) + 1;
     // Measured (320 / 448 / 576 / 768): chunks of 200 to 1,024 tokens over 16-bit
     // pages 236 / 223 / 215 / 219 us; 64-dim prompts of up to 700 tokens (192 / 320 /
