@@ -133,6 +133,15 @@ struct TcParams {
     int box, box_shift, boxes;          // keys of a TMA box (and its log2), boxes of a step
     float* ws_o;                        // [2 * kMaxCtas][D / 4][kItemRows][4] parts
     float* ws_ml;                       // [2 * kMaxCtas][kItemRows][2] (m, sum)
+    struct CutItem* ws_cut;             // [kMaxCtas] the item that each range cuts first
+};
+
+// An item whose first part a range holds: what attn_tc_merge has to join.
+// Written by every CTA, cut or not.
+struct CutItem {
+    int N, c;                           // steps (0: none) and length of the item
+    int h, q_row, n_q, tok0;            // as in Item
+    int64_t x, per;                     // end of the range within the item, length of a range
 };
 
 // A sequence on the line.  Tile j holds tokens [j U, (j + 1) U), U = 2 TR, and
@@ -197,16 +206,16 @@ __device__ __forceinline__ int cut(int64_t x, int c, int N) {
     return st < kMinShare ? 0 : (st > N - kMinShare ? N : st);
 }
 
-// The line: its length, the length of a range, the point range (blockIdx.x +
-// shift) begins at, and the sequence (and its first point) that holds it.  One
-// warp; every lane gets the answer.
+// The line: its length, the length of a range, the point this CTA's range
+// begins at, and the sequence (and its first point) that holds it.  One warp;
+// every lane gets the answer.
 struct Line {
     int64_t total, per, at, start;
     int b;
     Seq seq;
 };
 
-__device__ __forceinline__ Line line_at(const TcParams& p, int ctas, int shift) {
+__device__ __forceinline__ Line line_at(const TcParams& p) {
     const int lane = threadIdx.x & 31, B = p.a.kv.num_seqs;
     Seq mine_seq{};
     auto length = [&](int b) -> int64_t {
@@ -223,7 +232,7 @@ __device__ __forceinline__ Line line_at(const TcParams& p, int ctas, int shift) 
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     l.total = sum;
     l.per = max((int64_t)__umul64hi((uint64_t)l.total, p.ctas_mul) + 1, (int64_t)kMinRange);
-    l.at = ((int64_t)blockIdx.x + shift) * l.per;
+    l.at = (int64_t)blockIdx.x * l.per;
     l.b = B;
     l.start = 0;
     if (l.at >= l.total) return l;
@@ -288,13 +297,14 @@ static_assert(sizeof(Item) == 48, "TcSmem::items");
 // Walks the shares of this CTA's range: the producer does, and hands each item
 // to the MMA thread and the softmax through two slots in shared memory.
 struct Walk {
-    int64_t left;               // of the range
+    int64_t left, per;          // of the range: what is left, its length
     int64_t x;                  // point within the item (j, h)
     int b, j, h;
     Seq s;
 
     __device__ __forceinline__ void begin(const TcParams& p, const Line& l) {
         left = x = 0;
+        per = l.per;
         b = l.b;
         j = h = 0;
         if (b >= p.a.kv.num_seqs) return;
@@ -330,6 +340,8 @@ struct Walk {
             const int v0 = two ? visible(p, s, it.tok0 + p.TR) : v1;
             it.n[0] = max(0, min((v0 + kStep - 1) / kStep, s1) - s0);
             it.n[1] = two ? s1 - s0 : 0;
+            if (s0 == 0 && s1 > 0 && s1 < N && (threadIdx.x & 31) == 0)
+                p.ws_cut[blockIdx.x] = CutItem{N, c, h, s.q_row, s.n_q, j * U, x1, per};
             left -= x1 - x0;
             x = x1;
             if (x1 == c) {
@@ -593,7 +605,7 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
 template <class E, int D, int SRC>
 __global__ void __launch_bounds__(TcBlock<SRC>::threads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-               const __grid_constant__ CUtensorMap mv, const TcParams p, int ctas) {
+               const __grid_constant__ CUtensorMap mv, const TcParams p) {
     using L = TcSmem<D, SRC>;
     constexpr bool PAGED = SRC != SRC_PACKED, F8 = L::f8;
     constexpr bool kScaledQ = F8 && std::is_same<E, BF16>::value;    // q's rows go to fp16
@@ -650,7 +662,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             tma_prefetch_map(&mv);
         }
         grid_dependency_wait();
-        walk.begin(p, line_at(p, ctas, 0));
+        walk.begin(p, line_at(p));
+        if (lane == 0) p.ws_cut[blockIdx.x].N = 0;
         more = walk.next(p, next_item);
     }
     tc_fence_before();
@@ -1127,48 +1140,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     }
 }
 
-// Block (x, y) joins rows 32 y .. 32 y + 31 of the parts of the item that
-// border x (between the ranges of CTAs x and x + 1) cuts first: lane = row,
-// each warp some of the dims; the result crosses over in shared memory to be
-// written row by row.
+// Block (x, y) joins rows 32 y .. 32 y + 31 of the parts of the item that range
+// x cuts first: lane = row, each warp some of the dims; the result crosses over
+// in shared memory to be written row by row.  (Finding the cuts here again took
+// longer than joining: 16 us where nothing was cut.)
 constexpr int kMergeThreads = 256;
 
 template <class E, int D>
-__global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p) {
     constexpr int kWarps = kMergeThreads / 32;
     constexpr int Q = D / 4 / kWarps;                    // 4-dim groups of a warp
     __shared__ uint2 turn[32][D / 4 + 1];
     const SeqAttn& a = p.a;
     const float kPShift = std::is_same<E, BF16>::value && a.kv.f8 == 0 ? 0.f : 7.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // The lists are older than the main kernel, which waited for them before
-    // this one could start; its parts are not.  (Every block waits, also those
-    // with nothing to do: this grid must not be over before the main one.)
-    const Line line = line_at(p, ctas, 1);
-    int j = 0, h = 0, c = 1, N = 0, first = 0;
-    int64_t x = 0;
-    Seq s{};
-    if (line.b < a.kv.num_seqs) {
-        s = line.seq;
-        find_item(p, s, line.at - line.start, j, h, x);
-        c = cost(p, s, j);
-        N = (visible(p, s, (j + 1) * 2 * p.TR) + kStep - 1) / kStep;
-        first = cut(x, c, N);
-    }
     grid_dependency_wait();
-    // not cut here, or cut before
-    if (first == 0 || first == N || cut(x - line.per, c, N) > 0) return;
-    const int parts = 1 + (int)((c - x + line.per - 1) / line.per);
-    const int r = blockIdx.y * 32 + lane, rr = r % kTileM, tok = j * 2 * p.TR + r / kTileM * p.TR + rr / a.G;
-    const bool valid = rr < p.TR * a.G && tok < s.n_q;
+    const CutItem it = p.ws_cut[blockIdx.x];
+    const int N = it.N, h = it.h;
+    if (N == 0) return;
+    const int r = blockIdx.y * 32 + lane, rr = r % kTileM, tok = it.tok0 + r / kTileM * p.TR + rr / a.G;
+    const bool valid = rr < p.TR * a.G && tok < it.n_q;
     if (!__any_sync(0xffffffffu, valid)) return;         // (the same in every warp)
     float M = -INFINITY, l = 0.f;
     float4 acc[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    int last = 0;                                        // steps before part i
-    for (int i = 0; i < parts; ++i) {
-        const int end = cut(x + i * line.per, c, N);
+    for (int i = 0, last = 0; last < N; ++i) {           // `last` steps lie before part i
+        const int end = cut(it.x + i * it.per, it.c, N);
         const bool empty = end == last;                  // two borders moved to the same step
         last = end;
         if (empty) continue;
@@ -1196,7 +1194,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p,
     const bool none = l == 0.f;
     const float vs = a.kv.f8 && a.kv.scale_v ? a.kv.scale_v[h] : 1.f;
     const float inv = none ? 0.f : vs / l;
-    const int64_t row = (int64_t)(s.q_row + tok) * a.Hq + h * a.G + rr % a.G;
+    const int64_t row = (int64_t)(it.q_row + tok) * a.Hq + h * a.G + rr % a.G;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
         turn[lane][q * kWarps + warp] = none ? make_uint2(0u, 0u)
@@ -1283,12 +1281,12 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStr
     }
     if (!regs_ok) return cudaErrorInvalidConfiguration;
     const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-    err = launch_pdl(kern, dim3(ctas), dim3(TcBlock<SRC>::threads), L::alloc, stream, mq, mk, mv, p, ctas);
+    err = launch_pdl(kern, dim3(ctas), dim3(TcBlock<SRC>::threads), L::alloc, stream, mq, mk, mv, p);
     if (err != cudaSuccess) return err;
     count_launches(1);
     // items of fewer than 2 kMinShare steps are never cut
     if (longest >= 2 * kMinShare * kStep - kStep + 1) {
-        err = launch_pdl(attn_tc_merge<E, D>, dim3(ctas - 1, kItemRows / 32), dim3(kMergeThreads), 0, stream, p, ctas);
+        err = launch_pdl(attn_tc_merge<E, D>, dim3(ctas - 1, kItemRows / 32), dim3(kMergeThreads), 0, stream, p);
         if (err == cudaSuccess) count_launches(1);
     }
     return err;
@@ -1302,7 +1300,9 @@ bool attn_tc_supported(const SeqKV& kv, int G) {
            (!kv.page_table || (int64_t)kv.num_pages * kv.page_size * kv.Hkv < 0xffffffffLL);
 }
 
-size_t attn_tc_ws_bytes(int G, int D) { return G <= kTileM ? (size_t)2 * kMaxCtas * kItemRows * (D + 2) * 4 : 0; }
+size_t attn_tc_ws_bytes(int G, int D) {
+    return G <= kTileM ? (size_t)2 * kMaxCtas * kItemRows * (D + 2) * 4 + kMaxCtas * sizeof(CutItem) : 0;
+}
 
 cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaStream_t stream) {
     TcParams p{};
@@ -1332,6 +1332,7 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
     p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.ws_o = static_cast<float*>(a.ws);
     p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;
+    p.ws_cut = reinterpret_cast<CutItem*>(p.ws_ml + (int64_t)2 * kMaxCtas * kItemRows * 2);
     // no sequence has more keys than this
     const int64_t longest = a.kv.page_table ? (int64_t)a.kv.max_pages * a.kv.page_size : a.kv.rows;
     const bool bf16 = dtype == SFA_DTYPE_BF16;
