@@ -73,7 +73,7 @@ def build_tensors() -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
            *[x for i in include for x in ("-isystem", i)],
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-o", tmp, TENSORS_SRC,
-           "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on tensors.cpp:\n{r.stderr}")

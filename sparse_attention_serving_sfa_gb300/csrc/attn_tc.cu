@@ -1272,13 +1272,10 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStr
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::alloc);
     if (err != cudaSuccess) return err;
     // the register split assumes a launch with that many registers a thread
-    static int regs_ok = -1;
-    if (regs_ok < 0) {
+    static const bool regs_ok = [&] {
         cudaFuncAttributes fa;
-        err = cudaFuncGetAttributes(&fa, kern);
-        if (err != cudaSuccess) return err;
-        regs_ok = fa.numRegs == TcBlock<SRC>::launch ? 1 : 0;
-    }
+        return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs == TcBlock<SRC>::launch;
+    }();
     if (!regs_ok) return cudaErrorInvalidConfiguration;
     const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
     err = launch_pdl(kern, dim3(ctas), dim3(TcBlock<SRC>::threads), L::alloc, stream, mq, mk, mv, p);
