@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
 // CTAs x and x + 1) cuts first: a warp per row, the parts' (m, sum) a lane
 // each, eight parts of O in flight.
 template <class E, int D, int F8>
-__global__ void __launch_bounds__(kThreads) attn_rows_merge(const SeqAttn p, uint64_t ctas_mul) {
+__global__ void __launch_bounds__(32 * kRows, 1) attn_rows_merge(const SeqAttn p, uint64_t ctas_mul) {
     constexpr int chunk = RowsCfg<D, F8>::chunk;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // The lists are older than the main kernel, which waited for them before
@@ -653,24 +653,15 @@ __global__ void __launch_bounds__(kThreads) attn_rows_merge(const SeqAttn p, uin
     auto slot_of = [&](int i) { return i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i); };
 
     constexpr int W = D / 32;                     // dims of a lane
-    for (int r = warp; r < kRows; r += kWarps) {
-        if (row_base + r >= rows) break;
+    // (as many warps as the longest sequence is said to have rows)
+    for (int r = warp; r < kRows && row_base + r < rows; r += blockDim.x >> 5) {
         float M = -INFINITY, L = 0.f, acc[W];
 #pragma unroll
         for (int i = 0; i < W; ++i) acc[i] = 0.f;
         for (int i0 = 0; i0 < parts; i0 += 32) {
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (i0 + lane < parts)
-                ml = *reinterpret_cast<const float2*>(ws_ml + ((int64_t)slot_of(i0 + lane) * kRows + r) * 2);
-            const float m_new = fmaxf(M, warp_max(ml.x));
-            const float old = rescale_factor(M, m_new), f = rescale_factor(ml.x, m_new);
-            M = m_new;
-            L = L * old + warp_sum(ml.y * f);
-#pragma unroll
-            for (int i = 0; i < W; ++i) acc[i] *= old;
             const int m = min(32, parts - i0);
-            for (int j0 = 0; j0 < m; j0 += 8) {
-                float v[8][W];
+            float v[8][W];
+            auto load = [&](int j0) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float* src = ws_o + ((int64_t)slot_of(i0 + min(j0 + j, m - 1)) * kRows + r) * D + lane * W;
@@ -678,6 +669,18 @@ __global__ void __launch_bounds__(kThreads) attn_rows_merge(const SeqAttn p, uin
                     for (int i = 0; i < W; i += 2)
                         *reinterpret_cast<float2*>(&v[j][i]) = *reinterpret_cast<const float2*>(src + i);
                 }
+            };
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < m) ml = *reinterpret_cast<const float2*>(ws_ml + ((int64_t)slot_of(i0 + lane) * kRows + r) * 2);
+            load(0);
+            const float m_new = fmaxf(M, warp_max(ml.x));
+            const float old = rescale_factor(M, m_new), f = rescale_factor(ml.x, m_new);
+            M = m_new;
+            L = L * old + warp_sum(ml.y * f);
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] *= old;
+            for (int j0 = 0; j0 < m; j0 += 8) {
+                if (j0 > 0) load(j0);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float g = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
@@ -715,7 +718,9 @@ cudaError_t launch_rows_t(const SeqAttn& p, int num_sms, cudaStream_t stream) {
     // tiles of fewer than 2 kMinPart chunks are never cut
     const int64_t longest = p.kv.page_table ? (int64_t)p.kv.max_pages * p.kv.page_size : p.kv.rows;
     if (longest > (int64_t)(2 * kMinPart - 1) * C::chunk) {
-        err = launch_pdl(attn_rows_merge<E, D, F8>, dim3(ctas - 1), dim3(kThreads), 0, stream, p, mul);
+        const int64_t most = (int64_t)p.max_q_len * p.G;           // rows of a kv head
+        err = launch_pdl(attn_rows_merge<E, D, F8>, dim3(ctas - 1), dim3(32 * (int)min(most, (int64_t)kRows)), 0, stream, p,
+                         mul);
         if (err == cudaSuccess) count_launches(1);
     }
     return err;

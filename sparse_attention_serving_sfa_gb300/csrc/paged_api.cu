@@ -60,7 +60,14 @@ bool bad_stride(int64_t stride, int heads, int D) {
     return stride < (int64_t)heads * D || stride % 8 != 0 || stride > (int64_t)1 << 38;
 }
 
-constexpr int kFewRows = 16;
+// Up to this many rows a kv head (the longest sequence's) go to 16-row tiles,
+// which read the keys at HBM's pace; the tensor-core tiles of 128 rows stand
+// mostly empty then, but more rows cost them nothing.  64 sequences of 4,096
+// keys, 8 kv heads of 128: 16 rows take 183 us in 16-row tiles and 172 us in
+// 128-row ones, 32 rows 337 and 174 us (one sequence of 500 keys: 16 rows 12.2
+// and 12.7 us).  Over an 8-bit cache, which the latter must convert first: 16
+// rows 106 and 228 us, 32 rows 190 and 232 us, 64 rows 357 and 235 us.
+constexpr int kFewRows = 16, kFewRows8 = 32;
 
 // Workspace of either path.
 size_t attention_ws_bytes(int Hq, int Hkv, int D) {
@@ -91,9 +98,7 @@ sfa_status run_attention(SeqAttn& p, int num_tokens, int num_qo_heads, int max_q
     p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)p.kv.D)) * kLog2e;
     p.ws = ws;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // Few rows a kv head: one 16-row tile reads the keys at HBM's pace, the
-    // 128-row tensor-core tiles would stand mostly empty.
-    const bool few = (int64_t)p.max_q_len * p.G <= kFewRows;
+    const bool few = (int64_t)p.max_q_len * p.G <= (p.kv.f8 ? kFewRows8 : kFewRows);
     cudaError_t err;
     if (!few && attn_tc_supported(p.kv, p.G)) {
         p.err_word = device_error_word();
