@@ -1150,6 +1150,7 @@ template <class E, int D>
 __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p) {
     constexpr int kWarps = kMergeThreads / 32;
     constexpr int Q = D / 4 / kWarps;                    // 4-dim groups of a warp
+    constexpr int kBatch = 4;
     __shared__ uint2 turn[32][D / 4 + 1];
     const SeqAttn& a = p.a;
     const float kPShift = std::is_same<E, BF16>::value && a.kv.f8 == 0 ? 0.f : 7.f;
@@ -1165,30 +1166,42 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p)
     float4 acc[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0, last = 0; last < N; ++i) {           // `last` steps lie before part i
-        const int end = cut(it.x + i * it.per, it.c, N);
-        const bool empty = end == last;                  // two borders moved to the same step
-        last = end;
-        if (empty) continue;
-        const int64_t slot = i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i);
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (valid) ml = *reinterpret_cast<const float2*>(p.ws_ml + (slot * kItemRows + r) * 2);
-        float4 v[Q];
+    // kBatch parts in flight (`last`: steps before part i)
+    for (int i = 0, last = 0; last < N; i += kBatch) {
+        float2 ml[kBatch];
+        float4 v[kBatch][Q];
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
-            v[q] = valid ? *reinterpret_cast<const float4*>(p.ws_o + slot * kItemRows * D + ((q * kWarps + warp) * kItemRows + r) * 4)
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < kBatch; ++j) {
+            const int end = last < N ? cut(it.x + (i + j) * it.per, it.c, N) : last;
+            const bool some = valid && end != last;      // (two borders can move to the same step)
+            last = end;
+            const int64_t slot = i + j == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i + j);
+            ml[j] = some ? *reinterpret_cast<const float2*>(p.ws_ml + (slot * kItemRows + r) * 2) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                v[j][q] = some ? *reinterpret_cast<const float4*>(p.ws_o + slot * kItemRows * D + ((q * kWarps + warp) * kItemRows + r) * 4)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         // (a part without a visible key: m = -inf, everything else 0)
-        const float m_new = fmaxf(M, ml.x);
-        const float old = rescale_factor(M, m_new), f = rescale_factor(ml.x, m_new);
-        M = m_new;
-        l = l * old + ml.y * f;
+        float m_new = M;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            acc[q].x = acc[q].x * old + v[q].x * f;
-            acc[q].y = acc[q].y * old + v[q].y * f;
-            acc[q].z = acc[q].z * old + v[q].z * f;
-            acc[q].w = acc[q].w * old + v[q].w * f;
+        for (int j = 0; j < kBatch; ++j) m_new = fmaxf(m_new, ml[j].x);
+        const float old = rescale_factor(M, m_new);
+        M = m_new;
+        l *= old;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) acc[q] = make_float4(acc[q].x * old, acc[q].y * old, acc[q].z * old, acc[q].w * old);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const float f = rescale_factor(ml[j].x, M);
+            l += ml[j].y * f;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                acc[q].x += v[j][q].x * f;
+                acc[q].y += v[j][q].y * f;
+                acc[q].z += v[j][q].z * f;
+                acc[q].w += v[j][q].w * f;
+            }
         }
     }
     const bool none = l == 0.f;

@@ -60,14 +60,31 @@ bool bad_stride(int64_t stride, int heads, int D) {
     return stride < (int64_t)heads * D || stride % 8 != 0 || stride > (int64_t)1 << 38;
 }
 
-// Up to this many rows a kv head (the longest sequence's) go to 16-row tiles,
-// which read the keys at HBM's pace; the tensor-core tiles of 128 rows stand
-// mostly empty then, but more rows cost them nothing.  64 sequences of 4,096
-// keys, 8 kv heads of 128: 16 rows take 183 us in 16-row tiles and 172 us in
-// 128-row ones, 32 rows 337 and 174 us (one sequence of 500 keys: 16 rows 12.2
-// and 12.7 us).  Over an 8-bit cache, which the latter must convert first: 16
-// rows 106 and 228 us, 32 rows 190 and 232 us, 64 rows 357 and 235 us.
-constexpr int kFewRows = 16, kFewRows8 = 32;
+// 16-row tiles read the keys at HBM's pace and begin early; the 128-row
+// tensor-core tiles stand mostly empty with few rows, but more rows cost them
+// nothing.  So 16-row tiles take
+//   - up to kFewRows rows a kv head (by the longest sequence): 64 sequences of
+//     4,096 keys, 8 kv heads of 128: 16 rows take 173 to 182 us in 16-row tiles
+//     and 172 us in 128-row ones, 32 rows 337 and 174 us; one sequence of 8,192
+//     keys: 16 rows 17.7 and 29.9 us.  Over an 8-bit cache, which 128-row tiles
+//     must convert first, twice as many: 16 rows 104 and 228 us, 32 rows 188
+//     and 232 us, 64 rows 357 and 235 us.
+//   - where there are few of them and they read few keys over again: one
+//     sequence of 8,192 keys, 8 kv heads, 32 rows (16 tiles): 20.4 and 29.7 us,
+//     2 kv heads, 64 rows (8 tiles): 17.4 and 60.6 us; but of 65,536 keys, 8 kv
+//     heads, 32 rows: 88 and 64 us; 4 sequences of 500 keys, 64 tiles: 14.4 and
+//     12.9 us.  8-bit: 8,192 keys, 64 tiles: 33.8 and 35.1 us; 4 sequences of
+//     16,384 keys, 2 kv heads, 96 rows (48 tiles): 44 and 39 us.
+constexpr int kFewRows = 16, kFewTiles = 16;
+constexpr int64_t kFewReads = 1 << 18;               // tiles x keys, by what the table or the packed rows can hold
+
+bool few_rows(const SeqAttn& p) {
+    const int f = p.kv.f8 ? 2 : 1;
+    const int64_t rows = (int64_t)p.max_q_len * p.G;
+    const int64_t tiles = (rows + 15) / 16 * p.kv.num_seqs * p.kv.Hkv;
+    const int64_t keys = p.kv.page_table ? (int64_t)p.kv.max_pages * p.kv.page_size : p.kv.rows;
+    return rows <= f * kFewRows || (tiles <= f * f * kFewTiles && tiles * keys <= f * kFewReads);
+}
 
 // Workspace of either path.
 size_t attention_ws_bytes(int Hq, int Hkv, int D) {
@@ -98,9 +115,8 @@ sfa_status run_attention(SeqAttn& p, int num_tokens, int num_qo_heads, int max_q
     p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)p.kv.D)) * kLog2e;
     p.ws = ws;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool few = (int64_t)p.max_q_len * p.G <= (p.kv.f8 ? kFewRows8 : kFewRows);
     cudaError_t err;
-    if (!few && attn_tc_supported(p.kv, p.G)) {
+    if (!few_rows(p) && attn_tc_supported(p.kv, p.G)) {
         p.err_word = device_error_word();
         if (!p.err_word) return SFA_ERR_CUDA;
         err = launch_attn_tc(p, dtype, num_sms(), s);
