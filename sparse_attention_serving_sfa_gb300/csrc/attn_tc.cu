@@ -24,13 +24,13 @@
 //   - MMA thread: S_t = Q_t K^T into TMEM, O_t += P_t V with P from TMEM and
 //     V an MN-major operand; tile 0's P.V and next Q.K^T run while the
 //     softmax works on tile 1, and the other way round.
-//   - producer: Q tiles and a ring of 128-key K and V tiles in the order the
+//   - loader: Q tiles and a ring of 128-key K and V tiles in the order the
 //     MMAs use them, running ahead across items.  Packed rows and 16-bit pages
 //     of a multiple of 16 tokens come by TMA (one warp; a page is a box of a
-//     4-D map).  8-bit pages come by TMA into two swizzled staging tiles, from
-//     which four mover warps write them out as fp16 (exact) into the tiles the
-//     MMA reads.  Pages of other sizes come row by row through the movers'
-//     16-byte cp.async.  Rows without a key are zeros.
+//     4-D map).  8-bit pages (of a multiple of 8) come by TMA into two swizzled
+//     staging tiles, from which four mover warps write them out as fp16 (exact)
+//     into the tiles the MMA reads.  Pages of other sizes come row by row
+//     through the movers' 16-byte cp.async.  Rows without a key are zeros.
 // TMEM: tile t at column 256 t: S / P in [0, 128), O in [128, 128 + D).
 //
 // With an 8-bit cache both products run in fp16.  bf16 rows of q are scaled to
@@ -44,8 +44,19 @@
 // largest stay normal.  Sums of P use the unrounded fp32 values.
 //
 // V rows behind kv_len (the next sequence's, or whatever a page holds) would
-// turn 0 x NaN into NaN: where TMA brought them the producer waits for such a
+// turn 0 x NaN into NaN: where TMA brought them the loader waits for such a
 // tile itself, writes zeros over those rows and then hands it on.
+//
+// Bound: the tensor pipe and the softmax's issue slots, which take turns (4 D
+// operations a score against one exp2, one subtraction, a max, half a
+// conversion ...); short items by the way from one barrier to the next.  Two
+// tiles of a CTA hide the one behind the other; 208 registers a softmax thread
+// hold a row's 128 scores, so that S is read from TMEM once.  Measured: one
+// causal prompt of 16,384 tokens, 32/8 heads of 128, 1.40 to 1.52 ms, 1.45 to
+// 1.57 PFLOP/s (0.86 to 0.93 of a sustained library product's rate); chunks of
+// 200 to 1,024 tokens over up to 8,192 keys in 32-token pages 203 us, 1.24
+// PFLOP/s; over E4M3 pages 389 us, 1.08 PFLOP/s; 40 prompts of up to 700
+// tokens, 12/4 heads of 64, 31.5 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -66,6 +77,11 @@ constexpr int kTmemCols = 512, kTileCols = 256, kOCol = 128;
 constexpr float kRescale = 8.0f;            // log2 units
 constexpr int kItemRows = 2 * kTileM;
 constexpr int kMinShare = 2;                // fewest steps of a part
+// Pages of a multiple of this many tokens come by TMA, others row by row.  8
+// sequences' chunks of 512 tokens over 4,096 keys, 32/8 heads of 128: 16-bit
+// pages of 32 tokens 192 us, of 16 218, of 8 317 (row by row 299); E4M3 pages of
+// 16 tokens 296 us, of 8 302 (row by row 431).
+constexpr int kMinBox = 16, kMinBox8 = 8;
 constexpr int kMinRange = kStep;            // shortest range of a CTA, in keys
 constexpr int kMaxCtas = 160;               // ranges (the workspace's size goes by it)
 
@@ -472,7 +488,7 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
     };
     static_assert(kMovers == kStep, "a thread a row number");
     uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::rows);
-    const bool tma = F8 && p.box >= 16;                      // staging tiles filled by the loader's TMA
+    const bool tma = F8 && p.box >= kMinBox8;                     // staging tiles filled by the loader's TMA
     int loads = 0, tables = 0;
     bool ok = true;
     // both movers are here (with what they wrote to shared memory)
@@ -646,7 +662,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(bar(B_Q + t), kScaledQ ? 4 : 1);
         }
         for (int s = 0; s < L::slots; ++s) {
-            mbar_init(bar(B_FULL + s), !L::gather ? 1 : (L::f8 && p.box >= 16 ? kMovers / 64 : kMovers / 32));
+            mbar_init(bar(B_FULL + s), !L::gather ? 1 : (L::f8 && p.box >= kMinBox8 ? kMovers / 64 : kMovers / 32));
             mbar_init(bar(B_FREE + s), 1);
         }
         fence_barrier_init();
@@ -682,7 +698,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             int number = 0;
             int items = 0, loads = 0, tails = 0;   // items with keys, tiles loaded, tiles cleared
             int qs[2] = {0, 0};                    // Q tiles loaded
-            const bool tma = !L::gather || (L::f8 && p.box >= 16);
+            const bool tma = !L::gather || (L::f8 && p.box >= kMinBox8);
             bool ok = true;
             for (;; more = walk.next(p, next_item)) {
                 if (!more) next_item.b = -1;
@@ -1274,7 +1290,7 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStr
     if (!rows_map(&mq, a.q, bf16, D, a.Hq, a.tokens, a.q_stride, a.G, p.TR)) return cudaErrorInvalidValue;
     if (L::gather) {
         mk = mv = mq;              // (unused where rows are gathered without maps)
-        if (L::f8 && p.box >= 16 && (!codes_map(&mk, a.kv.k, a.kv, p.hnd, p.box) || !codes_map(&mv, a.kv.v, a.kv, p.hnd, p.box)))
+        if (L::f8 && p.box >= kMinBox8 && (!codes_map(&mk, a.kv.k, a.kv, p.hnd, p.box) || !codes_map(&mv, a.kv.v, a.kv, p.hnd, p.box)))
             return cudaErrorInvalidValue;
     } else if (SRC == SRC_PAGES ? (!pool_map(&mk, a.kv.k, bf16, a.kv, p.hnd, p.box) || !pool_map(&mv, a.kv.v, bf16, a.kv, p.hnd, p.box))
               : (!rows_map(&mk, a.kv.k, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.s_tok, 1, kStep) ||
@@ -1348,7 +1364,7 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
     const bool bf16 = dtype == SFA_DTYPE_BF16;
     const int src = !a.kv.page_table ? SRC_PACKED
                     : a.kv.f8        ? (a.kv.f8 == 1 ? SRC_E4M3 : SRC_E5M2)
-                                     : (a.kv.page_size % 16 == 0 ? SRC_PAGES : SRC_G16);
+                                     : (a.kv.page_size % kMinBox == 0 ? SRC_PAGES : SRC_G16);
 #define SFA_ATTN_TC(D_, SRC_)                                                        \
     if (a.kv.D == D_ && src == SRC_)                                                 \
         return bf16 ? launch_tc_t<BF16, D_, SRC_>(p, longest, num_sms, stream)         \

@@ -13,7 +13,11 @@
 // elements measured slower on most calls: 47.4 -> 50.6 and 54.9 us for 261 MB
 // read back.)  The sequence of a warp's first token is found by a 32-way search
 // of cu (one load per factor of 32 in the number of sequences), then each lane
-// walks to its own token's.
+// walks to its own token's.  Measured: 261 MB read back from E4M3 pages 48 us
+// (5.4 TB/s, 0.80 of the measured copy rate); 12,800 tokens of 8 heads of 128
+// quantised into E4M3 pages 17.9 us (4.4 TB/s), 12,500 of 4 heads of 64 copied
+// into 24-token pages 6.6 us (from and into L2); a decode step's 64 tokens 3.1
+// us, a launch's latency.
 //
 // Rounding to codes: x times the scale's rounded reciprocal is within 2 units
 // in the last place of the quotient.  A border between two codes has 19 zero

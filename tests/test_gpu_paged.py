@@ -213,6 +213,61 @@ def test_paged_attention(shape, cache, layout, dtype):
             check_paged(c, out, lse, causal)
 
 
+@pytest.mark.parametrize("cache,layout,dtype", [("same", "NHD", "bf16"), ("e4m3", "HND", "f16"),
+                                                ("e5m2", "NHD", "bf16")])
+@pytest.mark.parametrize("shape", [1, 2, 3, 4, 6, 9, 10])
+def test_table_much_wider_than_the_sequences(shape, cache, layout, dtype):
+    """A table made for a million tokens: small calls on the large tiles too."""
+    q_lens, kv_lens, heads, kv_heads, dim, page = SHAPES[shape]
+    c = P.Cache(200 + shape, q_lens, kv_lens, heads, kv_heads, dim, page, dtype, cache, layout,
+                before=1, behind=2).poison()
+    c.table = torch.cat([c.table, torch.full((len(q_lens), (1 << 20) // page), -1, dtype=torch.int32)], 1)
+    out, lse = run_paged(c, True, 0)
+    check_paged(c, out, lse, True)
+
+
+@pytest.mark.parametrize("cache,layout,dtype", [("same", "NHD", "f16"), ("same", "HND", "bf16"),
+                                                ("e4m3", "HND", "f16"), ("e5m2", "NHD", "bf16")])
+@pytest.mark.parametrize("page,dim", [(1, 64), (8, 128), (8, 64), (12, 128), (20, 64), (24, 128), (40, 64), (56, 128)])
+def test_chunks_over_pages_of_any_size(page, dim, cache, layout, dtype):
+    c = P.Cache(300 + page, [150, 300], [700, 1111], 8, 2, dim, page, dtype, cache, layout, behind=1).poison()
+    c.table[1, 100 // page] = c.pages               # a page that is not there
+    for hint in (300, 0):
+        out, lse = run_paged(c, True, hint)
+        check_paged(c, out, lse, True)
+
+
+@pytest.mark.parametrize("cache,dtype", [("same", "bf16"), ("same", "f16"), ("e4m3", "bf16"), ("e5m2", "f16")])
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,dim,page", [
+    ([12], [6000], 8, 2, 128, 16),                  # three tiles a head, cut into many parts
+    ([20, 5], [3000, 900], 4, 1, 64, 24),
+    ([2, 2], [5000, 40], 16, 2, 128, 64),           # sixteen rows
+    ([64], [2500], 1, 1, 128, 32),
+    ([3], [20000], 5, 1, 64, 16),
+])
+def test_few_rows_cut_into_parts(q_lens, kv_lens, heads, kv_heads, dim, page, cache, dtype):
+    c = P.Cache(41, q_lens, kv_lens, heads, kv_heads, dim, page, dtype, cache, before=2, behind=1).poison()
+    # what is said about the lengths changes the kernel and its joins, not the result
+    for hint in (max(q_lens), 1, 0):
+        out, lse = run_paged(c, True, hint)
+        check_paged(c, out, lse, True)
+
+
+@pytest.mark.parametrize("hint,q_lens", [(1, [1, 1]), (0, [40, 70])])
+def test_out_at_any_16_bytes(hint, q_lens):
+    """An out that begins 16 bytes behind a 32-byte border."""
+    c = P.Cache(42, q_lens, [900, 333], 8, 2, 128, 16, "bf16")
+    d = c.to("cuda")
+    q, _, _ = c.split(d["qkv"])
+    room = torch.full((c.T * c.Hq * c.D + 16,), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = room[8:-8].view(c.T, c.Hq, c.D)
+    assert out.data_ptr() % 32 == 16
+    _, lse = sfa.paged_attention(q, d["k"], d["v"], d["table"], d["lens"], d["cu"], max_q_len=hint, out=out,
+                                 return_lse=True)
+    check_paged(c, out.cpu(), lse.cpu(), True)
+    assert (room[:8] == 9).all() and (room[-8:] == 9).all()
+
+
 @pytest.mark.parametrize("cache", ["same", "e4m3"])
 @pytest.mark.parametrize("hint", [1, 0])
 def test_pages_out_of_range_are_absent(cache, hint):
