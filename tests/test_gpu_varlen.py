@@ -63,6 +63,8 @@ SHAPES = [
     ([1, 1, 1], [900, 1, 130], 16, 4, 128),              # single rows
     ([40, 260, 5, 3], [1500, 100, 0, 2], 8, 2, 128),     # other numbers of keys, empty rows, none
     ([2048], None, 2, 1, 128),
+    ([40], [4000], 2, 1, 128),                           # few tiles, long keys
+    ([9, 33], [2500, 100], 6, 2, 64),
 ]
 
 
