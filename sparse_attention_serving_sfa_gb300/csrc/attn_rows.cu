@@ -68,7 +68,12 @@ struct RowsCfg {
     static constexpr int ml = masks + kWarps * NS * 4;
     static constexpr int total = ml + kWarps * kRows * 2 * 4;
     static constexpr int chunk = kWarps * KS;
-    static_assert(kRows * D * 4 <= warp_bytes, "a warp's O fits its ring");
+    // A warp's O in shared memory (over its ring): dim d of a row at o_at(d).
+    // Rows and, where a thread holds D / 4 dims on end, those are spread over
+    // the banks (without that the writes of a part took 8,000 cycles).
+    static constexpr int o_row = F8 ? D + 16 : D + 8;
+    __device__ static constexpr int o_at(int d) { return F8 ? d + d / (D / 4) * 4 : d; }
+    static_assert(kRows * o_row * 4 <= warp_bytes, "a warp's O fits its ring");
 };
 
 // A sequence on the line: tiles * Hkv pieces of chunks + kCharge units, a tile's
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
         int x0;
         int64_t th;
         split_unit(u - seq_start, sq.chunks + kCharge, x0, th);
-        const int tile = (int)((uint32_t)th / (uint32_t)p.kv.Hkv), h = (int)((uint32_t)th - (uint32_t)tile * p.kv.Hkv);
+        const int tile = over((int)th, p.by_heads), h = (int)th - tile * p.kv.Hkv;
         const int64_t x1 = min((int64_t)sq.chunks + kCharge, x0 + (u_end - u));
         const int c0 = cut(x0, sq.chunks), c1 = cut(x1, sq.chunks);
         u += x1 - x0;
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
         // number of visible keys of a row (rows past the tile: all, unused)
         auto limit = [&](int r) -> int {
             if (!p.causal || row_base + r >= rows) return kv_len;
-            const int i = (row_base + r) / p.G;
+            const int i = over(row_base + r, p.by_group);
             return max(0, min(kv_len, i + kv_len - n_q + 1));
         };
         const int last_row = min(kRows, rows - row_base) - 1;
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             const int key = key0(st) + lane;
             if (st >= nsteps || lane >= KS || key >= kv_len) return -1;
             if constexpr (!PAGED) return 0;
-            return p.kv.page_table[(int64_t)b * p.kv.max_pages + key / p.kv.page_size];
+            return p.kv.page_table[(int64_t)b * p.kv.max_pages + over(key, p.by_page)];
         };
         auto issue = [&](int st, int page) {
             if (PAGED && (unsigned)page >= (unsigned)p.kv.num_pages) page = -1;
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                 int64_t ko = -1, vo = -1;
                 if (page >= 0) {
                     if constexpr (PAGED) {
-                        ko = (int64_t)page * p.kv.s_page + (int64_t)(key % p.kv.page_size) * p.kv.s_tok;
+                        ko = (int64_t)page * p.kv.s_page + (int64_t)(key - over(key, p.by_page) * p.kv.page_size) * p.kv.s_tok;
                     } else {
                         ko = (int64_t)(sq.k_row + key) * p.kv.s_tok;
                         vo = (int64_t)(sq.k_row + key) * p.kv.sv_tok;
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             const uint16_t* qb = static_cast<const uint16_t*>(p.q);
             auto q_row = [&](int r) -> const uint16_t* {
                 if (row_base + r >= rows) return nullptr;
-                const int i = (row_base + r) / p.G;
+                const int i = over(row_base + r, p.by_group);
                 return qb + (sq.q_row + i) * p.q_stride + (h * p.G + (row_base + r) - i * p.G) * D;
             };
             const uint16_t* q0 = q_row(g);
@@ -553,14 +558,25 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             l1 += __shfl_xor_sync(0xffffffffu, l1, of);
         }
         float* wo = reinterpret_cast<float*>(ring);
+        const int rows_here = rows - row_base;     // (rows behind the last need no result)
 #pragma unroll
-        for (int i = 0; i < ND; ++i)
+        for (int half = 0; half < 2; ++half) {
+            if (8 * half >= rows_here) continue;
+            float* to = wo + (g + 8 * half) * C::o_row;
+            if constexpr (F8) {
+                // dims D / 8 (2c + j) .. + D / 8 - 1
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int d = F8 ? (D / 8) * (2 * c + j) + i : 8 * i + 2 * c + j;
-                wo[g * D + d] = o[i][j];
-                wo[(g + 8) * D + d] = o[i][2 + j];
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < ND; i += 4)
+                        *reinterpret_cast<float4*>(to + C::o_at((D / 8) * (2 * c + j) + i)) =
+                            make_float4(o[i][2 * half + j], o[i + 1][2 * half + j], o[i + 2][2 * half + j], o[i + 3][2 * half + j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < ND; ++i)
+                    *reinterpret_cast<float2*>(to + 8 * i + 2 * c) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
             }
+        }
         if (c == 0) {
             float* mw = ml + warp * kRows * 2;
             mw[2 * g] = m0;
@@ -569,56 +585,51 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             mw[2 * (g + 8) + 1] = l1;
         }
         __syncthreads();
-        {
-            const int r = tid >> 3;
-            constexpr int W = D / 8;                   // dims of a thread
-            const int d0 = (tid & 7) * W;
+        const int r = tid >> 3;
+        if (r < rows_here) {
+            // dims 32 i + d0 .. + 3: the eight threads of a row read side by side
+            constexpr int N = D / 32;
+            const int d0 = (tid & 7) * 4;
             float M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[(w * kRows + r) * 2]);
-            float L = 0.f, acc[W];
+            float L = 0.f;
+            float4 acc[N];
 #pragma unroll
-            for (int i = 0; i < W; ++i) acc[i] = 0.f;
+            for (int i = 0; i < N; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float mw = ml[(w * kRows + r) * 2];
                 const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
                 L += f * ml[(w * kRows + r) * 2 + 1];
-                const float4* src = reinterpret_cast<const float4*>(smem + w * C::warp_bytes + (r * D + d0) * 4);
+                const float* src = reinterpret_cast<const float*>(smem + w * C::warp_bytes) + r * C::o_row;
 #pragma unroll
-                for (int i = 0; i < W / 4; ++i) {
-                    const float4 t = src[i];
-                    acc[4 * i] += f * t.x;
-                    acc[4 * i + 1] += f * t.y;
-                    acc[4 * i + 2] += f * t.z;
-                    acc[4 * i + 3] += f * t.w;
+                for (int i = 0; i < N; ++i) {
+                    const float4 t = *reinterpret_cast<const float4*>(src + C::o_at(32 * i + d0));
+                    acc[i].x += f * t.x;
+                    acc[i].y += f * t.y;
+                    acc[i].z += f * t.z;
+                    acc[i].w += f * t.w;
                 }
             }
             if (c0 == 0 && c1 == sq.chunks) {
-                if (row_base + r < rows) {
-                    const float vs = F8 && p.kv.scale_v ? p.kv.scale_v[h] : 1.f;
-                    const bool none = L == 0.f;        // no visible key (a NaN sum is not that)
-                    const float inv = none ? 0.f : vs / L;
-                    const int i = (row_base + r) / p.G;
-                    const int64_t row = (int64_t)(sq.q_row + i) * p.Hq + h * p.G + (row_base + r) - i * p.G;
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<typename E::T*>(p.out) + row * D + d0);
+                const float vs = F8 && p.kv.scale_v ? p.kv.scale_v[h] : 1.f;
+                const bool none = L == 0.f;        // no visible key (a NaN sum is not that)
+                const float inv = none ? 0.f : vs / L;
+                const int i = over(row_base + r, p.by_group);
+                const int64_t row = (int64_t)(sq.q_row + i) * p.Hq + h * p.G + (row_base + r) - i * p.G;
+                typename E::T* dst = static_cast<typename E::T*>(p.out) + row * D + d0;
 #pragma unroll
-                    for (int i = 0; i < W / 8; ++i) {
-                        uint4 w;
-                        w.x = none ? 0u : E::pack2(acc[8 * i] * inv, acc[8 * i + 1] * inv);
-                        w.y = none ? 0u : E::pack2(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv);
-                        w.z = none ? 0u : E::pack2(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv);
-                        w.w = none ? 0u : E::pack2(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv);
-                        dst[i] = w;
-                    }
-                    if (p.lse && (tid & 7) == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
-                }
+                for (int i = 0; i < N; ++i)
+                    *reinterpret_cast<uint2*>(dst + 32 * i) =
+                        none ? make_uint2(0u, 0u)
+                             : make_uint2(E::pack2(acc[i].x * inv, acc[i].y * inv), E::pack2(acc[i].z * inv, acc[i].w * inv));
+                if (p.lse && (tid & 7) == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
             } else {
                 const int slot = 2 * blockIdx.x + (c0 == 0 ? 1 : 0);
-                float4* dst = reinterpret_cast<float4*>(ws_o + ((int64_t)slot * kRows + r) * D + d0);
+                float* dst = ws_o + ((int64_t)slot * kRows + r) * D + d0;
 #pragma unroll
-                for (int i = 0; i < W / 4; ++i)
-                    dst[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                for (int i = 0; i < N; ++i) *reinterpret_cast<float4*>(dst + 32 * i) = acc[i];
                 if ((tid & 7) == 0)
                     *reinterpret_cast<float2*>(ws_ml + ((int64_t)slot * kRows + r) * 2) = make_float2(M, L);
             }
@@ -649,7 +660,7 @@ __global__ void __launch_bounds__(32 * kRows, 1) attn_rows_merge(const SeqAttn p
     const int n = sq.chunks, c = cut(x, n);
     // not cut here, or first cut earlier
     if (c == 0 || c == n || cut(x - line.per, n) > 0) return;
-    const int tile = (int)((uint32_t)th / (uint32_t)p.kv.Hkv), h = (int)((uint32_t)th - (uint32_t)tile * p.kv.Hkv);
+    const int tile = over((int)th, p.by_heads), h = (int)th - tile * p.kv.Hkv;
     const int rows = sq.n_q * p.G, row_base = tile * kRows;
     // one before this border and one behind each border that still cuts
     const int parts = 2 + (int)((uint32_t)(n - kMinPart + kCharge / 2 - x) / (uint32_t)min(line.per, (int64_t)0x7fffffff));
@@ -699,7 +710,7 @@ __global__ void __launch_bounds__(32 * kRows, 1) attn_rows_merge(const SeqAttn p
         const bool none = L == 0.f;
         const float vs = F8 && p.kv.scale_v ? p.kv.scale_v[h] : 1.f;
         const float inv = none ? 0.f : vs / L;
-        const int i = (row_base + r) / p.G;
+        const int i = over(row_base + r, p.by_group);
         const int64_t row = (int64_t)(sq.q_row + i) * p.Hq + h * p.G + (row_base + r) - i * p.G;
         typename E::T* out = static_cast<typename E::T*>(p.out) + row * D + lane * W;
 #pragma unroll

@@ -141,8 +141,7 @@ enum {
 struct TcParams {
     SeqAttn a;
     int TR, hnd;
-    uint32_t unit_mul, page_mul;        // x / (2 TR) = x * unit_mul >> unit_shift for 0 <= x < 2^31,
-    int unit_shift, page_shift;         // x / page_size likewise
+    Divisor by_unit;                    // tokens of an item, 2 TR
     uint64_t ctas_mul;                  // x / ctas = high word of x * ctas_mul for x < 2^56
     int charge;                         // an item's fixed cost, in keys
     int out32;                          // out is 32-byte aligned
@@ -169,12 +168,12 @@ struct Seq {
 
 // x / (2 TR)
 __device__ __forceinline__ int units(const TcParams& p, int x) {
-    return (int)(((uint64_t)(uint32_t)x * p.unit_mul) >> p.unit_shift);
+    return over(x, p.by_unit);
 }
 
 // x / page_size
 __device__ __forceinline__ int page_slot(const TcParams& p, int x) {
-    return (int)(((uint64_t)(uint32_t)x * p.page_mul) >> p.page_shift);
+    return over(x, p.a.by_page);
 }
 
 __device__ __forceinline__ Seq seq_of(const TcParams& p, int b) {
@@ -1340,15 +1339,7 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
         while (a.kv.page_size % p.box != 0) p.box /= 2;
     p.boxes = kStep / p.box;
     while ((1 << p.box_shift) < p.box) ++p.box_shift;
-    // for x < 2^31: multiplier rounded up at 2^(31 + ceil(log2 d))
-    auto divide_by = [](uint32_t d, uint32_t& mul, int& shift) {
-        int up = 0;
-        while (((uint64_t)1 << up) < d) ++up;
-        shift = 31 + up;
-        mul = (uint32_t)((((uint64_t)1 << shift) + d - 1) / d);
-    };
-    divide_by(2 * p.TR, p.unit_mul, p.unit_shift);
-    if (a.kv.page_table) divide_by(a.kv.page_size, p.page_mul, p.page_shift);
+    p.by_unit = divide_by(2 * p.TR);
     p.ctas_mul = ~uint64_t(0) / (uint64_t)(num_sms < kMaxCtas ? num_sms : kMaxCtas) + 1;
     // Measured (320 / 448 / 576 / 768): chunks of 200 to 1,024 tokens over 16-bit
     // pages 236 / 223 / 215 / 219 us; 64-dim prompts of up to 700 tokens (192 / 320 /

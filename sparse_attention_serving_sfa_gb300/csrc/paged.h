@@ -32,6 +32,19 @@ struct SeqKV {
     const float* scale_v;
 };
 
+// x / d = x * mul >> shift for 0 <= x < 2^31 (the multiplier rounded up at
+// 2^(31 + ceil(log2 d))): a division takes a few hundred cycles of a call's
+// first look-ups, this a few.
+struct Divisor {
+    uint32_t mul;
+    int shift;
+};
+inline Divisor divide_by(uint32_t d) {
+    int up = 0;
+    while (((uint64_t)1 << up) < d) ++up;
+    return {(uint32_t)((((uint64_t)1 << (31 + up)) + d - 1) / d), 31 + up};
+}
+
 // One attention call over SeqKV.
 struct SeqAttn {
     SeqKV kv;
@@ -42,7 +55,8 @@ struct SeqAttn {
     int tokens, Hq, G, causal, max_q_len;
     int64_t q_stride;
     float scale_log2;            // scale * log2(e)
-    void* ws;                    // attn_ws_bytes() bytes
+    Divisor by_group, by_heads, by_page;   // G, kv heads, page_size
+    void* ws;                    // attn_rows_ws_bytes() / attn_tc_ws_bytes() bytes
     int* err_word;
 };
 
@@ -52,7 +66,7 @@ size_t attn_rows_ws_bytes(int D);
 cudaError_t launch_attn_rows(const SeqAttn& p, sfa_dtype dtype, int num_sms, cudaStream_t stream);
 
 // Tensor-core path (two tiles of 128 rows of one kv head per CTA): groups of
-// up to 128 heads; packed rows, or 16-bit pages of a multiple of 16 tokens.
+// up to 128 heads, packed rows or pages of any size.
 bool attn_tc_supported(const SeqKV& kv, int G);
 size_t attn_tc_ws_bytes(int G, int D);
 cudaError_t launch_attn_tc(const SeqAttn& p, sfa_dtype dtype, int num_sms, cudaStream_t stream);
@@ -64,6 +78,7 @@ cudaError_t launch_paged_read(const SeqKV& kv, const int32_t* cu, int tokens, sf
                               void* k_out, void* v_out, cudaStream_t stream);
 
 #ifdef __CUDACC__
+__device__ __forceinline__ int over(int x, Divisor d) { return (int)(((uint64_t)(uint32_t)x * d.mul) >> d.shift); }
 // Rows [first, last) of sequence b in packed rows described by cu, clamped to
 // [0, rows].
 __device__ __forceinline__ int2 seq_rows(const int32_t* cu, int b, int rows) {

@@ -114,6 +114,9 @@ sfa_status run_attention(SeqAttn& p, int num_tokens, int num_qo_heads, int max_q
     p.max_q_len = max_q_len > 0 && max_q_len < num_tokens ? max_q_len : num_tokens;
     p.q_stride = q_stride;
     p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)p.kv.D)) * kLog2e;
+    p.by_group = divide_by(p.G);
+    p.by_heads = divide_by(p.kv.Hkv);
+    p.by_page = divide_by(p.kv.page_table ? p.kv.page_size : 1);
     p.ws = ws;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err;
