@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -221,7 +222,10 @@ PyObject* py_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
 }
 
 struct Outputs {
-    at::Tensor out, lse, ws;
+    at::Tensor out, lse;
+    at::DataPtr own;              // the workspace, unless one is given
+    void* ws;
+    size_t ws_bytes;
     Outputs(const at::Tensor& q, PyObject* o, PyObject* l, PyObject* w, bool want_lse, size_t need) {
         const at::Device dev = q.device();
         out = output(maybe(o, "out"), "out", q.sizes(), q.scalar_type(), dev);
@@ -230,9 +234,12 @@ struct Outputs {
         const at::Tensor* gw = maybe(w, "workspace");
         if (gw) {
             expect(gw->device() == dev && gw->is_contiguous(), "workspace: a contiguous tensor on q's device expected");
-            ws = *gw;
+            ws = gw->data_ptr();
+            ws_bytes = gw->nbytes();
         } else {
-            ws = fresh({(int64_t)need}, at::kByte, dev);
+            own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+            ws = own.get();
+            ws_bytes = need;
         }
     }
     float* lse_ptr() const { return lse.defined() ? lse.data_ptr<float>() : nullptr; }
@@ -259,7 +266,7 @@ PyObject* py_paged(PyObject*, PyObject* const* o, Py_ssize_t n) {
     if (st != SFA_OK) return Py_BuildValue("(iOO)", st, Py_None, Py_None);
     const Outputs r(q, o[13], o[14], o[15], truth(o[11]), need);
     st = fn.run(&c, q.const_data_ptr(), qs, cu, T, Hq, hint, (float)scale, truth(o[7]), (sfa_dtype)t,
-                r.out.data_ptr(), r.lse_ptr(), r.ws.data_ptr(), r.ws.nbytes(), on.stream);
+                r.out.data_ptr(), r.lse_ptr(), r.ws, r.ws_bytes, on.stream);
     return wrap(st, r.out, r.lse);
     SFA_LEAVE
 }
@@ -290,7 +297,7 @@ PyObject* py_varlen(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const Outputs r(q, o[9], o[10], o[11], truth(o[7]), need);
     st = fn.varlen(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qs, ks, vs, cq, ck, B, T, N, Hq, Hkv,
                    (int)D, hint, (float)scale, truth(o[6]), (sfa_dtype)t, r.out.data_ptr(), r.lse_ptr(),
-                   r.ws.data_ptr(), r.ws.nbytes(), on.stream);
+                   r.ws, r.ws_bytes, on.stream);
     return wrap(st, r.out, r.lse);
     SFA_LEAVE
 }
