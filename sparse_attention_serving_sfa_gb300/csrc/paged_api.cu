@@ -63,28 +63,28 @@ bool bad_stride(int64_t stride, int heads, int D) {
 // 16-row tiles read the keys at HBM's pace and begin early; the 128-row
 // tensor-core tiles stand mostly empty with few rows, but more rows cost them
 // nothing.  So 16-row tiles take (times: 16-row tiles, 128-row tiles; head_dim
-// 128)
-//   - up to kFewRows rows a kv head (by the longest sequence): 16 rows, 64
-//     sequences of 4,096 keys, 8 kv heads 175 and 171 us, one sequence of 8,192
-//     keys 17.5 and 22.8 us; but 32 rows, 64 sequences 334 and 173 us.  Over an
-//     8-bit cache, which 128-row tiles must convert first, twice as many: 16
-//     rows 104 and 227 us, 32 rows 188 and 231 us, 64 rows 355 and 235 us.
-//   - where they are few and read few keys over again: 32 rows of one sequence,
-//     8 kv heads (16 tiles), of 8,192 keys 20.5 and 22.5 us, of 2,000 keys 14.2
-//     and 18.0 us, but of 65,536 keys 89 and 57 us; 64 rows, 2 kv heads (8
-//     tiles), 8,192 keys 17.5 and 37.7 us; 4 sequences of 500 keys, 64 tiles
-//     14.4 and 12.1 us.  8-bit: one sequence of 8,192 keys, 8 kv heads, 96 rows
-//     (48 tiles) 27.9 and 28.0 us, 128 rows 33.8 and 28.3 us; 4 of 16,384 keys,
-//     2 kv heads, 64 rows (32 tiles) 34.8 and 31.5 us.
-constexpr int kFewRows = 16, kFewTiles = 16;
-constexpr int64_t kFewReads = 1 << 17;               // tiles x keys, by what the table or the packed rows can hold
-
+// 128, 8 kv heads unless said otherwise)
+//   - up to 16 rows a kv head (by the longest sequence): 16 rows, 64 sequences
+//     of 4,096 keys 174 and 171 us, one sequence of 8,192 keys 15.4 and 22.7 us;
+//     but 32 rows, 64 sequences 333 and 173 us.  Over an 8-bit cache, which
+//     128-row tiles must convert first, up to 32: 16 rows, 64 sequences 93 and
+//     226 us, 32 rows 170 and 230 us, 48 rows 245 and 232 us.
+//   - where they are few and read few keys over again.  One sequence, 48 rows
+//     (24 tiles): of 2,000 keys 12.5 and 18.2 us, of 8,192 keys 19.9 and 22.8 us,
+//     of 65,536 keys 85 and 58 us; 96 rows (48 tiles) of 8,192 keys 29.0 and
+//     23.5 us.  2 kv heads, 128 rows (16 tiles) of 8,192 keys 16.8 and 40.1 us.  4
+//     sequences of 500 keys, 64 tiles 11.3 and 12.2 us, 128 tiles 13.6 and 12.3
+//     us.  8-bit: one sequence of 8,192 keys, 128 rows (64 tiles) 27.7 and 28.5
+//     us; 4 of 16,384 keys, 2 kv heads, 64 rows (32 tiles) 28.2 and 31.7 us, 96
+//     rows 36.3 and 32.2 us; 16 of 1,000 keys, 2 kv heads, 128 tiles 15.2 and 18.5
+//     us, 192 tiles 19.6 and 19.2 us.
 bool few_rows(const SeqAttn& p) {
     const bool f8 = p.kv.f8 != 0;
     const int64_t rows = (int64_t)p.max_q_len * p.G;
     const int64_t tiles = (rows + 15) / 16 * p.kv.num_seqs * p.kv.Hkv;
+    // (keys: what the table or the packed rows can hold, the lengths are on the device)
     const int64_t keys = p.kv.page_table ? (int64_t)p.kv.max_pages * p.kv.page_size : p.kv.rows;
-    return rows <= (f8 ? 2 : 1) * kFewRows || (tiles <= (f8 ? 4 : 1) * kFewTiles && tiles * keys <= (f8 ? 3 : 2) * kFewReads);
+    return rows <= (f8 ? 32 : 16) || (tiles <= (f8 ? 128 : 64) && tiles * keys <= (f8 ? 524288 : 196608));
 }
 
 // Workspace of either path.

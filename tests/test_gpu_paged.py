@@ -213,15 +213,19 @@ def test_paged_attention(shape, cache, layout, dtype):
             check_paged(c, out, lse, causal)
 
 
+def widen(c):
+    """A page table with room for a million tokens: the large tiles take what has more than 32 rows."""
+    c.table = torch.cat([c.table, torch.full((len(c.q_lens), (1 << 20) // c.page), -1, dtype=torch.int32)], 1)
+
+
 @pytest.mark.parametrize("cache,layout,dtype", [("same", "NHD", "bf16"), ("e4m3", "HND", "f16"),
                                                 ("e5m2", "NHD", "bf16")])
 @pytest.mark.parametrize("shape", [1, 2, 3, 4, 6, 9, 10])
 def test_table_much_wider_than_the_sequences(shape, cache, layout, dtype):
-    """A table made for a million tokens: small calls on the large tiles too."""
     q_lens, kv_lens, heads, kv_heads, dim, page = SHAPES[shape]
     c = P.Cache(200 + shape, q_lens, kv_lens, heads, kv_heads, dim, page, dtype, cache, layout,
                 before=1, behind=2).poison()
-    c.table = torch.cat([c.table, torch.full((len(q_lens), (1 << 20) // page), -1, dtype=torch.int32)], 1)
+    widen(c)
     out, lse = run_paged(c, True, 0)
     check_paged(c, out, lse, True)
 
@@ -269,21 +273,23 @@ def test_out_at_any_16_bytes(hint, q_lens):
 
 
 @pytest.mark.parametrize("cache", ["same", "e4m3"])
-@pytest.mark.parametrize("hint", [1, 0])
-def test_pages_out_of_range_are_absent(cache, hint):
+@pytest.mark.parametrize("hint,wide", [(1, False), (0, False), (0, True)])
+def test_pages_out_of_range_are_absent(cache, hint, wide):
     c = P.Cache(21, [1, 70, 3], [90, 200, 64], 8, 2, 128, 16, "bf16", cache).poison()
     c.table[0, 2] = c.pages
     c.table[1, 0] = -1
     c.table[1, 5] = 1 << 30
     c.table[2] = -5                          # nothing left: +0 and -inf
+    if wide:
+        widen(c)
     out, lse = run_paged(c, True, hint)
     check_paged(c, out, lse, True)
     assert torch.isneginf(lse[-5:-2] if c.cu[-1] < c.T else lse[c.cu[2]:]).all()
 
 
 @pytest.mark.parametrize("dtype,cache", [("bf16", "same"), ("f16", "same"), ("bf16", "e4m3"), ("bf16", "e5m2")])
-@pytest.mark.parametrize("hint", [1, 0])
-def test_large_scores_and_scales(dtype, cache, hint):
+@pytest.mark.parametrize("hint,wide", [(1, False), (0, False), (0, True)])
+def test_large_scores_and_scales(dtype, cache, hint, wide):
     """Scores in the hundreds, growing along the keys (the running maximum
     moves at every step), rows of q of very different size."""
     c = P.Cache(22, [6, 1, 40], [700, 333, 600], 8, 2, 128, 16, dtype, cache)
@@ -293,6 +299,8 @@ def test_large_scores_and_scales(dtype, cache, hint):
         page, place = c.cells(b)
         if cache == "same":
             c.k[page, place] *= torch.linspace(0.01, 3, len(page)).to(c.k.dtype)[:, None, None]
+    if wide:
+        widen(c)
     for scale in (0.0, 1.0):
         out, lse = run_paged(c, True, hint, scale)
         check_paged(c, out, lse, True, scale)
