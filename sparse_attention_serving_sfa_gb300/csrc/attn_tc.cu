@@ -1158,14 +1158,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 // Block (x, y) joins rows 32 y .. 32 y + 31 of the parts of the item that range
 // x cuts first: lane = row, each warp some of the dims; the result crosses over
 // in shared memory to be written row by row.  (Finding the cuts here again took
-// longer than joining: 16 us where nothing was cut.)
+// longer than joining: 16 us where nothing was cut.)  Most blocks have nothing
+// to do, so what counts is how many fit an SM: 512 threads, or 4 parts in flight at
+// 118 registers, took 3 to 6 and 1 to 2 us longer.
 constexpr int kMergeThreads = 256;
 
 template <class E, int D>
-__global__ void __launch_bounds__(kMergeThreads) attn_tc_merge(const TcParams p) {
+__global__ void __launch_bounds__(kMergeThreads, 4) attn_tc_merge(const TcParams p) {
     constexpr int kWarps = kMergeThreads / 32;
     constexpr int Q = D / 4 / kWarps;                    // 4-dim groups of a warp
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 2;
     __shared__ uint2 turn[32][D / 4 + 1];
     const SeqAttn& a = p.a;
     const float kPShift = std::is_same<E, BF16>::value && a.kv.f8 == 0 ? 0.f : 7.f;
