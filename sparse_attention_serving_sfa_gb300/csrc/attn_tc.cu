@@ -52,11 +52,11 @@
 // conversion ...); short items by the way from one barrier to the next.  Two
 // tiles of a CTA hide the one behind the other; 208 registers a softmax thread
 // hold a row's 128 scores, so that S is read from TMEM once.  Measured: one
-// causal prompt of 16,384 tokens, 32/8 heads of 128, 1.40 to 1.52 ms, 1.45 to
-// 1.57 PFLOP/s (0.86 to 0.93 of a sustained library product's rate); chunks of
+// causal prompt of 16,384 tokens, 32/8 heads of 128, 1.38 to 1.52 ms, 1.45 to
+// 1.59 PFLOP/s (0.85 to 0.94 of a sustained library product's rate); chunks of
 // 200 to 1,024 tokens over up to 8,192 keys in 32-token pages 203 us, 1.24
-// PFLOP/s; over E4M3 pages 389 us, 1.08 PFLOP/s; 40 prompts of up to 700
-// tokens, 12/4 heads of 64, 31.5 us.
+// PFLOP/s; over E4M3 pages 386 to 417 us, 1.01 to 1.09 PFLOP/s; 40 prompts of up to
+// 700 tokens, 12/4 heads of 64, 31.3 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -1343,8 +1343,8 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
     while ((1 << p.box_shift) < p.box) ++p.box_shift;
     p.by_unit = divide_by(2 * p.TR);
     p.ctas_mul = ~uint64_t(0) / (uint64_t)(num_sms < kMaxCtas ? num_sms : kMaxCtas) + 1;
-    // Measured (320 / 448 / 576 / 768): chunks of 200 to 1,024 tokens over 16-bit
-    // pages 236 / 223 / 215 / 219 us; 64-dim prompts of up to 700 tokens (192 / 320 /
+    // Measured, with the joins slower than now (320 / 448 / 576 / 768): chunks of 200
+    // to 1,024 tokens over 16-bit pages 236 / 223 / 215 / 219 us; 64-dim prompts of up to 700 tokens (192 / 320 /
     // 448) 38.4 / 36.2 / 36.2 us; chunks over E4M3 pages (384 / 512 / 640) 454 / 448 /
     // 445 us.  A step of 128 keys takes about 2,700 cycles (64-dim 2,400, 8-bit 3,900).
     p.charge = a.kv.f8 ? 640 : (a.kv.D == 128 ? 576 : 448);

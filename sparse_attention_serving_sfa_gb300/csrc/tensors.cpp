@@ -154,7 +154,7 @@ struct On {
     }
 };
 
-// Straight from torch's allocator: through the dispatcher each of a call's three
+// Straight from torch's allocator: through the dispatcher each of a call's
 // tensors took about half a microsecond more.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType t, at::Device dev) {
     return at::Tensor(at::detail::empty_cuda(shape, t, dev, std::nullopt));
