@@ -257,6 +257,41 @@ def test_few_rows_cut_into_parts(q_lens, kv_lens, heads, kv_heads, dim, page, ca
         check_paged(c, out, lse, True)
 
 
+@pytest.mark.parametrize("cache,dtype", [("same", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("decode", [True, False])
+def test_many_sequences_sharing_pages(decode, cache, dtype):
+    """More sequences than a warp has lanes, some without rows or keys; every
+    other one reads its neighbour's pages (a shared prefix)."""
+    B = 70
+    q_lens = [1 if decode else (0 if b % 7 == 3 else 1 + (b * 37) % 120) for b in range(B)]
+    kv_lens = [0 if b % 11 == 5 else 1 + (b * 53) % 400 for b in range(B)]
+    c = P.Cache(43, q_lens, kv_lens, 8, 2, 64, 16, dtype, cache, behind=3).poison()
+    for b in range(0, B - 1, 2):
+        n = -(-min(kv_lens[b], kv_lens[b + 1]) // 16)
+        c.table[b + 1, :n] = c.table[b, :n]
+    # a place poisoned for one sequence and read by the other is cleared
+    for x in (c.k, c.v):
+        y = x.view(torch.uint8) if cache != "same" else x
+        bad = (y == 0x7F) if cache != "same" else ~torch.isfinite(y)
+        for b in range(1, B, 2):
+            page, place = c.cells(b)
+            z = y[page, place]
+            z[bad[page, place]] = 0
+            y[page, place] = z
+    for hint in (max(q_lens), 0):
+        out, lse = run_paged(c, True, hint)
+        check_paged(c, out, lse, True)
+
+
+@pytest.mark.parametrize("cache,dtype", [("same", "f16"), ("e4m3", "bf16"), ("e5m2", "f16")])
+@pytest.mark.parametrize("group", [65, 127, 128, 129])
+def test_large_groups(group, cache, dtype):
+    c = P.Cache(44, [9, 30], [200, 131], group, 1, 128, 16, dtype, cache).poison()
+    for hint in (0, 1):
+        out, lse = run_paged(c, True, hint)
+        check_paged(c, out, lse, True)
+
+
 @pytest.mark.parametrize("hint,q_lens", [(1, [1, 1]), (0, [40, 70])])
 def test_out_at_any_16_bytes(hint, q_lens):
     """An out that begins 16 bytes behind a 32-byte border."""
