@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             const int key = key0(st) + lane;
             if (st >= nsteps || lane >= KS || key >= kv_len) return -1;
             if constexpr (!PAGED) return 0;
-            return p.kv.page_table[(int64_t)b * p.kv.max_pages + over(key, p.by_page)];
+            return p.kv.page_table[(int64_t)b * p.kv.max_pages + over(key, p.kv.by_page)];
         };
         auto issue = [&](int st, int page) {
             if (PAGED && (unsigned)page >= (unsigned)p.kv.num_pages) page = -1;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                 int64_t ko = -1, vo = -1;
                 if (page >= 0) {
                     if constexpr (PAGED) {
-                        ko = (int64_t)page * p.kv.s_page + (int64_t)(key - over(key, p.by_page) * p.kv.page_size) * p.kv.s_tok;
+                        ko = (int64_t)page * p.kv.s_page + (int64_t)(key - over(key, p.kv.by_page) * p.kv.page_size) * p.kv.s_tok;
                     } else {
                         ko = (int64_t)(sq.k_row + key) * p.kv.s_tok;
                         vo = (int64_t)(sq.k_row + key) * p.kv.sv_tok;

@@ -173,7 +173,7 @@ __device__ __forceinline__ int units(const TcParams& p, int x) {
 
 // x / page_size
 __device__ __forceinline__ int page_slot(const TcParams& p, int x) {
-    return over(x, p.a.by_page);
+    return over(x, p.a.kv.by_page);
 }
 
 __device__ __forceinline__ Seq seq_of(const TcParams& p, int b) {

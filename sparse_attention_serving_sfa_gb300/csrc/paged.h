@@ -9,6 +9,19 @@
 
 namespace sfa {
 
+// x / d = x * mul >> shift for 0 <= x < 2^31 (the multiplier rounded up at
+// 2^(31 + ceil(log2 d))): a division takes a few hundred cycles of a call's
+// first look-ups, this a few.
+struct Divisor {
+    uint32_t mul;
+    int shift;
+};
+inline Divisor divide_by(uint32_t d) {
+    int up = 0;
+    while (((uint64_t)1 << up) < d) ++up;
+    return {(uint32_t)((((uint64_t)1 << (31 + up)) + d - 1) / d), 31 + up};
+}
+
 // Keys and values of a batch of sequences.  Token j of sequence b lies
 //   paged  (page_table set): in page page_table[b][j / page_size], place
 //          j % page_size, kv_lens[b] tokens in all;
@@ -25,25 +38,13 @@ struct SeqKV {
     const int32_t* cu_k;         // [num_seqs + 1]
     int num_seqs, num_pages, page_size, max_pages, rows;   // rows: packed rows of k / v
     int Hkv, D;
+    Divisor by_page;                 // page_size
     int64_t s_page, s_tok, s_head;   // of k, and of v when paged
     int64_t sv_tok, sv_head;         // of v when packed
     int f8;                          // 0: 16-bit, 1: E4M3, 2: E5M2
     const float* scale_k;            // [Hkv] or NULL (= 1)
     const float* scale_v;
 };
-
-// x / d = x * mul >> shift for 0 <= x < 2^31 (the multiplier rounded up at
-// 2^(31 + ceil(log2 d))): a division takes a few hundred cycles of a call's
-// first look-ups, this a few.
-struct Divisor {
-    uint32_t mul;
-    int shift;
-};
-inline Divisor divide_by(uint32_t d) {
-    int up = 0;
-    while (((uint64_t)1 << up) < d) ++up;
-    return {(uint32_t)((((uint64_t)1 << (31 + up)) + d - 1) / d), 31 + up};
-}
 
 // One attention call over SeqKV.
 struct SeqAttn {
@@ -55,7 +56,7 @@ struct SeqAttn {
     int tokens, Hq, G, causal, max_q_len;
     int64_t q_stride;
     float scale_log2;            // scale * log2(e)
-    Divisor by_group, by_heads, by_page;   // G, kv heads, page_size
+    Divisor by_group, by_heads;  // G, kv heads
     void* ws;                    // attn_rows_ws_bytes() / attn_tc_ws_bytes() bytes
     int* err_word;
 };

@@ -52,6 +52,7 @@ sfa_status resolve_cache(const paged_kv* c, SeqKV& kv) {
     kv.s_head = c->kv_layout == SFA_KV_LAYOUT_NHD ? D : P * D;
     kv.f8 = is16(c->dtype) ? 0 : (c->dtype == SFA_DTYPE_E4M3 ? 1 : 2);
     kv.scale_k = c->scale_k; kv.scale_v = c->scale_v;
+    kv.by_page = divide_by(c->page_size);
     return SFA_OK;
 }
 
@@ -116,7 +117,6 @@ sfa_status run_attention(SeqAttn& p, int num_tokens, int num_qo_heads, int max_q
     p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)p.kv.D)) * kLog2e;
     p.by_group = divide_by(p.G);
     p.by_heads = divide_by(p.kv.Hkv);
-    p.by_page = divide_by(p.kv.page_table ? p.kv.page_size : 1);
     p.ws = ws;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err;
