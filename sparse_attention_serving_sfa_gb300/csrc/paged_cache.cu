@@ -13,11 +13,12 @@
 // elements measured slower on most calls: 47.4 -> 50.6 and 54.9 us for 261 MB
 // read back.)  The sequence of a warp's first token is found by a 32-way search
 // of cu (one load per factor of 32 in the number of sequences), then each lane
-// walks to its own token's.  Measured: 261 MB read back from E4M3 pages 48 us
-// (5.4 TB/s, 0.80 of the measured copy rate); 12,800 tokens of 8 heads of 128
-// quantised into E4M3 pages 17.9 us (4.4 TB/s), 12,500 of 4 heads of 64 copied
-// into 24-token pages 6.6 us (from and into L2); a decode step's 64 tokens 3.1
-// us, a launch's latency.
+// walks to its own token's.  Measured: 261 MB read back from E4M3 pages 49 us
+// (5.3 TB/s, 0.78 of the measured copy rate; streaming stores: 49.7 without);
+// 12,800 tokens of 8 heads of 128 quantised into E4M3 pages 16.4 us (4.8 TB/s;
+// 17.9 at half the warps an SM), 12,500 of 4 heads of 64 copied into 24-token
+// pages 6.5 us (from and into L2); a decode step's 64 tokens 2.8 us, a launch's
+// latency.
 //
 // Rounding to codes: x times the scale's rounded reciprocal is within 2 units
 // in the last place of the quotient.  A border between two codes has 19 zero
@@ -37,7 +38,7 @@
 namespace sfa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;   // (256: a decode step 2.85 instead of 2.75 us)
 constexpr int kVec = 16;   // elements of a thread's piece
 
 // Number of entries of cu[1 .. B] that are <= t: the sequence holding row t
@@ -127,7 +128,7 @@ __device__ __forceinline__ void decode16(uint4 c, float s, uint4 (&y)[2]) {
 
 // F8: 0 the pools hold E's 16-bit elements, 1 E4M3, 2 E5M2.
 template <class E, int F8, bool READ>
-__global__ void __launch_bounds__(kThreads, READ ? 8 : 6)     // (6: 17.9 -> 17.0 us for 12,800 tokens against 4)
+__global__ void __launch_bounds__(kThreads, READ ? 16 : 12)
 paged_move_kernel(const SeqKV kv, const void* src_k, const void* src_v, void* dst_k, void* dst_v,
                   int64_t k_stride, int64_t v_stride, const int32_t* cu, int tokens, Divisor by_token) {
     grid_dependency_wait();
@@ -180,8 +181,8 @@ paged_move_kernel(const SeqKV kv, const void* src_k, const void* src_v, void* ds
         }
         uint4* ok = reinterpret_cast<uint4*>(static_cast<char*>(dst_k) + ((int64_t)t * k_stride + h * kv.D + d) * 2);
         uint4* ov = reinterpret_cast<uint4*>(static_cast<char*>(dst_v) + ((int64_t)t * v_stride + h * kv.D + d) * 2);
-        ok[0] = k[0]; ok[1] = k[1];
-        ov[0] = v[0]; ov[1] = v[1];
+        __stcs(ok, k[0]); __stcs(ok + 1, k[1]);
+        __stcs(ov, v[0]); __stcs(ov + 1, v[1]);
     } else {
         if (at < 0) return;
         uint4* ok = reinterpret_cast<uint4*>(static_cast<char*>(dst_k) + cell * EB);
