@@ -54,9 +54,9 @@
 // hold a row's 128 scores, so that S is read from TMEM once.  Measured: one
 // causal prompt of 16,384 tokens, 32/8 heads of 128, 1.38 to 1.52 ms, 1.45 to
 // 1.59 PFLOP/s (0.85 to 0.94 of a sustained library product's rate); chunks of
-// 200 to 1,024 tokens over up to 8,192 keys in 32-token pages 203 us, 1.24
+// 200 to 1,024 tokens over up to 8,192 keys in 32-token pages 200 us, 1.25
 // PFLOP/s; over E4M3 pages 386 to 417 us, 1.01 to 1.09 PFLOP/s; 40 prompts of up to
-// 700 tokens, 12/4 heads of 64, 31.3 us.
+// 700 tokens, 12/4 heads of 64, 30.9 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -76,7 +76,7 @@ constexpr int kMoveWarp = 12, kMovers = 128; // the movers: warps 12 to 15
 constexpr int kTmemCols = 512, kTileCols = 256, kOCol = 128;
 constexpr float kRescale = 8.0f;            // log2 units
 constexpr int kItemRows = 2 * kTileM;
-constexpr int kMinShare = 2;                // fewest steps of a part
+constexpr int kMinShare = 2;                // fewest steps of a part (1: 8 prompts of 300 tokens 22.7 instead of 14.9 us)
 // Pages of a multiple of this many tokens come by TMA, others row by row.  8
 // sequences' chunks of 512 tokens over 4,096 keys, 32/8 heads of 128: 16-bit
 // pages of 32 tokens 192 us, of 16 218, of 8 317 (row by row 299); E4M3 pages of
@@ -1343,11 +1343,12 @@ cudaError_t launch_attn_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaS
     while ((1 << p.box_shift) < p.box) ++p.box_shift;
     p.by_unit = divide_by(2 * p.TR);
     p.ctas_mul = ~uint64_t(0) / (uint64_t)(num_sms < kMaxCtas ? num_sms : kMaxCtas) + 1;
-    // Measured, with the joins slower than now (320 / 448 / 576 / 768): chunks of 200
-    // to 1,024 tokens over 16-bit pages 236 / 223 / 215 / 219 us; 64-dim prompts of up to 700 tokens (192 / 320 /
-    // 448) 38.4 / 36.2 / 36.2 us; chunks over E4M3 pages (384 / 512 / 640) 454 / 448 /
-    // 445 us.  A step of 128 keys takes about 2,700 cycles (64-dim 2,400, 8-bit 3,900).
-    p.charge = a.kv.f8 ? 640 : (a.kv.D == 128 ? 576 : 448);
+    // Measured (448 / 576): chunks of 200 to 1,024 tokens over 16-bit pages 199.8 /
+    // 202.0 us, 4 causal prompts of 2,048 tokens 139.6 / 145.5 us; 64-dim ones (320 /
+    // 448) 101.2 / 103.8 us, prompts of up to 700 tokens 30.9 / 31.2 us; chunks over
+    // E4M3 pages (512 / 640) 399 / 394 us.  A step of 128 keys takes about 2,700
+    // cycles (64-dim 2,400, 8-bit 3,900).
+    p.charge = a.kv.f8 ? 640 : (a.kv.D == 128 ? 448 : 320);
     p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.ws_o = static_cast<float*>(a.ws);
     p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;
