@@ -488,12 +488,12 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
     static_assert(kMovers == kStep, "a thread a row number");
     uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::rows);
     const bool tma = F8 && p.box >= kMinBox8;                     // staging tiles filled by the loader's TMA
-    int loads = 0, tables = 0;
+    int loads = 0, meetings = 0, steps = 0;    // tiles, barrier phases, steps of the items before
     bool ok = true;
-    // both movers are here (with what they wrote to shared memory)
+    // the four mover warps are here (with what they wrote to shared memory)
     auto together = [&]() -> bool {
         arrive(B_ROWS);
-        return all(mbar_wait(bar(B_ROWS), tables++ & 1, err, abort_flag));
+        return all(mbar_wait(bar(B_ROWS), meetings++ & 1, err, abort_flag));
     };
     for (int number = 0; ok; ++number) {
         Item it;
@@ -510,15 +510,19 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
             const int key = (s0 + st) * kStep + x;
             ahead = st < n && key < kv_len ? table[page_slot(p, key)] : -1;
         };
-        // Row numbers (in units of D elements) of step st's keys.  (The table
-        // of a step is written over two steps later: by then every thread
-        // has passed the barrier of the step between, after its last read.)
+        // Row numbers (in units of D elements) of step st's keys, in the two
+        // tables by turns over all steps of the range, whatever the item: a
+        // table is written again two steps later, and by then every warp has
+        // met the others in the step between, after its last read.  (Turns
+        // that began anew with each item would write the table that a slower
+        // warp still reads for the last step of an odd number.)
+        auto table_of = [&](int st) { return rows + ((steps + st) & 1) * kStep; };
         auto find_rows = [&](int st) -> bool {
             const int key = (s0 + st) * kStep + x, place = key - page_slot(p, key) * a.kv.page_size;
             const uint32_t pg = (uint32_t)ahead;
-            rows[(st & 1) * kStep + x] = pg >= (uint32_t)a.kv.num_pages ? 0xffffffffu
-                                         : p.hnd ? (pg * a.kv.Hkv + h) * a.kv.page_size + place
-                                                 : (pg * a.kv.page_size + place) * a.kv.Hkv + h;
+            table_of(st)[x] = pg >= (uint32_t)a.kv.num_pages ? 0xffffffffu
+                              : p.hnd ? (pg * a.kv.Hkv + h) * a.kv.page_size + place
+                                      : (pg * a.kv.page_size + place) * a.kv.Hkv + h;
             return together();
         };
         auto wait_free = [&](int load) {
@@ -529,7 +533,7 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
         auto copy = [&](int y, int load) -> bool {
             if (y < 2 * n) {
                 const int st = y >> 1;
-                // (here, too: both have read what the staging tile held)
+                // (here, too: all have read what the staging tile held)
                 if (!(y & 1)) {
                     if (!find_rows(st)) return false;
                     look_up(st + 1);
@@ -540,11 +544,12 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
                 const char* src = static_cast<const char*>((y & 1) ? a.kv.v : a.kv.k);
                 unsigned char* stage = smem + L::staging + (load & 1) * kStep * D;
                 unsigned char* slot = smem + L::ring + (load % L::slots) * L::tile;
+                const uint32_t* row_of = table_of(st);
                 const int ch = x % PR;
                 // kMovers / PR rows at a time, a row's pieces side by side
 #pragma unroll 8
                 for (int r = x / PR; r < kStep; r += kMovers / PR) {
-                    const uint32_t row = rows[(st & 1) * kStep + r];
+                    const uint32_t row = row_of[r];
                     const bool in = row != 0xffffffffu;
                     unsigned char* dst = F8 ? stage + staged<D>(r, ch)
                                             : slot + (ch >> 3) * L::panel + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
@@ -613,6 +618,7 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
             arrive(B_FULL + loads % L::slots);
             ++loads;
         }
+        steps += n;
     }
     cp_async_wait<0>();
 }

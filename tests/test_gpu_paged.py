@@ -241,6 +241,23 @@ def test_chunks_over_pages_of_any_size(page, dim, cache, layout, dtype):
         check_paged(c, out, lse, True)
 
 
+@pytest.mark.parametrize("cache,dtype,dim", [("same", "f16", 128), ("same", "bf16", 64), ("e5m2", "f16", 128)])
+@pytest.mark.parametrize("page,steps", [(20, (1,)), (24, (1, 3)), (20, (1, 3, 5)), (12, (1, 2, 3, 4))])
+def test_many_short_items_over_gathered_pages(page, steps, cache, dtype, dim):
+    """Pages fetched row by row, items of odd numbers of 128-key steps one after
+    the other in every block: the same bits at every call."""
+    B = 96
+    kv_lens = [128 * steps[b % len(steps)] - (b * 29) % 100 for b in range(B)]
+    q_lens = [min(20 + (b * 17) % 41, n) for b, n in enumerate(kv_lens)]
+    c = P.Cache(60, q_lens, kv_lens, 32, 8, dim, page, dtype, cache).poison()
+    d = c.to("cuda")
+    out, lse = run_paged(c, True, max(q_lens), d=d)
+    check_paged(c, out, lse, True)
+    for _ in range(20):
+        again, lse2 = run_paged(c, True, max(q_lens), d=d)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("cache,dtype", [("same", "bf16"), ("same", "f16"), ("e4m3", "bf16"), ("e5m2", "f16")])
 @pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,dim,page", [
     ([12], [6000], 8, 2, 128, 16),                  # three tiles a head, cut into many parts
