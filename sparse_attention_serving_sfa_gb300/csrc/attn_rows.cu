@@ -33,7 +33,10 @@
 //
 // P is carried to P.V as a 16-bit high part plus the 16-bit rounding of the
 // remainder (two MMAs; the tensor pipe is idle most of the time here), the
-// 8-bit cache's in fp16 alone (2^-12, its V are exact in fp16).  8-bit K / V
+// 8-bit cache's in fp16 alone (its V are exact in fp16): at most half a step,
+// 2^-11 of a weight.  fp16 P carries a factor 2^7 (at most 2^15 in all, as m lags
+// by up to 2^8), so a weight below 2^-21 of the one at m, where fp16's steps no
+// longer shrink, is off by at most 2^-32 of that one.  8-bit K / V
 // become fp16 in registers (exact); q is then scaled by a power of two per row
 // to a largest magnitude in [8, 16) so that bf16 q fits fp16 (elements below
 // 2^-28 of the row's largest round), and the power leaves with the scores.
@@ -58,6 +61,11 @@ constexpr int kCharge = 2;           // a tile's fixed cost, in chunks
 // instead of 4.8 us, a join's launch.)
 constexpr int kMinCut = 4;
 constexpr float kRescale = 8.f;      // log2 growth of m that rescales O
+
+// log2 of the factor that P, and with it O and the sums, carries: in fp16 the
+// small weights of many keys would be lost without.
+template <class E, int F8>
+constexpr float kPShift = F8 || std::is_same<E, F16>::value ? 7.f : 0.f;
 
 template <int D, int F8>
 struct RowsCfg {
@@ -493,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                 }
             }
             // a row that has seen no key has only -inf scores: subtracting 0 gives P = 0
-            const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+            constexpr float kShift = kPShift<E, F8>;
+            const float z0 = m0 == -INFINITY ? 0.f : m0 - kShift, z1 = m1 == -INFINITY ? 0.f : m1 - kShift;
             // ---- P, O += P V ----
 #pragma unroll
             for (int ks = 0; ks < KS / 16; ++ks) {
@@ -629,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                     *reinterpret_cast<uint2*>(dst + 32 * i) =
                         none ? make_uint2(0u, 0u)
                              : make_uint2(E::pack2(acc[i].x * inv, acc[i].y * inv), E::pack2(acc[i].z * inv, acc[i].w * inv));
-                if (p.lse && (tid & 7) == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
+                if (p.lse && (tid & 7) == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L) - kPShift<E, F8>) * kLn2;
             } else {
                 const int slot = 2 * blockIdx.x + (c0 == 0 ? 1 : 0);
                 float* dst = ws_o + ((int64_t)slot * kRows + r) * D + d0;
@@ -721,7 +730,7 @@ __global__ void __launch_bounds__(32 * kRows, 1) attn_rows_merge(const SeqAttn p
 #pragma unroll
         for (int k = 0; k < W; k += 2)
             *reinterpret_cast<uint32_t*>(out + k) = none ? 0u : E::pack2(acc[k] * inv, acc[k + 1] * inv);
-        if (p.lse && lane == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
+        if (p.lse && lane == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L) - kPShift<E, F8>) * kLn2;
     }
 }
 
