@@ -932,8 +932,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             const int lim = a.causal && valid ? max(0, min(it.kv_len, tok + it.kv_len - it.n_q + 1)) : it.kv_len;
             const int lim_min = __reduce_min_sync(0xffffffffu, lim);
             float rs = a.scale_log2;
-            if constexpr (F8)
-                if (a.kv.scale_k) rs *= a.kv.scale_k[it.h];
             if constexpr (kScaledQ) {
                 // This thread's row of q as fp16, scaled by 2^-e.  (The last
                 // Q.K^T that read the tile was done before the S of the item
@@ -969,6 +967,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     if (lane == 0) mbar_arrive(bar(B_Q + t));
                     rs *= __uint_as_float((uint32_t)(127 + e) << 23);
                 }
+            }
+            if constexpr (F8) {
+                if (a.kv.scale_k) rs *= a.kv.scale_k[it.h];
+                // Scores are masked before they are scaled, and -inf * 0 is NaN:
+                // where the product of the scales underflows the smallest number
+                // serves, under which every score is still nothing.
+                rs = fmaxf(rs, __uint_as_float(1u));
             }
             float m_used = -INFINITY, l = 0.f;
             // Pages of the boxes (runs of p.box keys that no page border cuts)

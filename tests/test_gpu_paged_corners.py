@@ -38,3 +38,17 @@ def test_many_small_weights_next_to_large_ones(q_lens, kv_lens, hint, cache, dty
     c.k, c.v = k.to(c.k.dtype), v.to(c.v.dtype)
     out, lse = run_paged(c, True, hint, math.log(2))
     check_paged(c, out, lse, True, math.log(2))
+
+
+@pytest.mark.parametrize("cache,dtype,dim", [("e4m3", "bf16", 128), ("e4m3", "f16", 64), ("e5m2", "bf16", 64),
+                                             ("e5m2", "f16", 128)])
+@pytest.mark.parametrize("hint", [1, 0])
+def test_scales_whose_product_underflows(hint, cache, dtype, dim):
+    """scale * scale_k is 0 in fp32: visible keys weigh the same, masked ones and
+    those of a missing page nothing."""
+    c = P.Cache(62, [3, 150, 40], [200, 333, 40], 8, 2, dim, 16, dtype, cache)
+    c.scale_k *= 1e-30
+    c.table[1, 3] = c.pages
+    for causal in (True, False):
+        out, lse = run_paged(c, causal, hint, 1e-20)
+        check_paged(c, out, lse, causal, 1e-20)
