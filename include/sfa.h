@@ -548,8 +548,9 @@ typedef struct {
  * Into an 8-bit cache the value x of kv head h is written as the code nearest
  * to x / scale[h] (exact quotient, ties to even, saturating to the largest
  * finite value; NaN stays NaN), into a 16-bit cache unchanged.  A token whose
- * position is negative or behind the page table is not written.  Two rows of
- * one call must not name the same place.
+ * position is negative is not written.  (A kv_len beyond the page table is read
+ * as the table's end, here as in attention: the newest tokens then take the
+ * table's last places.)  Two rows of one call must not name the same place.
  * Errors: SFA_ERR_INVALID_ARG / SFA_ERR_UNSUPPORTED before any launch.
  */
 sfa_status paged_append(const paged_kv* cache, const void* k_new, const void* v_new,

@@ -1,7 +1,7 @@
 // Writing a paged KV cache and reading it back.
 //
 // append: row t of sequence b (cu[b] <= t < cu[b + 1]) is token
-//     pos = kv_lens[b] - (cu[b + 1] - t)
+//     pos = kv_lens[b] - (cu[b + 1] - t)       (lists clamped to the sizes given)
 // and goes to page page_table[b][pos / P], place pos % P, either as it is or as
 //     code = sat(rne(x / scale[head]))           (E4M3 / E5M2);
 // read: x = code * scale[head], rounded once to 16 bits.  Both move every
@@ -59,15 +59,17 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int B, int t) {
     return min(lo, B);
 }
 
-// Element offset of token row t's place (head 0) in the pools, or -1.
-__device__ __forceinline__ int64_t place_of(const SeqKV& kv, const int32_t* cu, int b, int t) {
+// Element offset of token row t's place (head 0) in the pools, or -1.  Lists
+// are read as attention reads them (seq_rows, seq_keys), so that a row is the
+// same token to both.
+__device__ __forceinline__ int64_t place_of(const SeqKV& kv, const int32_t* cu, int b, int t, int tokens) {
     if (b >= kv.num_seqs || t < cu[b]) return -1;
-    const int64_t pos = (int64_t)kv.kv_lens[b] - ((int64_t)cu[b + 1] - t);
-    if (pos < 0 || pos >= (int64_t)kv.max_pages * kv.page_size) return -1;
-    const int slot = over((int)pos, kv.by_page);
+    const int pos = seq_keys(kv, b).y - (seq_rows(cu, b, tokens).y - t);
+    if (pos < 0) return -1;
+    const int slot = over(pos, kv.by_page);
     const int page = kv.page_table[(int64_t)b * kv.max_pages + slot];
     if ((unsigned)page >= (unsigned)kv.num_pages) return -1;
-    return page * kv.s_page + (pos - (int64_t)slot * kv.page_size) * kv.s_tok;
+    return page * kv.s_page + (pos - slot * kv.page_size) * kv.s_tok;
 }
 
 __device__ __forceinline__ float quotient(float x, float s) {
@@ -159,7 +161,7 @@ paged_move_kernel(const SeqKV kv, const void* src_k, const void* src_v, void* ds
     int b = find_seq(cu, kv.num_seqs, token_of(first));
     if (t >= tokens) return;
     while (b < kv.num_seqs && cu[b + 1] <= t) ++b;
-    const int64_t at = place_of(kv, cu, b, t);
+    const int64_t at = place_of(kv, cu, b, t, tokens);
     const int64_t cell = at + h * kv.s_head + d;
     const float sk = F8 && kv.scale_k ? kv.scale_k[h] : 1.f;
     const float sv = F8 && kv.scale_v ? kv.scale_v[h] : 1.f;

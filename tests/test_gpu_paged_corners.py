@@ -52,3 +52,43 @@ def test_scales_whose_product_underflows(hint, cache, dtype, dim):
     for causal in (True, False):
         out, lse = run_paged(c, causal, hint, 1e-20)
         check_paged(c, out, lse, causal, 1e-20)
+
+
+@pytest.mark.parametrize("cache,dtype,layout", [("same", "bf16", "NHD"), ("e4m3", "f16", "HND")])
+@pytest.mark.parametrize("T,behind", [(12, 0), (15, 3)])
+def test_lists_are_read_as_clamped(T, behind, cache, dtype, layout):
+    """Rows said to lie behind the last, lengths behind the table or negative: append,
+    read and attention take the lists as clamped, and so mean the same tokens."""
+    # what the lists come to
+    c = P.Cache(63, [4, 2, 6], [40, 0, 96], 8, 2, 64, 16, dtype, cache, layout, behind=behind)
+    c.table = c.table[:, :6].contiguous()               # 96 tokens and no more
+    d = c.to("cuda")
+    # (the rows behind the last sequence are no rows of it, unless the list says so)
+    d["cu"] = torch.tensor([-2, 4, 6, 12 if behind else 19], dtype=torch.int32, device="cuda")
+    d["lens"] = torch.tensor([40, -7, 99], dtype=torch.int32, device="cuda")
+    assert c.T == T
+    _, k, v = c.split(d["qkv"])
+    sfa.paged_append(k, v, d["cu"], d["k"], d["v"], d["table"], d["lens"], **kw(c, d))
+    for x, n, scale in ((1, "k", c.scale_k), (2, "v", c.scale_v)):
+        pool = getattr(c, n)
+        w = raw(pool).clone()
+        w = w.transpose(1, 2) if layout == "HND" else w
+        for b in (0, 2):
+            new = c.split(c.qkv)[x][c.cu[b]: c.cu[b + 1]]
+            page, place = (y[-c.q_lens[b]:] for y in c.cells(b))
+            w[page, place] = (new.contiguous().view(torch.int16) if cache == "same" else
+                              P.nearest_code(new.double() / scale.double().view(1, -1, 1), cache))
+        w = w.transpose(1, 2) if layout == "HND" else w
+        assert torch.equal(raw(d[n]), w)
+        setattr(c, n, d[n].cpu())
+    got = sfa.paged_read(d["k"], d["v"], d["table"], d["lens"], d["cu"], c.T, dtype=dtype, **kw(c, d))
+    h = torch.finfo(P.TORCH[dtype]).eps / 2
+    for x, pool, scale in ((got[0].cpu(), c.k, c.scale_k), (got[1].cpu(), c.v, c.scale_v)):
+        assert torch.all(x[4:6] == 0)
+        for b in (0, 2):
+            want = c.values(pool, scale, b)[0][c.kv_lens[b] - c.q_lens[b]:]
+            err = (x[c.cu[b]: c.cu[b + 1]].double() - want).abs()
+            assert torch.all(err <= (h + 2.0 ** -24) * (1 + h) * want.abs() + 2.0 ** -25)
+    for hint in (1, 0):
+        out, lse = run_paged(c, True, hint, d=d)
+        check_paged(c, out, lse, True)
