@@ -38,8 +38,9 @@
 // by up to 2^8), so a weight below 2^-21 of the one at m, where fp16's steps no
 // longer shrink, is off by at most 2^-32 of that one.  8-bit K / V
 // become fp16 in registers (exact); q is then scaled by a power of two per row
-// to a largest magnitude in [8, 16) so that bf16 q fits fp16 (elements below
-// 2^-28 of the row's largest round), and the power leaves with the scores.
+// to a largest magnitude in [2^14, 2^15), so that bf16 q fits fp16: elements
+// down to 2^-31 of the row's largest are exact, smaller ones off by at most
+// 2^-39 of it.  The power leaves with the scores.
 #include <type_traits>
 
 #include "common.cuh"
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                     // exponent of the row's largest, kept where both 2^x and 2^-x are normal
                     auto expo = [](float a) {
                         const int e = (int)((__float_as_uint(a) >> 23) & 255u) - 127;
-                        return (a == 0.f || e > 127) ? 0 : min(max(e - 3, -120), 120);
+                        return (a == 0.f || e > 127) ? 0 : max(e - 14, -120);
                     };
                     const int e0 = expo(a0), e1 = expo(a1);
                     const float f0 = __uint_as_float((uint32_t)(127 - e0) << 23);

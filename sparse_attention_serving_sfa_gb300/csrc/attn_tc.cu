@@ -34,8 +34,9 @@
 // TMEM: tile t at column 256 t: S / P in [0, 128), O in [128, 128 + D).
 //
 // With an 8-bit cache both products run in fp16.  bf16 rows of q are scaled to
-// a largest magnitude in [8, 16) by a power of two each (elements below 2^-28
-// of the row's largest round), which leaves with the scores.
+// a largest magnitude in [2^14, 2^15) by a power of two each, which leaves with
+// the scores: elements down to 2^-31 of the row's largest are exact, smaller
+// ones off by at most 2^-39 of it.
 //
 // P is rounded once to 16 bits (at most half a step of the output's type per
 // weight, so the output moves by no more than its own rounding of
@@ -950,7 +951,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
                     const int e8 = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
-                    const int e = (top == 0.f || e8 > 127) ? 0 : min(max(e8 - 3, -120), 120);
+                    const int e = (top == 0.f || e8 > 127) ? 0 : max(e8 - 14, -120);
                     const float f = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
                     for (int c = 0; c < D / 2; ++c) {

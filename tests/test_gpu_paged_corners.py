@@ -92,3 +92,17 @@ def test_lists_are_read_as_clamped(T, behind, cache, dtype, layout):
     for hint in (1, 0):
         out, lse = run_paged(c, True, hint, d=d)
         check_paged(c, out, lse, True)
+
+
+@pytest.mark.parametrize("cache,dim", [("e4m3", 128), ("e5m2", 64)])
+@pytest.mark.parametrize("hint", [1, 0])
+def test_small_elements_of_a_row_beside_a_large_one(hint, cache, dim):
+    """bf16 rows over an 8-bit cache whose scores come from elements 2^-24 of the
+    largest, which meets zeros."""
+    c = P.Cache(64, [2, 90, 60], [300, 333, 500], 8, 2, dim, 16, "bf16", cache)
+    q, _, _ = c.split(c.qkv)
+    q *= 2.0 ** -24
+    q[:, :, 0] = 1
+    c.k.view(torch.uint8)[..., 0] = 0
+    out, lse = run_paged(c, True, hint, 2.0 ** 23)
+    check_paged(c, out, lse, True, 2.0 ** 23)
