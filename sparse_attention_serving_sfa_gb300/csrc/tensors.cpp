@@ -154,6 +154,16 @@ struct On {
     }
 };
 
+// The interpreter lock is let go while outputs are allocated and kernels
+// launched: both can wait for the GPU (a full launch queue, say), and what they
+// wait for can be a host function on a stream that needs the lock.
+struct Unlocked {
+    PyThreadState* held = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(held); }
+};
+
 // Straight from torch's allocator: through the dispatcher each of a call's
 // tensors took about half a microsecond more.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType t, at::Device dev) {
@@ -189,10 +199,14 @@ PyObject* py_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
            "k_new and v_new: one shape and type, on the pools' device, expected");
     const int64_t ks = rows(k, "k_new", c.num_kv_heads, c.head_dim), vs = rows(v, "v_new", c.num_kv_heads, c.head_dim);
     const int32_t* cu = list(tensor(o[2], "cu_seqlens"), "cu_seqlens", dev, (int64_t)c.num_seqs + 1);
-    const int t = type_code(k.scalar_type());
+    const int t = type_code(k.scalar_type()), T = count(k.size(0), "tokens");
     On on(dev, o[10]);
-    return PyLong_FromLong(fn.append(&c, k.const_data_ptr(), v.const_data_ptr(), ks, vs, cu,
-                                     count(k.size(0), "tokens"), (sfa_dtype)t, on.stream));
+    int st;
+    {
+        Unlocked here;
+        st = fn.append(&c, k.const_data_ptr(), v.const_data_ptr(), ks, vs, cu, T, (sfa_dtype)t, on.stream);
+    }
+    return PyLong_FromLong(st);
     SFA_LEAVE
 }
 
@@ -215,27 +229,37 @@ PyObject* py_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
                                                                   : at::kBFloat16;
     On on(dev, o[12]);
     const int64_t shape[3] = {T, c.num_kv_heads, c.head_dim};
-    const at::Tensor k = output(gk, "out", shape, t, dev), v = output(gv, "out", shape, t, dev);
-    const int st = fn.read(&c, cu, T, (sfa_dtype)type_code(t), k.data_ptr(), v.data_ptr(), on.stream);
+    at::Tensor k, v;
+    int st;
+    {
+        Unlocked here;
+        k = output(gk, "out", shape, t, dev);
+        v = output(gv, "out", shape, t, dev);
+        st = fn.read(&c, cu, T, (sfa_dtype)type_code(t), k.data_ptr(), v.data_ptr(), on.stream);
+    }
     return wrap(st, k, v);
     SFA_LEAVE
 }
 
+// Outputs and workspace of an attention call: out, lse, workspace as given.
 struct Outputs {
+    const at::Tensor *given_out, *given_lse, *given_ws;
+    bool want_lse;
     at::Tensor out, lse;
     at::DataPtr own;              // the workspace, unless one is given
-    void* ws;
-    size_t ws_bytes;
-    Outputs(const at::Tensor& q, PyObject* o, PyObject* l, PyObject* w, bool want_lse, size_t need) {
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
+    Outputs(PyObject* const* o, bool want)
+        : given_out(maybe(o[0], "out")), given_lse(maybe(o[1], "lse")), given_ws(maybe(o[2], "workspace")), want_lse(want) {}
+    void make(const at::Tensor& q, size_t need) {
         const at::Device dev = q.device();
-        out = output(maybe(o, "out"), "out", q.sizes(), q.scalar_type(), dev);
-        const at::Tensor* gl = maybe(l, "lse");
-        if (gl || want_lse) lse = output(gl, "lse", q.sizes().slice(0, 2), at::kFloat, dev);
-        const at::Tensor* gw = maybe(w, "workspace");
-        if (gw) {
-            expect(gw->device() == dev && gw->is_contiguous(), "workspace: a contiguous tensor on q's device expected");
-            ws = gw->data_ptr();
-            ws_bytes = gw->nbytes();
+        out = output(given_out, "out", q.sizes(), q.scalar_type(), dev);
+        if (given_lse || want_lse) lse = output(given_lse, "lse", q.sizes().slice(0, 2), at::kFloat, dev);
+        if (given_ws) {
+            expect(given_ws->device() == dev && given_ws->is_contiguous(),
+                   "workspace: a contiguous tensor on q's device expected");
+            ws = given_ws->data_ptr();
+            ws_bytes = given_ws->nbytes();
         } else {
             own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
             ws = own.get();
@@ -260,13 +284,18 @@ PyObject* py_paged(PyObject*, PyObject* const* o, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) throw python_error();
     const int T = count(q.size(0), "tokens"), Hq = count(q.size(1), "heads"), hint = count(o[12], "max_q_len");
     const int t = type_code(q.scalar_type());
+    const bool causal = truth(o[7]);
+    Outputs r(o + 13, truth(o[11]));
     On on(dev, o[16]);
     size_t need = 0;
     int st = fn.ws_size(c.num_seqs, T, Hq, c.num_kv_heads, c.head_dim, &need);
     if (st != SFA_OK) return Py_BuildValue("(iOO)", st, Py_None, Py_None);
-    const Outputs r(q, o[13], o[14], o[15], truth(o[11]), need);
-    st = fn.run(&c, q.const_data_ptr(), qs, cu, T, Hq, hint, (float)scale, truth(o[7]), (sfa_dtype)t,
-                r.out.data_ptr(), r.lse_ptr(), r.ws, r.ws_bytes, on.stream);
+    {
+        Unlocked here;
+        r.make(q, need);
+        st = fn.run(&c, q.const_data_ptr(), qs, cu, T, Hq, hint, (float)scale, causal, (sfa_dtype)t,
+                    r.out.data_ptr(), r.lse_ptr(), r.ws, r.ws_bytes, on.stream);
+    }
     return wrap(st, r.out, r.lse);
     SFA_LEAVE
 }
@@ -290,14 +319,19 @@ PyObject* py_varlen(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const int B = count(lq.numel() - 1, "num_seqs"), T = count(q.size(0), "tokens"), Hq = count(q.size(1), "heads");
     const int N = count(k.size(0), "keys"), Hkv = count(k.size(1), "heads"), hint = count(o[8], "max_q_len");
     const int t = type_code(q.scalar_type());
+    const bool causal = truth(o[6]);
+    Outputs r(o + 9, truth(o[7]));
     On on(dev, o[12]);
     size_t need = 0;
     int st = fn.ws_size(B, T, Hq, Hkv, (int)D, &need);
     if (st != SFA_OK) return Py_BuildValue("(iOO)", st, Py_None, Py_None);
-    const Outputs r(q, o[9], o[10], o[11], truth(o[7]), need);
-    st = fn.varlen(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qs, ks, vs, cq, ck, B, T, N, Hq, Hkv,
-                   (int)D, hint, (float)scale, truth(o[6]), (sfa_dtype)t, r.out.data_ptr(), r.lse_ptr(),
-                   r.ws, r.ws_bytes, on.stream);
+    {
+        Unlocked here;
+        r.make(q, need);
+        st = fn.varlen(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qs, ks, vs, cq, ck, B, T, N, Hq, Hkv,
+                       (int)D, hint, (float)scale, causal, (sfa_dtype)t, r.out.data_ptr(), r.lse_ptr(),
+                       r.ws, r.ws_bytes, on.stream);
+    }
     return wrap(st, r.out, r.lse);
     SFA_LEAVE
 }

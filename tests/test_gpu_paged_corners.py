@@ -1,6 +1,8 @@
 """Corners of the paged cache and of the attention over it on the GPU, against
 plain 64-bit arithmetic."""
+import ctypes
 import math
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -106,3 +108,54 @@ def test_small_elements_of_a_row_beside_a_large_one(hint, cache, dim):
     c.k.view(torch.uint8)[..., 0] = 0
     out, lse = run_paged(c, True, hint, 2.0 ** 23)
     check_paged(c, out, lse, True, 2.0 ** 23)
+
+
+def test_the_interpreter_lock_is_let_go():
+    """While the library runs, other Python threads can: its entry points, stood in
+    for by the function that tells whether the calling thread holds the lock."""
+    lib, native = sfa.load(), sfa._native()
+    held = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    size = ctypes.cast(lib.paged_workspace_size, ctypes.c_void_p).value
+    c = P.Cache(65, [3, 4], [20, 30], 4, 2, 64, 16, "f16")
+    d = c.to("cuda")
+    q, k, v = c.split(d["qkv"])
+    pools = d["k"], d["v"], d["table"], d["lens"]
+    native.bind(held, held, held, size, held)
+    try:                                    # status 1 (held) would raise
+        sfa.paged_append(k, v, d["cu"], *pools)
+        sfa.paged_read(*pools, d["cu"], c.T)
+        sfa.paged_attention(q, *pools, d["cu"])
+        sfa.varlen_attention(q, k, v, d["cu"], d["cu"])
+    finally:
+        native.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
+                      (lib.paged_append, lib.paged_read, lib.paged_run, lib.paged_workspace_size, lib.varlen_run)])
+
+
+@pytest.mark.parametrize("hint", [1, 0])
+def test_calls_from_several_threads(hint):
+    """Threads with a stream each: every one gets what it gets alone."""
+    cases = [P.Cache(70 + i, [1 + 40 * i, 70, 9], [900, 400 + i, 33], 8, 2, 128, 16, "f16", "e4m3") for i in range(4)]
+    dev = [c.to("cuda") for c in cases]
+    for c, d in zip(cases, dev):
+        sfa.paged_append(*c.split(d["qkv"])[1:], d["cu"], d["k"], d["v"], d["table"], d["lens"], **kw(c, d))
+        c.k, c.v = d["k"].cpu(), d["v"].cpu()
+    torch.cuda.synchronize()
+
+    def work(i):
+        c, d = cases[i], dev[i]
+        q, k, v = c.split(d["qkv"])
+        stream = torch.cuda.Stream()
+        got = []
+        with torch.cuda.stream(stream):
+            for _ in range(30):
+                sfa.paged_append(k, v, d["cu"], d["k"], d["v"], d["table"], d["lens"], **kw(c, d))
+                got.append(sfa.paged_attention(q, d["k"], d["v"], d["table"], d["lens"], d["cu"], max_q_len=hint,
+                                               return_lse=True, **kw(c, d)))
+        stream.synchronize()
+        return got
+    with ThreadPoolExecutor(len(cases)) as pool:
+        results = list(pool.map(work, range(len(cases))))
+    for c, got in zip(cases, results):
+        check_paged(c, got[0][0].cpu(), got[0][1].cpu(), True)
+        for out, lse in got[1:]:
+            assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
