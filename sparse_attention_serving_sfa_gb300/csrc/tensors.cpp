@@ -222,6 +222,7 @@ PyObject* py_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
     expect(T >= 0, "num_tokens: not negative");
     const at::Tensor *gk = maybe(o[10], "out"), *gv = maybe(o[11], "out");
     const long want = integer(o[6]);
+    expect(want == -1 || want == SFA_DTYPE_F16 || want == SFA_DTYPE_BF16, "dtype: f16 or bf16 expected");
     const at::ScalarType t = want == SFA_DTYPE_F16                ? at::kHalf
                              : want == SFA_DTYPE_BF16             ? at::kBFloat16
                              : gk                                 ? gk->scalar_type()

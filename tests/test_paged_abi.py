@@ -164,3 +164,10 @@ def test_python_checks_of_attention():
             sfa.varlen_attention(*bad, t["cu"], t["cu"])
     with pytest.raises(ValueError):
         sfa.paged_read(t["k"], t["v"], t["table"], t["lens"], t["cu"].long(), 4)
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "e5m2", 7, 4])
+def test_read_refuses_types_it_does_not_write(dtype):
+    t = tensors()
+    with pytest.raises(ValueError, match="dtype"):
+        sfa.paged_read(t["k"], t["v"], t["table"], t["lens"], t["cu"], 4, dtype=dtype)
