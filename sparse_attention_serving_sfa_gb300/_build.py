@@ -1,12 +1,15 @@
 """Builds libsfa_gb300.so from csrc/*.cu with nvcc for sm_103a, and the module
 _tensors (csrc/tensors.cpp: argument marshalling for torch tensors) with g++
-against the installed torch's headers (both in-tree)."""
+against the installed torch's headers (both in-tree).  The library needs nvcc
+alone: where the module cannot be built, a warning says why and the calls that
+need it raise."""
 from __future__ import annotations
 
 import concurrent.futures
 import glob
 import os
 import subprocess
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -76,17 +79,26 @@ def build_tensors() -> str:
            "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
+        if os.path.exists(out):
+            os.remove(out)              # an older module may not fit the library
         raise RuntimeError(f"g++ failed on tensors.cpp:\n{r.stderr}")
     os.replace(tmp, out)
     return out
 
 
+def _try_tensors(force: bool) -> None:
+    try:
+        if force or tensors_stale():
+            build_tensors()
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"the library is built, the module for calls on torch tensors is not: {e}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every kernel source (in parallel) and link the shared library;
-    compile the _tensors module beside it."""
+    compile the _tensors module beside it, if it can be."""
     if not force and not stale():
-        if tensors_stale():
-            build_tensors()
+        _try_tensors(False)
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -102,10 +114,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        tensors = ex.submit(build_tensors) if force or tensors_stale() else None
+        tensors = ex.submit(_try_tensors, force)
         results = list(ex.map(compile_one, _sources()))
-        if tensors is not None:
-            tensors.result()
+        tensors.result()
     if verbose:
         for _, log in results:
             print(log)

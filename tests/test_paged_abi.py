@@ -171,3 +171,17 @@ def test_read_refuses_types_it_does_not_write(dtype):
     t = tensors()
     with pytest.raises(ValueError, match="dtype"):
         sfa.paged_read(t["k"], t["v"], t["table"], t["lens"], t["cu"], 4, dtype=dtype)
+
+
+@pytest.mark.parametrize("error", [RuntimeError("g++ failed"), FileNotFoundError("g++"), ImportError("torch")])
+def test_library_builds_without_the_module_for_torch(monkeypatch, error):
+    """The C library's users need neither g++ nor Python's headers."""
+    from sparse_attention_serving_sfa_gb300 import _build
+
+    def fails():
+        raise error
+    monkeypatch.setattr(_build, "stale", lambda: False)
+    monkeypatch.setattr(_build, "tensors_stale", lambda: True)
+    monkeypatch.setattr(_build, "build_tensors", fails)
+    with pytest.warns(UserWarning, match="torch"):
+        assert _build.build() == _build.LIB_PATH
