@@ -159,3 +159,62 @@ def test_calls_from_several_threads(hint):
         check_paged(c, got[0][0].cpu(), got[0][1].cpu(), True)
         for out, lse in got[1:]:
             assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("cache,dtype,layout,page", [("e4m3", "bf16", "NHD", 16), ("e5m2", "f16", "HND", 20)])
+@pytest.mark.parametrize("have", ["", "k", "v"])
+def test_eight_bits_without_scales(have, cache, dtype, layout, page):
+    """No scale, or one of the two: the codes of the other are the values."""
+    c = P.Cache(66, [5, 180, 90], [70, 300, 400], 8, 2, 128, page, dtype, cache, layout)
+    for n in "kv":
+        if n not in have:
+            setattr(c, f"scale_{n}", None)
+            pool = getattr(c, n)
+            setattr(c, n, (pool.float() / 64).to(pool.dtype))       # values of ordinary size
+    d = c.to("cuda")
+    _, k, v = c.split(d["qkv"])
+    sfa.paged_append(k, v, d["cu"], d["k"], d["v"], d["table"], d["lens"], **kw(c, d))
+    for x, n, scale in ((1, "k", c.scale_k), (2, "v", c.scale_v)):
+        w = raw(getattr(c, n)).clone()
+        w = w.transpose(1, 2) if layout == "HND" else w
+        for b, m in enumerate(c.q_lens):
+            new = c.split(c.qkv)[x][c.cu[b]: c.cu[b + 1]].double()
+            page_, place = (y[-m:] for y in c.cells(b))
+            w[page_, place] = P.nearest_code(new if scale is None else new / scale.double().view(1, -1, 1), cache)
+        assert torch.equal(raw(d[n]), w.transpose(1, 2) if layout == "HND" else w)
+        setattr(c, n, d[n].cpu())
+    got = sfa.paged_read(d["k"], d["v"], d["table"], d["lens"], d["cu"], c.T, dtype=dtype, **kw(c, d))
+    h = torch.finfo(P.TORCH[dtype]).eps / 2
+    for x, pool, scale in ((got[0].cpu(), c.k, c.scale_k), (got[1].cpu(), c.v, c.scale_v)):
+        for b, m in enumerate(c.q_lens):
+            want = c.values(pool, scale, b)[0][c.kv_lens[b] - m:]
+            err = (x[c.cu[b]: c.cu[b + 1]].double() - want).abs()
+            assert torch.all(err <= (h + 2.0 ** -24) * (1 + h) * want.abs() + 2.0 ** -25)
+    for hint in (1, 0):
+        out, lse = run_paged(c, True, hint, d=d)
+        check_paged(c, out, lse, True)
+
+
+@pytest.mark.parametrize("hint,page", [(1, 64), (0, 64), (0, 20)])
+def test_eight_bit_pools_beyond_32_bits(hint, page):
+    """Pools of more than 2^32 codes, the pages used at their far end."""
+    H, D = 8, 128
+    c = P.Cache(67, [2, 70], [100, 400], 32, H, D, page, "bf16", "e4m3")
+    d = c.to("cuda")
+    pages = (1 << 32) // (H * D * page) + c.pages + 1
+    shift = pages - c.pages
+    for n in "kv":
+        big = torch.empty((pages, page, H, D), dtype=torch.uint8, device="cuda")
+        big[shift:] = d[n].view(torch.uint8)
+        d[n] = big.view(torch.float8_e4m3fn)
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + shift, d["table"])
+    _, k, v = c.split(d["qkv"])
+    sfa.paged_append(k, v, d["cu"], d["k"], d["v"], d["table"], d["lens"], **kw(c, d))
+    c.k, c.v = (d[n].view(torch.uint8)[shift:].view(torch.float8_e4m3fn).cpu() for n in "kv")
+    ko, vo = sfa.paged_read(d["k"], d["v"], d["table"], d["lens"], d["cu"], c.T, **kw(c, d))
+    for x, new, scale in ((ko, k, c.scale_k), (vo, v, c.scale_v)):
+        y = P.nearest_code(new.cpu().double() / scale.double().view(1, -1, 1), "e4m3").view(torch.float8_e4m3fn)
+        want = (y.float() * scale.view(1, -1, 1)).bfloat16()
+        assert torch.equal(x.cpu(), want)
+    out, lse = run_paged(c, True, hint, d=d)
+    check_paged(c, out, lse, True)
