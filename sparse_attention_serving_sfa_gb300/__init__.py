@@ -500,7 +500,8 @@ def sparse_flash_attention(query, key, value, sparse_indices, scale, layout="BSN
 # paged_read, paged_attention and varlen_attention take torch tensors; the module
 # _tensors checks what the C entry points cannot see (shapes, strides, element
 # types, devices: ValueError) and calls them on the tensors' device, on torch's
-# current stream of that device unless `stream` is given.
+# current stream of that device unless `stream` is given (new outputs are then
+# that stream's memory, as inside torch.cuda.stream(stream)).
 
 _tensors = None
 

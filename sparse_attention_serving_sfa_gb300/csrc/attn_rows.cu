@@ -12,9 +12,10 @@
 // Bound: HBM, each cached K / V row of a kv head read once per 16-row tile;
 // over an 8-bit cache also the issue slots of the conversions; a small batch by
 // latency (two launches, three dependent look-ups).  Measured: 64 sequences of
-// 2,000 to 8,192 keys, 32/8 heads of 128, bf16 183 us, 6.5 TB/s (0.96 of the
-// measured copy rate); 16 of 3,001 to 65,536 keys, 64/8 heads, E4M3 114 to 126
-// us, 5.2 to 5.8 TB/s; 4 of 100 to 1,024 keys 8.0 us.
+// 2,000 to 8,192 keys, 32/8 heads of 128, bf16 183 to 186 us, 6.4 to 6.5 TB/s
+// (0.94 to 0.96 of the measured copy rate); 16 of 3,001 to 65,536 keys, 64/8
+// heads, E4M3 114 to 127 us, 5.2 to 5.8 TB/s; 4 of 100 to 1,024 keys 8 us on the
+// device.
 // All tiles lie on one line, each as long as its chunks plus a fixed charge
 // for what a tile costs besides, and the line is cut into equal ranges, one
 // per CTA (two CTAs per SM), whatever the mix of lengths.  A cut falls on a

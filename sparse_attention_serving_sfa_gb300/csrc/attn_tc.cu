@@ -48,16 +48,17 @@
 // turn 0 x NaN into NaN: where TMA brought them the loader waits for such a
 // tile itself, writes zeros over those rows and then hands it on.
 //
-// Bound: the tensor pipe and the softmax's issue slots, which take turns (4 D
-// operations a score against one exp2, one subtraction, a max, half a
-// conversion ...); short items by the way from one barrier to the next.  Two
-// tiles of a CTA hide the one behind the other; 208 registers a softmax thread
-// hold a row's 128 scores, so that S is read from TMEM once.  Measured: one
-// causal prompt of 16,384 tokens, 32/8 heads of 128, 1.38 to 1.52 ms, 1.45 to
-// 1.59 PFLOP/s (0.85 to 0.94 of a sustained library product's rate); chunks of
-// 200 to 1,024 tokens over up to 8,192 keys in 32-token pages 200 us, 1.25
-// PFLOP/s; over E4M3 pages 386 to 417 us, 1.01 to 1.09 PFLOP/s; 40 prompts of up to
-// 700 tokens, 12/4 heads of 64, 30.9 us.
+// Bound: the way from one barrier to the next.  S, softmax, P and P.V of a step
+// follow one another; two tiles of a CTA hide the one behind the other, and
+// still nothing is busy throughout (tensor pipe, issue slots, exponentials' unit:
+// long prompt 72%, 41%, 36%; chunks over 16-bit pages 60%, 40%, 30%, over E4M3
+// 48%, 44%, 24%, whose conversion takes slots; short prompts 12%, 23%, 13%).  208
+// registers a softmax thread hold a row's 128 scores, so that S is read from
+// TMEM once.  Measured: one causal prompt of 16,384 tokens, 32/8 heads of 128,
+// 1.38 to 1.53 ms, 1.43 to 1.59 PFLOP/s (0.85 to 0.94 of a sustained library
+// product's rate); chunks of 200 to 1,024 tokens over up to 8,192 keys in
+// 32-token pages 200 to 214 us, 1.17 to 1.25 PFLOP/s; over E4M3 pages 386 to 417
+// us, 1.01 to 1.09 PFLOP/s; 40 prompts of up to 700 tokens, 12/4 heads of 64, 31 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -80,8 +81,8 @@ constexpr int kItemRows = 2 * kTileM;
 constexpr int kMinShare = 2;                // fewest steps of a part (1: 8 prompts of 300 tokens 22.7 instead of 14.9 us)
 // Pages of a multiple of this many tokens come by TMA, others row by row.  8
 // sequences' chunks of 512 tokens over 4,096 keys, 32/8 heads of 128: 16-bit
-// pages of 32 tokens 192 us, of 16 218, of 8 317 (row by row 299); E4M3 pages of
-// 16 tokens 296 us, of 8 302 (row by row 431).
+// pages of 32 tokens 195 us, of 16 217, of 8 317 (row by row 302); E4M3 pages of
+// 16 tokens 290 us, of 8 300 (row by row 415).
 constexpr int kMinBox = 16, kMinBox8 = 8;
 constexpr int kMinRange = kStep;            // shortest range of a CTA, in keys
 constexpr int kMaxCtas = 160;               // ranges (the workspace's size goes by it)

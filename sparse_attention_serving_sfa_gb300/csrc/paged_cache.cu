@@ -4,21 +4,21 @@
 //     pos = kv_lens[b] - (cu[b + 1] - t)       (lists clamped to the sizes given)
 // and goes to page page_table[b][pos / P], place pos % P, either as it is or as
 //     code = sat(rne(x / scale[head]))           (E4M3 / E5M2);
-// read: x = code * scale[head], rounded once to 16 bits.  Both move every
-// element once: bound by HBM (read 2 bytes, write 1 or 2 per element of K and
-// of V).  A thread moves 16 consecutive elements of a head's row of K and of V
+// read: x = code * scale[head] in fp32, rounded to 16 bits.  Both move every
+// element once (read 2 bytes, write 1 or 2 per element of K and of V).  A thread moves 16 consecutive elements of a head's row of K and of V
 // (two 16-byte loads each, and one 16-byte store each for 8-bit codes), so a
 // warp covers 512 elements of a token and the loads of K and V are in flight
 // together.  (Two pieces a thread, of one token or of several, and pieces of 8
 // elements measured slower on most calls: 47.4 -> 50.6 and 54.9 us for 261 MB
 // read back.)  The sequence of a warp's first token is found by a 32-way search
 // of cu (one load per factor of 32 in the number of sequences), then each lane
-// walks to its own token's.  Measured: 261 MB read back from E4M3 pages 49 us
-// (5.3 TB/s, 0.78 of the measured copy rate; streaming stores: 49.7 without);
-// 12,800 tokens of 8 heads of 128 quantised into E4M3 pages 16.4 us (4.8 TB/s;
-// 17.9 at half the warps an SM), 12,500 of 4 heads of 64 copied into 24-token
-// pages 6.5 us (from and into L2); a decode step's 64 tokens 2.8 us, a launch's
-// latency.
+// walks to its own token's.  Measured: 261 MB read back from E4M3 pages 48 to
+// 49 us (5.3 to 5.4 TB/s, 0.79 to 0.80 of the measured copy rate), bound by HBM;
+// 12,800 tokens of 8 heads of 128 quantised into E4M3 pages 16.2 to 16.5 us (4.8
+// TB/s; 17.9 at half the warps an SM), bound by nothing alone: issue slots 68%
+// and the ALUs 60% busy, HBM 39%, half the warps waiting for memory; 12,500 of 4
+// heads of 64 copied into 24-token pages 6.2 us (from and into L2); a decode
+// step's 64 tokens 2.9 to 3.1 us, a launch's latency.
 //
 // Rounding to codes: x times the scale's rounded reciprocal is within 2 units
 // in the last place of the quotient.  A border between two codes has 19 zero
@@ -38,7 +38,7 @@
 namespace sfa {
 namespace {
 
-constexpr int kThreads = 128;   // (256: a decode step 2.85 instead of 2.75 us)
+constexpr int kThreads = 128;   // (256: a decode step 0.1 us longer)
 constexpr int kVec = 16;   // elements of a thread's piece
 
 // Number of entries of cu[1 .. B] that are <= t: the sequence holding row t
