@@ -561,8 +561,8 @@ sfa_status paged_append(const paged_kv* cache, const void* k_new, const void* v_
  * paged_read -- the newest cu_seqlens[b + 1] - cu_seqlens[b] tokens of every
  * sequence b (all of them with cu_seqlens the running sum of kv_lens) back as
  * packed rows: the fp32 product code * scale[h], rounded to `dtype`, or a
- * 16-bit cache's elements as they are.  Tokens without a place (a negative position, a page
- * out of range) are written as zeros.
+ * 16-bit cache's elements as they are.  Tokens without a place (a negative
+ * position, a page out of range) are written as zeros.
  *   k_out, v_out  device (num_tokens, num_kv_heads, head_dim) of `dtype`.
  */
 sfa_status paged_read(const paged_kv* cache, const int32_t* cu_seqlens, int num_tokens,
@@ -596,16 +596,16 @@ sfa_status varlen_workspace_size(int num_seqs, int num_tokens, int num_qo_heads,
  *              overlap on the GPU (other streams, graphs replayed side by
  *              side) need one each.
  * Scores, softmax and sums are fp32; where a score, or scale times scale_k,
- * times log2(e) is beyond fp32's range the row is unspecified.  The weights exp(s_j - m) enter the product with v in
- * 16 bits: the kernel for few rows carries them over a 16-bit cache (and
- * packed rows) as a rounded part and its remainder, elsewhere they are rounded
- * once, to q's type or, over an 8-bit cache, to fp16.  That moves out by at most
- * half a step of that type relative to sum_j p_j |v_j|, and a weight in fp16 that
- * is below 2^-21 of the largest by at most 2^-32 of the largest.  bf16 q over an
- * 8-bit cache becomes fp16 by a power of two a row: exact for elements down to
- * 2^-31 of the row's largest.  A NaN or infinity in a visible key or value
- * makes every row of its sequence that shares a key tile with it unspecified,
- * causally earlier ones included.
+ * times log2(e) is beyond fp32's range the row is unspecified.  The weights
+ * exp(s_j - m) enter the product with v in 16 bits: the kernel for few rows
+ * carries them over a 16-bit cache (and packed rows) as a rounded part and its
+ * remainder, elsewhere they are rounded once, to q's type or, over an 8-bit
+ * cache, to fp16.  That moves out by at most half a step of that type relative
+ * to sum_j p_j |v_j|; a weight in fp16 below 2^-21 of the largest is off by at
+ * most 2^-32 of the largest.  bf16 q over an 8-bit cache becomes fp16 by a power
+ * of two a row: exact for elements down to 2^-31 of the row's largest.  A NaN or
+ * infinity in a visible key or value makes every row of its sequence that
+ * shares a key tile with it unspecified, causally earlier ones included.
  * Errors: SFA_ERR_INVALID_ARG / SFA_ERR_UNSUPPORTED / SFA_ERR_WORKSPACE before
  * any launch; SFA_ERR_CUDA if a launch fails.
  */

@@ -13,6 +13,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <limits>
 #include <optional>
 #include <string>
 
@@ -79,6 +80,12 @@ bool truth(PyObject* o) {
     const int v = PyObject_IsTrue(o);
     if (v < 0) throw python_error();
     return v != 0;
+}
+// A positive scale stays positive in fp32 (zero would select the default).
+float softmax_scale(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw python_error();
+    return v > 0.0 && (float)v == 0.f ? std::numeric_limits<float>::denorm_min() : (float)v;
 }
 
 // (tokens, heads, dim) rows whose heads are contiguous; returns the token stride.
@@ -281,8 +288,7 @@ PyObject* py_paged(PyObject*, PyObject* const* o, Py_ssize_t n) {
     expect(q.device() == dev, "q: on the pools' device expected");
     const int64_t qs = rows(q, "q", -1, c.head_dim);
     const int32_t* cu = list(tensor(o[5], "cu_seqlens_q"), "cu_seqlens_q", dev, (int64_t)c.num_seqs + 1);
-    const double scale = PyFloat_AsDouble(o[6]);
-    if (scale == -1.0 && PyErr_Occurred()) throw python_error();
+    const float scale = softmax_scale(o[6]);
     const int T = count(q.size(0), "tokens"), Hq = count(q.size(1), "heads"), hint = count(o[12], "max_q_len");
     const int t = type_code(q.scalar_type());
     const bool causal = truth(o[7]);
@@ -294,7 +300,7 @@ PyObject* py_paged(PyObject*, PyObject* const* o, Py_ssize_t n) {
     {
         Unlocked here;
         r.make(q, need);
-        st = fn.run(&c, q.const_data_ptr(), qs, cu, T, Hq, hint, (float)scale, causal, (sfa_dtype)t,
+        st = fn.run(&c, q.const_data_ptr(), qs, cu, T, Hq, hint, scale, causal, (sfa_dtype)t,
                     r.out.data_ptr(), r.lse_ptr(), r.ws, r.ws_bytes, on.stream);
     }
     return wrap(st, r.out, r.lse);
@@ -315,8 +321,7 @@ PyObject* py_varlen(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const at::Tensor& lq = tensor(o[3], "cu_seqlens_q");
     const int32_t* cq = list(lq, "cu_seqlens_q", dev, -1);
     const int32_t* ck = list(tensor(o[4], "cu_seqlens_k"), "cu_seqlens_k", dev, lq.numel());
-    const double scale = PyFloat_AsDouble(o[5]);
-    if (scale == -1.0 && PyErr_Occurred()) throw python_error();
+    const float scale = softmax_scale(o[5]);
     const int B = count(lq.numel() - 1, "num_seqs"), T = count(q.size(0), "tokens"), Hq = count(q.size(1), "heads");
     const int N = count(k.size(0), "keys"), Hkv = count(k.size(1), "heads"), hint = count(o[8], "max_q_len");
     const int t = type_code(q.scalar_type());
@@ -330,7 +335,7 @@ PyObject* py_varlen(PyObject*, PyObject* const* o, Py_ssize_t n) {
         Unlocked here;
         r.make(q, need);
         st = fn.varlen(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qs, ks, vs, cq, ck, B, T, N, Hq, Hkv,
-                       (int)D, hint, (float)scale, causal, (sfa_dtype)t, r.out.data_ptr(), r.lse_ptr(),
+                       (int)D, hint, scale, causal, (sfa_dtype)t, r.out.data_ptr(), r.lse_ptr(),
                        r.ws, r.ws_bytes, on.stream);
     }
     return wrap(st, r.out, r.lse);

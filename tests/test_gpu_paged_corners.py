@@ -218,3 +218,18 @@ def test_eight_bit_pools_beyond_32_bits(hint, page):
         assert torch.equal(x.cpu(), want)
     out, lse = run_paged(c, True, hint, d=d)
     check_paged(c, out, lse, True)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [200, 130]])
+def test_a_scale_below_fp32_is_not_the_default(q_lens):
+    """Every visible key weighs the same."""
+    c = P.Cache(68, q_lens, [300, 150], 8, 2, 64, 16, "bf16")
+    out, lse = run_paged(c, True, max(q_lens), 1e-50)
+    check_paged(c, out, lse, True, 1e-50)
+    d = c.to("cuda")
+    q, k, v = c.split(d["qkv"])
+    out, lse = (x.cpu() for x in sfa.varlen_attention(q, k, v, d["cu"], d["cu"], 1e-50, return_lse=True))
+    q, k, v = (x.double() for x in c.split(c.qkv))
+    for b, n in enumerate(q_lens):
+        s = slice(int(c.cu[b]), int(c.cu[b + 1]))
+        P.check(out[s], lse[s], P.attend(q[s], k[s], v[s], torch.ones(n, dtype=torch.bool), True, 1e-50), "bf16", n)
