@@ -558,6 +558,34 @@ sfa_status paged_append(const paged_kv* cache, const void* k_new, const void* v_
                         int num_tokens, sfa_dtype dtype, sfa_stream_t stream);
 
 /*
+ * paged_append_rotated -- paged_append with the position rotation on the way, and
+ * the queries of the same rows rotated beside it.  With pos the row's token (as in
+ * paged_append) and angle = pos * inv_freq[i], pair i of a head's first rotary_dim
+ * elements becomes
+ *     (x, y) -> (x cos(angle) - y sin(angle), x sin(angle) + y cos(angle)),
+ * in q and k; their other elements and v move as they are.
+ *   q, q_out      device packed rows of num_qo_heads heads, `dtype`, each with its
+ *                 stride; q_out may be q itself (same stride).  q NULL: keys and
+ *                 values alone.  Rows of no sequence are left alone.
+ *   inv_freq      device float32 [rotary_dim / 2], finite.
+ *   rotary_dim    even, at most head_dim; a multiple of 16 in this build.
+ *   interleaved   0: pair i is elements (i, i + rotary_dim / 2);
+ *                 else (2 i, 2 i + 1).
+ * The angle is taken of the exact product, whatever the position (off by at most
+ * 2^-22 of a radian where |pos * inv_freq[i]| < 2^28); the rotation is
+ * fp32, rounded once: to `dtype`, or in an 8-bit cache to the code nearest to its
+ * quotient by the head's scale.  A query whose position is negative is rotated by
+ * it, its key is not written.
+ * Errors: as paged_append; SFA_ERR_UNSUPPORTED for another even rotary_dim.
+ */
+sfa_status paged_append_rotated(const paged_kv* cache, const void* q, const void* k_new,
+                                const void* v_new, void* q_out, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, int64_t q_out_stride, const int32_t* cu_seqlens,
+                                int num_tokens, int num_qo_heads, const float* inv_freq,
+                                int rotary_dim, int interleaved, sfa_dtype dtype,
+                                sfa_stream_t stream);
+
+/*
  * paged_read -- the newest cu_seqlens[b + 1] - cu_seqlens[b] tokens of every
  * sequence b (all of them with cu_seqlens the running sum of kv_lens) back as
  * packed rows: the fp32 product code * scale[h], rounded to `dtype`, or a
@@ -615,6 +643,51 @@ sfa_status paged_run(const paged_kv* cache, const void* q, int64_t q_stride,
                      void* workspace, size_t workspace_bytes, sfa_stream_t stream);
 
 /*
+ * paged_run_window -- causal attention through a sliding window whose first tokens
+ * stay visible: with p = i + L_b - n_b the row's position, key j is visible if
+ *     j < L_b, j <= p and (p - j < window or j < sinks).
+ *   window     keys a row sees up to its own, >= 1.
+ *   sinks      first tokens of the sequence that every row sees, >= 0.
+ * What lies behind the window of a call's first row of a sequence, sinks apart, is
+ * not looked at: its pages may be gone (any entry in the table) or hold anything.
+ * Other arguments, precision and errors as paged_run.
+ */
+sfa_status paged_run_window(const paged_kv* cache, const void* q, int64_t q_stride,
+                            const int32_t* cu_seqlens_q, int num_tokens, int num_qo_heads,
+                            int max_q_len, int window, int sinks, float scale, sfa_dtype dtype,
+                            void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            sfa_stream_t stream);
+
+/* Bytes of workspace paged_run_shared needs for these sizes on the current
+ * device.  Host only. */
+sfa_status paged_shared_workspace_size(int num_seqs, int num_tokens, int num_qo_heads,
+                                       int num_kv_heads, int head_dim, size_t* bytes);
+
+/*
+ * paged_run_shared -- paged_run for a batch whose sequences share their first tokens
+ * in groups: those are read once for all rows of a group.
+ *   cu_shared    device int32 (num_groups + 1), non-decreasing: group g is sequences
+ *                cu_shared[g] .. cu_shared[g + 1] - 1 (entries are read as clamped to
+ *                [0, num_seqs]); sequences of no group share nothing.
+ *   shared_lens  device int32 (num_groups): how many first tokens the sequences of
+ *                group g share (read as clamped to what the page table holds).
+ * Every row of a group's sequence sees all of its shared tokens, taken from the
+ * pages of the group's first sequence, and of its own tokens j >= shared_lens[g]
+ * those paged_run shows it, from its own pages.  So where the shared tokens are
+ * the same in all sequences of the group, and no row's position lies before their
+ * end, the result is paged_run's.  kv_lens and page_table count and list the shared
+ * tokens, too; what the sequences but the first hold in their places is not
+ * looked at.  Lists that overlap or decrease give unspecified numbers.
+ * Other arguments, precision and errors as paged_run.
+ */
+sfa_status paged_run_shared(const paged_kv* cache, const void* q, int64_t q_stride,
+                            const int32_t* cu_seqlens_q, int num_tokens, int num_qo_heads,
+                            int max_q_len, const int32_t* cu_shared, const int32_t* shared_lens,
+                            int num_groups, float scale, int causal, sfa_dtype dtype, void* out,
+                            float* lse, void* workspace, size_t workspace_bytes,
+                            sfa_stream_t stream);
+
+/*
  * varlen_run -- the same attention over packed keys and values: sequence b's
  * n_b query rows (cu_seqlens_q, num_tokens rows) over its L_b key rows
  * (cu_seqlens_k, num_keys rows), L_b any (a whole prompt: the same list for
@@ -627,6 +700,17 @@ sfa_status varlen_run(const void* q, const void* k, const void* v, int64_t q_str
                       int num_qo_heads, int num_kv_heads, int head_dim, int max_q_len, float scale,
                       int causal, sfa_dtype dtype, void* out, float* lse, void* workspace,
                       size_t workspace_bytes, sfa_stream_t stream);
+
+/*
+ * varlen_run_window -- varlen_run through paged_run_window's window (p = i + L_b -
+ * n_b).
+ */
+sfa_status varlen_run_window(const void* q, const void* k, const void* v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens_q,
+                             const int32_t* cu_seqlens_k, int num_seqs, int num_tokens, int num_keys,
+                             int num_qo_heads, int num_kv_heads, int head_dim, int max_q_len,
+                             int window, int sinks, float scale, sfa_dtype dtype, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, sfa_stream_t stream);
 
 #ifdef __cplusplus
 }

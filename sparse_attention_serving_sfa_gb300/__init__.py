@@ -37,7 +37,9 @@ EXPORTS = ("sfa_run", "sfa_run_ex", "sfa_workspace_size", "sfa_get_last_error",
            "varbsr_plan_set_logits_soft_cap", "bsr_plan_set_kv_layout",
            "bsr_plan_set_data_types", "bsr_run_scaled", "sfa_gather_probe",
            "sfa_gather_probe_tma", "paged_append", "paged_read", "paged_workspace_size",
-           "paged_run", "varlen_workspace_size", "varlen_run")
+           "paged_run", "varlen_workspace_size", "varlen_run", "paged_append_rotated",
+           "paged_run_window", "varlen_run_window", "paged_shared_workspace_size",
+           "paged_run_shared")
 
 
 class SfaError(RuntimeError):
@@ -145,7 +147,17 @@ def load():
             lib.varlen_run.argtypes = ([vp] * 3 + [i64] * 3 + [vp] * 2 + [ci] * 7 + [cf] + [ci] * 2 +
                                        [vp] * 3 + [sz, vp])
             lib.varlen_run.restype = ci
-            for fn in (lib.paged_workspace_size, lib.varlen_workspace_size):
+            lib.paged_append_rotated.argtypes = [pkv] + [vp] * 4 + [i64] * 4 + [vp, ci, ci, vp, ci, ci, ci, vp]
+            lib.paged_append_rotated.restype = ci
+            lib.paged_run_window.argtypes = [pkv, vp, i64, vp] + [ci] * 5 + [cf, ci, vp, vp, vp, sz, vp]
+            lib.paged_run_window.restype = ci
+            lib.varlen_run_window.argtypes = ([vp] * 3 + [i64] * 3 + [vp] * 2 + [ci] * 9 + [cf, ci] +
+                                              [vp] * 3 + [sz, vp])
+            lib.varlen_run_window.restype = ci
+            lib.paged_run_shared.argtypes = ([pkv, vp, i64, vp, ci, ci, ci, vp, vp, ci, cf, ci, ci] +
+                                             [vp] * 3 + [sz, vp])
+            lib.paged_run_shared.restype = ci
+            for fn in (lib.paged_workspace_size, lib.varlen_workspace_size, lib.paged_shared_workspace_size):
                 fn.argtypes = [ci] * 5 + [ctypes.POINTER(sz)]
                 fn.restype = ci
             _lib = lib
@@ -497,8 +509,8 @@ def sparse_flash_attention(query, key, value, sparse_indices, scale, layout="BSN
 
 # ---------------------------------------------------------------------------
 # Paged KV cache, and dense attention over it and over packed rows.  paged_append,
-# paged_read, paged_attention and varlen_attention take torch tensors; the module
-# _tensors checks what the C entry points cannot see (shapes, strides, element
+# paged_append_rotated, paged_read, paged_attention, varlen_attention and
+# shared_prefix_attention take torch tensors; the module _tensors checks what the C entry points cannot see (shapes, strides, element
 # types, devices: ValueError) and calls them on the tensors' device, on torch's
 # current stream of that device unless `stream` is given (new outputs are then
 # that stream's memory, as inside torch.cuda.stream(stream)).
@@ -523,6 +535,9 @@ def _native():
                 mod.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
                            (lib.paged_append, lib.paged_read, lib.paged_run,
                             lib.paged_workspace_size, lib.varlen_run)])
+                mod.bind_more(*[ctypes.cast(f, ctypes.c_void_p).value for f in
+                                (lib.paged_append_rotated, lib.paged_run_window, lib.varlen_run_window,
+                                 lib.paged_run_shared, lib.paged_shared_workspace_size)])
                 _tensors = mod
     return _tensors
 
@@ -537,6 +552,22 @@ def paged_append(k_new, v_new, cu_seqlens, k_pages, v_pages, page_table, kv_lens
                                               _stream(stream))
     if st:
         raise SfaError(st, "paged_append")
+
+
+def paged_append_rotated(k_new, v_new, cu_seqlens, k_pages, v_pages, page_table, kv_lens, inv_freq, q=None,
+                         interleaved=False, kv_layout="NHD", scale_k=None, scale_v=None, q_out=None,
+                         stream=None):
+    """Forwards to paged_append_rotated(): paged_append with the new keys rotated by
+    their positions on the way, pair i of a head by position * inv_freq[i]
+    (float32, rotary_dim / 2 of them; pairs are halves apart, or neighbours with
+    interleaved).  q (tokens, qo heads, head_dim): the same rows' queries, rotated
+    into q_out (q itself, say; a new tensor unless given), which is returned."""
+    st, q_out = (_tensors or _native()).paged_append_rotated(
+        k_new, v_new, cu_seqlens, k_pages, v_pages, page_table, kv_lens, _enum(kv_layout, KV_LAYOUTS),
+        scale_k, scale_v, inv_freq, q, interleaved, q_out, _stream(stream))
+    if st:
+        raise SfaError(st, "paged_append_rotated")
+    return q_out
 
 
 def paged_read(k_pages, v_pages, page_table, kv_lens, cu_seqlens, num_tokens, dtype=None,
@@ -569,6 +600,13 @@ def varlen_workspace_size(num_seqs, num_tokens, num_qo_heads, num_kv_heads, head
     return out.value
 
 
+def paged_shared_workspace_size(num_seqs, num_tokens, num_qo_heads, num_kv_heads, head_dim) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().paged_shared_workspace_size(num_seqs, num_tokens, num_qo_heads, num_kv_heads, head_dim,
+                                              ctypes.byref(out)), "paged_shared_workspace_size")
+    return out.value
+
+
 def paged_run(cache: PagedKV, q, q_stride, cu_seqlens_q, num_tokens, num_qo_heads, max_q_len, scale,
               causal, dtype, out, lse, workspace, workspace_bytes, stream=None, check=True) -> int:
     """Forwards to paged_run(); returns the status (raises unless check=False)."""
@@ -597,28 +635,51 @@ def varlen_run(q, k, v, q_stride, k_stride, v_stride, cu_seqlens_q, cu_seqlens_k
 
 def paged_attention(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, scale=0.0, causal=True,
                     kv_layout="NHD", scale_k=None, scale_v=None, return_lse=False, max_q_len=0,
-                    out=None, lse=None, workspace=None, stream=None):
+                    out=None, lse=None, workspace=None, stream=None, window=0, sinks=0):
     """paged_run() on torch tensors: q (tokens, qo heads, head_dim), packed.
     Outputs and the workspace are allocated here unless given (a workspace
     from here belongs to this call alone; rows of no sequence are left alone,
-    so in a new out they are unset)."""
-    st, out, lse = (_tensors or _native()).paged_attention(
-        q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, scale, causal,
-        _enum(kv_layout, KV_LAYOUTS), scale_k, scale_v, return_lse, max_q_len, out, lse, workspace,
-        _stream(stream))
+    so in a new out they are unset).  With window > 0 paged_run_window(): a row
+    sees the `window` keys up to its own and the first `sinks` (causal only)."""
+    args = (q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, scale, causal,
+            _enum(kv_layout, KV_LAYOUTS), scale_k, scale_v, return_lse, max_q_len, out, lse, workspace,
+            _stream(stream))
+    if window or sinks:
+        st, out, lse = (_tensors or _native()).paged_attention_window(*args, window, sinks)
+    else:
+        st, out, lse = (_tensors or _native()).paged_attention(*args)
     if st:
         raise SfaError(st, "paged_attention")
     return (out, lse) if return_lse else out
 
 
 def varlen_attention(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=0.0, causal=True, return_lse=False,
-                     max_q_len=0, out=None, lse=None, workspace=None, stream=None):
+                     max_q_len=0, out=None, lse=None, workspace=None, stream=None, window=0, sinks=0):
     """varlen_run() on torch tensors: q (tokens, qo heads, head_dim), k and v
-    (keys, kv heads, head_dim), packed.  Outputs and workspace as
-    paged_attention."""
-    st, out, lse = (_tensors or _native()).varlen_attention(
-        q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, return_lse, max_q_len, out, lse,
-        workspace, _stream(stream))
+    (keys, kv heads, head_dim), packed.  Outputs, workspace, window and sinks
+    (varlen_run_window()) as paged_attention."""
+    args = (q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, return_lse, max_q_len, out, lse,
+            workspace, _stream(stream))
+    if window or sinks:
+        st, out, lse = (_tensors or _native()).varlen_attention_window(*args, window, sinks)
+    else:
+        st, out, lse = (_tensors or _native()).varlen_attention(*args)
     if st:
         raise SfaError(st, "varlen_attention")
+    return (out, lse) if return_lse else out
+
+
+def shared_prefix_attention(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, cu_shared, shared_lens,
+                            scale=0.0, causal=True, kv_layout="NHD", scale_k=None, scale_v=None,
+                            return_lse=False, max_q_len=0, out=None, lse=None, workspace=None, stream=None):
+    """paged_run_shared() on torch tensors: paged_attention where sequences
+    cu_shared[g] .. cu_shared[g + 1] - 1 begin with the same shared_lens[g] tokens
+    (int32 on the device), which are read once for all of them.  Outputs as
+    paged_attention, the workspace paged_shared_workspace_size() bytes."""
+    st, out, lse = (_tensors or _native()).shared_prefix_attention(
+        q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, scale, causal,
+        _enum(kv_layout, KV_LAYOUTS), scale_k, scale_v, return_lse, max_q_len, out, lse, workspace,
+        _stream(stream), cu_shared, shared_lens)
+    if st:
+        raise SfaError(st, "shared_prefix_attention")
     return (out, lse) if return_lse else out

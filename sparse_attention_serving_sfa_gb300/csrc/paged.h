@@ -46,6 +46,27 @@ struct SeqKV {
     const float* scale_v;
 };
 
+// What attention over parts of the keys takes besides: a row at position p sees
+// keys lo <= j < lim and j < min(sinks, lim), lim as without (the sequence's
+// length, causally p + 1) and
+//     lo = max(first, p - window + 1)        (no window: first),
+// first = 0, or behind a shared prefix its length.
+// A call with shared prefixes runs twice.  PREFIX: the line's sequences are the
+// groups, whose rows are those of all sequences of the group and whose keys are the
+// first shared_lens[g] of its first sequence, all visible; results stay
+// unnormalised in px_o and px_ml, a row a row.  OWN: each sequence's rows over its
+// keys from `first` on, joined with those results at the end.
+enum { PHASE_ALL = 0, PHASE_PREFIX = 1, PHASE_OWN = 2 };
+struct KeyParts {
+    int phase;
+    int window, sinks;           // at most 2^30; window 2^30: none
+    const int32_t* cu_shared;    // [groups + 1]: group g is sequences cu_shared[g] .. cu_shared[g + 1] - 1
+    const int32_t* shared_lens;  // [groups]
+    int groups;
+    float* px_o;                 // [tokens][Hq][D] unnormalised
+    float* px_ml;                // [tokens][Hq][2] (m in log2 units, sum)
+};
+
 // One attention call over SeqKV.
 struct SeqAttn {
     SeqKV kv;
@@ -59,24 +80,44 @@ struct SeqAttn {
     Divisor by_group, by_heads;  // G, kv heads
     void* ws;                    // attn_rows_ws_bytes() / attn_tc_ws_bytes() bytes
     int* err_word;
+    KeyParts parts;
 };
 
 // Row-tile path (16 rows of one kv head per tile, warp MMAs): any page size
 // and group size.
 size_t attn_rows_ws_bytes(int D);
 cudaError_t launch_attn_rows(const SeqAttn& p, sfa_dtype dtype, int num_sms, cudaStream_t stream);
+// the same over parts of the keys (SeqAttn::parts)
+cudaError_t launch_attn_rows_parts(const SeqAttn& p, sfa_dtype dtype, int num_sms, cudaStream_t stream);
 
 // Tensor-core path (two tiles of 128 rows of one kv head per CTA): groups of
 // up to 128 heads, packed rows or pages of any size.
 bool attn_tc_supported(const SeqKV& kv, int G);
 size_t attn_tc_ws_bytes(int G, int D);
 cudaError_t launch_attn_tc(const SeqAttn& p, sfa_dtype dtype, int num_sms, cudaStream_t stream);
+cudaError_t launch_attn_tc_parts(const SeqAttn& p, sfa_dtype dtype, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_paged_append(const SeqKV& kv, const void* k_new, const void* v_new,
                                 int64_t k_stride, int64_t v_stride, const int32_t* cu, int tokens,
                                 sfa_dtype dtype, cudaStream_t stream);
 cudaError_t launch_paged_read(const SeqKV& kv, const int32_t* cu, int tokens, sfa_dtype dtype,
                               void* k_out, void* v_out, cudaStream_t stream);
+
+// One append with rotation.
+struct RotateAppend {
+    SeqKV kv;
+    const void* q;               // NULL: Hq = 0
+    const void* k;
+    const void* v;
+    void* q_out;
+    int64_t q_stride, q_out_stride, k_stride, v_stride;
+    const int32_t* cu;
+    const float* inv_freq;       // [rotary / 2]
+    int tokens, Hq, rotary, interleaved;
+    int block_tokens;            // tokens of a block
+    Divisor by_token;            // 16-element pieces of a token
+};
+cudaError_t launch_paged_rotate(RotateAppend p, sfa_dtype dtype, cudaStream_t stream);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ int over(int x, Divisor d) { return (int)(((uint64_t)(uint32_t)x * d.mul) >> d.shift); }
@@ -92,6 +133,50 @@ __device__ __forceinline__ int2 seq_keys(const SeqKV& kv, int b) {
         return make_int2(0, (int)min((int64_t)max(kv.kv_lens[b], 0), (int64_t)kv.max_pages * kv.page_size));
     const int2 r = seq_rows(kv.cu_k, b, kv.rows);
     return make_int2(r.x, r.y - r.x);
+}
+
+// Sequence b of the line of a call: its rows [q_row, q_row + n_q), keys (k_row and
+// kv_len as seq_keys; `first` of them belong to a shared prefix) and page table row.
+struct LineSeq {
+    int q_row, n_q, k_row, kv_len, first, table;
+};
+template <bool PARTS>
+__device__ __forceinline__ int line_seqs(const SeqAttn& p) {
+    return PARTS && p.parts.phase == PHASE_PREFIX ? p.parts.groups : p.kv.num_seqs;
+}
+template <bool PARTS>
+__device__ __forceinline__ LineSeq line_seq(const SeqAttn& p, int b) {
+    LineSeq s;
+    s.first = 0;
+    s.table = b;
+    const KeyParts& x = p.parts;
+    if (PARTS && x.phase == PHASE_PREFIX) {
+        const int2 in = seq_rows(x.cu_shared, b, p.kv.num_seqs);
+        s.table = min(in.x, p.kv.num_seqs - 1);
+        s.q_row = min(max(p.cu_q[in.x], 0), p.tokens);
+        s.n_q = in.x < in.y ? min(max(p.cu_q[in.y], s.q_row), p.tokens) - s.q_row : 0;
+        s.k_row = 0;
+        s.kv_len = (int)min((int64_t)max(x.shared_lens[b], 0), (int64_t)p.kv.max_pages * p.kv.page_size);
+        return s;
+    }
+    const int2 q = seq_rows(p.cu_q, b, p.tokens);
+    const int2 k = seq_keys(p.kv, b);
+    s.q_row = q.x;
+    s.n_q = q.y - q.x;
+    s.k_row = k.x;
+    s.kv_len = k.y;
+    if (PARTS && x.phase == PHASE_OWN) {
+        // its group: the last that begins at or before b
+        int lo = 0, hi = x.groups;                       // lo: cu_shared[1 .. lo] <= b
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (x.cu_shared[mid + 1] <= b) lo = mid + 1;
+            else hi = mid;
+        }
+        if (lo < x.groups && x.cu_shared[lo] <= b)
+            s.first = (int)min((int64_t)max(x.shared_lens[lo], 0), (int64_t)p.kv.max_pages * p.kv.page_size);
+    }
+    return s;
 }
 #endif
 

@@ -1,6 +1,7 @@
-// C ABI of the paged KV cache (paged_append, paged_read), of dense attention
-// over it (paged_run) and over packed rows (varlen_run): argument checks,
-// layout -> stride resolution, choice of path.
+// C ABI of the paged KV cache (paged_append, paged_append_rotated, paged_read), of
+// dense attention over it (paged_run, paged_run_window, paged_run_shared) and over
+// packed rows (varlen_run, varlen_run_window): argument checks, layout -> stride
+// resolution, choice of path.
 #include <math.h>
 
 #include "common.cuh"
@@ -79,13 +80,23 @@ bool bad_stride(int64_t stride, int heads, int D) {
 //     us; 4 of 16,384 keys, 2 kv heads, 64 rows (32 tiles) 28.2 and 31.7 us, 96
 //     rows 36.3 and 32.2 us; 16 of 1,000 keys, 2 kv heads, 128 tiles 15.2 and 18.5
 //     us, 192 tiles 19.6 and 19.2 us.
-bool few_rows(const SeqAttn& p) {
-    const bool f8 = p.kv.f8 != 0;
-    const int64_t rows = (int64_t)p.max_q_len * p.G;
-    const int64_t tiles = (rows + 15) / 16 * p.kv.num_seqs * p.kv.Hkv;
-    // (keys: what the table or the packed rows can hold, the lengths are on the device)
-    const int64_t keys = p.kv.page_table ? (int64_t)p.kv.max_pages * p.kv.page_size : p.kv.rows;
+bool few_rows(int64_t rows, int64_t tiles, int64_t keys, bool f8) {
     return rows <= (f8 ? 32 : 16) || (tiles <= (f8 ? 128 : 64) && tiles * keys <= (f8 ? 524288 : 196608));
+}
+
+// The same for a call as described.  (The lengths are on the device; what counts is
+// what the table or the packed rows can hold and a window can show.)
+bool few_rows(const SeqAttn& p) {
+    int64_t keys = p.kv.page_table ? (int64_t)p.kv.max_pages * p.kv.page_size : p.kv.rows;
+    int64_t rows = (int64_t)p.max_q_len * p.G, seqs = p.kv.num_seqs;
+    if (p.parts.phase == PHASE_PREFIX) {
+        // all rows of a group are one sequence's
+        rows = (int64_t)p.tokens * p.G;
+        return few_rows(rows, ((rows + 15) / 16 + p.parts.groups - 1) * p.kv.Hkv, keys, p.kv.f8 != 0);
+    }
+    const int64_t seen = (int64_t)p.parts.window + p.parts.sinks + p.max_q_len;
+    if (p.parts.window > 0 && seen < keys) keys = seen;
+    return few_rows(rows, (rows + 15) / 16 * seqs * p.kv.Hkv, keys, p.kv.f8 != 0);
 }
 
 // Workspace of either path.
@@ -94,41 +105,98 @@ size_t attention_ws_bytes(int Hq, int Hkv, int D) {
     return r > t ? r : t;
 }
 
-sfa_status run_attention(SeqAttn& p, int num_tokens, int num_qo_heads, int max_q_len, float scale,
-                         int causal, sfa_dtype dtype, const void* q, int64_t q_stride,
-                         const int32_t* cu_q, void* out, float* lse, void* ws, size_t ws_bytes,
-                         sfa_stream_t stream) {
-    if (num_tokens < 0 || max_q_len < 0 || !cu_q || !al(cu_q, 4)) return SFA_ERR_INVALID_ARG;
-    sfa_status st = check_heads(num_qo_heads, p.kv.Hkv, p.kv.D);
+// A call's arguments besides keys and values.
+struct Call {
+    const void* q;
+    int64_t q_stride;
+    const int32_t* cu_q;
+    int tokens, Hq, max_q_len;
+    float scale;
+    int causal;
+    sfa_dtype dtype;
+    void* out;
+    float* lse;
+    void* ws;
+    size_t ws_bytes;
+    sfa_stream_t stream;
+};
+
+// Checks a call and fills `p` (its keys are filled); `need` bytes of workspace.
+// Nothing is to be done if there are no rows.
+sfa_status resolve_call(SeqAttn& p, const Call& c, size_t need) {
+    if (c.tokens < 0 || c.max_q_len < 0 || !c.cu_q || !al(c.cu_q, 4)) return SFA_ERR_INVALID_ARG;
+    sfa_status st = check_heads(c.Hq, p.kv.Hkv, p.kv.D);
     if (st != SFA_OK) return st;
-    if (!is16(dtype) || !isfinite(scale)) return SFA_ERR_INVALID_ARG;
-    if (bad_stride(q_stride, num_qo_heads, p.kv.D)) return SFA_ERR_INVALID_ARG;
-    if ((int64_t)num_tokens * num_qo_heads > 0x7fffffffLL / 2) return SFA_ERR_UNSUPPORTED;
-    if (num_tokens == 0) return SFA_OK;
-    if (!q || !out || !al(q, 16) || !al(out, 16) || !al(lse, 4)) return SFA_ERR_INVALID_ARG;
-    const size_t need = attention_ws_bytes(num_qo_heads, p.kv.Hkv, p.kv.D);
-    if (!ws || ws_bytes < need) return SFA_ERR_WORKSPACE;
-    if (!al(ws, 16)) return SFA_ERR_INVALID_ARG;
-    p.q = q; p.out = out; p.lse = lse; p.cu_q = cu_q;
-    p.tokens = num_tokens; p.Hq = num_qo_heads; p.G = num_qo_heads / p.kv.Hkv;
-    p.causal = causal ? 1 : 0;
-    p.max_q_len = max_q_len > 0 && max_q_len < num_tokens ? max_q_len : num_tokens;
-    p.q_stride = q_stride;
-    p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)p.kv.D)) * kLog2e;
+    if (!is16(c.dtype) || !isfinite(c.scale)) return SFA_ERR_INVALID_ARG;
+    if (bad_stride(c.q_stride, c.Hq, p.kv.D)) return SFA_ERR_INVALID_ARG;
+    if ((int64_t)c.tokens * c.Hq > 0x7fffffffLL / 2) return SFA_ERR_UNSUPPORTED;
+    if (c.tokens == 0) return SFA_OK;
+    if (!c.q || !c.out || !al(c.q, 16) || !al(c.out, 16) || !al(c.lse, 4)) return SFA_ERR_INVALID_ARG;
+    if (!c.ws || c.ws_bytes < need) return SFA_ERR_WORKSPACE;
+    if (!al(c.ws, 16)) return SFA_ERR_INVALID_ARG;
+    p.q = c.q; p.out = c.out; p.lse = c.lse; p.cu_q = c.cu_q;
+    p.tokens = c.tokens; p.Hq = c.Hq; p.G = c.Hq / p.kv.Hkv;
+    p.causal = c.causal ? 1 : 0;
+    p.max_q_len = c.max_q_len > 0 && c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
+    p.q_stride = c.q_stride;
+    p.scale_log2 = (c.scale > 0.f ? c.scale : 1.0f / sqrtf((float)p.kv.D)) * kLog2e;
     p.by_group = divide_by(p.G);
     p.by_heads = divide_by(p.kv.Hkv);
-    p.ws = ws;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    p.ws = c.ws;
+    return SFA_OK;
+}
+
+// One pass of a resolved call; `parts`: over parts of the keys.
+sfa_status launch_attention(SeqAttn& p, bool parts, const Call& c) {
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(c.stream);
     cudaError_t err;
-    if (!few_rows(p) && attn_tc_supported(p.kv, p.G)) {
+    if (!few_rows(p) && attn_tc_supported(p.kv, p.G) && !parts) {
         p.err_word = device_error_word();
         if (!p.err_word) return SFA_ERR_CUDA;
-        err = launch_attn_tc(p, dtype, num_sms(), s);
+        err = launch_attn_tc(p, c.dtype, num_sms(), s);
     } else {
-        err = launch_attn_rows(p, dtype, num_sms(), s);
+        err = parts ? launch_attn_rows_parts(p, c.dtype, num_sms(), s) : launch_attn_rows(p, c.dtype, num_sms(), s);
     }
     return err == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
+
+// Packed keys and values as `kv`.
+sfa_status resolve_packed(SeqKV& kv, const void* q, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                          const int32_t* cu_seqlens_k, int num_seqs, int num_keys, int Hq, int Hkv, int D) {
+    if (num_seqs < 1 || num_keys < 0 || !cu_seqlens_k || !al(cu_seqlens_k, 4)) return SFA_ERR_INVALID_ARG;
+    sfa_status st = check_heads(Hq, Hkv, D);
+    if (st != SFA_OK) return st;
+    if (bad_stride(k_stride, Hkv, D) || bad_stride(v_stride, Hkv, D)) return SFA_ERR_INVALID_ARG;
+    if (num_keys > 0x7fffffff / 2) return SFA_ERR_UNSUPPORTED;
+    // with no key at all the (then unused) pointers may be NULL
+    if (num_keys > 0 && (!k || !v || !al(k, 16) || !al(v, 16))) return SFA_ERR_INVALID_ARG;
+    kv.k = num_keys > 0 ? k : q;
+    kv.v = num_keys > 0 ? v : q;
+    kv.cu_k = cu_seqlens_k;
+    kv.num_seqs = num_seqs;
+    kv.rows = num_keys;
+    kv.Hkv = Hkv;
+    kv.D = D;
+    kv.s_tok = k_stride;
+    kv.sv_tok = v_stride;
+    kv.s_head = kv.sv_head = D;
+    return SFA_OK;
+}
+
+constexpr int kNoWindow = 1 << 30;     // (no position is larger)
+
+// The pass over all keys, or through a window.
+sfa_status run_attention(SeqAttn& p, const Call& c, int window, int sinks) {
+    sfa_status st = resolve_call(p, c, attention_ws_bytes(c.Hq, p.kv.Hkv, p.kv.D));
+    if (st != SFA_OK || c.tokens == 0) return st;
+    if (window == 0) return launch_attention(p, false, c);
+    p.parts.window = window < kNoWindow ? window : kNoWindow;
+    p.parts.sinks = sinks < kNoWindow ? sinks : kNoWindow;
+    return launch_attention(p, true, c);
+}
+
+// Results of a shared prefix's pass, behind the workspace of a pass.
+size_t prefix_bytes(int64_t tokens, int Hq, int D) { return (size_t)tokens * Hq * (D + 2) * 4; }
 
 }  // namespace
 
@@ -149,6 +217,41 @@ sfa_status paged_append(const paged_kv* cache, const void* k_new, const void* v_
     return launch_paged_append(kv, k_new, v_new, k_stride, v_stride, cu_seqlens, num_tokens, dtype,
                                reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? SFA_OK : SFA_ERR_CUDA;
+}
+
+sfa_status paged_append_rotated(const paged_kv* cache, const void* q, const void* k_new, const void* v_new,
+                                void* q_out, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                int64_t q_out_stride, const int32_t* cu_seqlens, int num_tokens,
+                                int num_qo_heads, const float* inv_freq, int rotary_dim, int interleaved,
+                                sfa_dtype dtype, sfa_stream_t stream) {
+    RotateAppend p{};
+    sfa_status st = resolve_cache(cache, p.kv);
+    if (st != SFA_OK) return st;
+    if (num_tokens < 0 || !cu_seqlens || !al(cu_seqlens, 4) || !is16(dtype)) return SFA_ERR_INVALID_ARG;
+    if (p.kv.f8 == 0 && dtype != cache->dtype) return SFA_ERR_INVALID_ARG;
+    if (!inv_freq || !al(inv_freq, 4) || rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > p.kv.D)
+        return SFA_ERR_INVALID_ARG;
+    if (rotary_dim % 16 != 0) return SFA_ERR_UNSUPPORTED;
+    if (bad_stride(k_stride, p.kv.Hkv, p.kv.D) || bad_stride(v_stride, p.kv.Hkv, p.kv.D)) return SFA_ERR_INVALID_ARG;
+    if (q && (num_qo_heads < 1 || bad_stride(q_stride, num_qo_heads, p.kv.D) ||
+              bad_stride(q_out_stride, num_qo_heads, p.kv.D)))
+        return SFA_ERR_INVALID_ARG;
+    p.Hq = q ? num_qo_heads : 0;
+    // 16-element pieces of the call, and of a block's tokens, are counted in 31 bits
+    if (((int64_t)p.Hq + 2LL * p.kv.Hkv) > (1 << 20) ||
+        (int64_t)num_tokens * ((int64_t)p.Hq + 2LL * p.kv.Hkv) > 0x7fffffffLL / 2)
+        return SFA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return SFA_OK;
+    if (!k_new || !v_new || !al(k_new, 16) || !al(v_new, 16)) return SFA_ERR_INVALID_ARG;
+    if (q && (!q_out || !al(q, 16) || !al(q_out, 16))) return SFA_ERR_INVALID_ARG;
+    p.q = q; p.k = k_new; p.v = v_new; p.q_out = q_out;
+    p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride; p.q_out_stride = q_out_stride;
+    p.cu = cu_seqlens;
+    p.inv_freq = inv_freq;
+    p.tokens = num_tokens;
+    p.rotary = rotary_dim;
+    p.interleaved = interleaved ? 1 : 0;
+    return launch_paged_rotate(p, dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
 sfa_status paged_read(const paged_kv* cache, const int32_t* cu_seqlens, int num_tokens,
@@ -180,6 +283,15 @@ sfa_status paged_workspace_size(int num_seqs, int num_tokens, int num_qo_heads, 
     return varlen_workspace_size(num_seqs, num_tokens, num_qo_heads, num_kv_heads, head_dim, bytes);
 }
 
+sfa_status paged_shared_workspace_size(int num_seqs, int num_tokens, int num_qo_heads, int num_kv_heads,
+                                       int head_dim, size_t* bytes) {
+    sfa_status st = varlen_workspace_size(num_seqs, num_tokens, num_qo_heads, num_kv_heads, head_dim, bytes);
+    if (st != SFA_OK) return st;
+    if ((int64_t)num_tokens * num_qo_heads > 0x7fffffffLL / 2) return SFA_ERR_UNSUPPORTED;
+    *bytes += prefix_bytes(num_tokens, num_qo_heads, head_dim);
+    return SFA_OK;
+}
+
 sfa_status paged_run(const paged_kv* cache, const void* q, int64_t q_stride,
                      const int32_t* cu_seqlens_q, int num_tokens, int num_qo_heads, int max_q_len,
                      float scale, int causal, sfa_dtype dtype, void* out, float* lse,
@@ -188,8 +300,52 @@ sfa_status paged_run(const paged_kv* cache, const void* q, int64_t q_stride,
     sfa_status st = resolve_cache(cache, p.kv);
     if (st != SFA_OK) return st;
     if (p.kv.f8 == 0 && dtype != cache->dtype) return SFA_ERR_INVALID_ARG;
-    return run_attention(p, num_tokens, num_qo_heads, max_q_len, scale, causal, dtype, q, q_stride,
-                         cu_seqlens_q, out, lse, workspace, workspace_bytes, stream);
+    return run_attention(p, Call{q, q_stride, cu_seqlens_q, num_tokens, num_qo_heads, max_q_len, scale, causal, dtype, out,
+                                 lse, workspace, workspace_bytes, stream}, 0, 0);
+}
+
+sfa_status paged_run_window(const paged_kv* cache, const void* q, int64_t q_stride,
+                            const int32_t* cu_seqlens_q, int num_tokens, int num_qo_heads, int max_q_len,
+                            int window, int sinks, float scale, sfa_dtype dtype, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, sfa_stream_t stream) {
+    SeqAttn p{};
+    sfa_status st = resolve_cache(cache, p.kv);
+    if (st != SFA_OK) return st;
+    if (window < 1 || sinks < 0) return SFA_ERR_INVALID_ARG;
+    if (p.kv.f8 == 0 && dtype != cache->dtype) return SFA_ERR_INVALID_ARG;
+    return run_attention(p, Call{q, q_stride, cu_seqlens_q, num_tokens, num_qo_heads, max_q_len, scale, 1, dtype, out, lse,
+                                 workspace, workspace_bytes, stream}, window, sinks);
+}
+
+sfa_status paged_run_shared(const paged_kv* cache, const void* q, int64_t q_stride,
+                            const int32_t* cu_seqlens_q, int num_tokens, int num_qo_heads, int max_q_len,
+                            const int32_t* cu_shared, const int32_t* shared_lens, int num_groups,
+                            float scale, int causal, sfa_dtype dtype, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, sfa_stream_t stream) {
+    SeqAttn p{};
+    sfa_status st = resolve_cache(cache, p.kv);
+    if (st != SFA_OK) return st;
+    if (num_groups < 1 || !cu_shared || !shared_lens || !al(cu_shared, 4) || !al(shared_lens, 4)) return SFA_ERR_INVALID_ARG;
+    if (p.kv.f8 == 0 && dtype != cache->dtype) return SFA_ERR_INVALID_ARG;
+    const Call c{q, q_stride, cu_seqlens_q, num_tokens, num_qo_heads, max_q_len, scale, causal, dtype, out, lse, workspace,
+                 workspace_bytes, stream};
+    const size_t pass = attention_ws_bytes(num_qo_heads, p.kv.Hkv, p.kv.D);
+    st = resolve_call(p, c, pass + prefix_bytes(num_tokens, num_qo_heads, p.kv.D));
+    if (st != SFA_OK || num_tokens == 0) return st;
+    p.parts.cu_shared = cu_shared;
+    p.parts.shared_lens = shared_lens;
+    p.parts.groups = num_groups;
+    p.parts.window = kNoWindow;
+    p.parts.px_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + pass);
+    p.parts.px_ml = p.parts.px_o + (int64_t)num_tokens * num_qo_heads * p.kv.D;
+    SeqAttn prefix = p;
+    prefix.parts.phase = PHASE_PREFIX;
+    prefix.causal = 0;
+    prefix.max_q_len = num_tokens;
+    st = launch_attention(prefix, true, c);
+    if (st != SFA_OK) return st;
+    p.parts.phase = PHASE_OWN;
+    return launch_attention(p, true, c);
 }
 
 sfa_status varlen_run(const void* q, const void* k, const void* v, int64_t q_stride,
@@ -198,27 +354,27 @@ sfa_status varlen_run(const void* q, const void* k, const void* v, int64_t q_str
                       int num_qo_heads, int num_kv_heads, int head_dim, int max_q_len, float scale,
                       int causal, sfa_dtype dtype, void* out, float* lse, void* workspace,
                       size_t workspace_bytes, sfa_stream_t stream) {
-    if (num_seqs < 1 || num_keys < 0 || !cu_seqlens_k || !al(cu_seqlens_k, 4)) return SFA_ERR_INVALID_ARG;
-    sfa_status st = check_heads(num_qo_heads, num_kv_heads, head_dim);
-    if (st != SFA_OK) return st;
-    if (bad_stride(k_stride, num_kv_heads, head_dim) || bad_stride(v_stride, num_kv_heads, head_dim))
-        return SFA_ERR_INVALID_ARG;
-    if (num_keys > 0x7fffffff / 2) return SFA_ERR_UNSUPPORTED;
-    // with no key at all the (then unused) pointers may be NULL
-    if (num_keys > 0 && (!k || !v || !al(k, 16) || !al(v, 16))) return SFA_ERR_INVALID_ARG;
     SeqAttn p{};
-    p.kv.k = num_keys > 0 ? k : q;
-    p.kv.v = num_keys > 0 ? v : q;
-    p.kv.cu_k = cu_seqlens_k;
-    p.kv.num_seqs = num_seqs;
-    p.kv.rows = num_keys;
-    p.kv.Hkv = num_kv_heads;
-    p.kv.D = head_dim;
-    p.kv.s_tok = k_stride;
-    p.kv.sv_tok = v_stride;
-    p.kv.s_head = p.kv.sv_head = head_dim;
-    return run_attention(p, num_tokens, num_qo_heads, max_q_len, scale, causal, dtype, q, q_stride,
-                         cu_seqlens_q, out, lse, workspace, workspace_bytes, stream);
+    sfa_status st = resolve_packed(p.kv, q, k, v, k_stride, v_stride, cu_seqlens_k, num_seqs, num_keys, num_qo_heads,
+                                   num_kv_heads, head_dim);
+    if (st != SFA_OK) return st;
+    return run_attention(p, Call{q, q_stride, cu_seqlens_q, num_tokens, num_qo_heads, max_q_len, scale, causal, dtype, out,
+                                 lse, workspace, workspace_bytes, stream}, 0, 0);
+}
+
+sfa_status varlen_run_window(const void* q, const void* k, const void* v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens_q,
+                             const int32_t* cu_seqlens_k, int num_seqs, int num_tokens, int num_keys,
+                             int num_qo_heads, int num_kv_heads, int head_dim, int max_q_len, int window,
+                             int sinks, float scale, sfa_dtype dtype, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, sfa_stream_t stream) {
+    if (window < 1 || sinks < 0) return SFA_ERR_INVALID_ARG;
+    SeqAttn p{};
+    sfa_status st = resolve_packed(p.kv, q, k, v, k_stride, v_stride, cu_seqlens_k, num_seqs, num_keys, num_qo_heads,
+                                   num_kv_heads, head_dim);
+    if (st != SFA_OK) return st;
+    return run_attention(p, Call{q, q_stride, cu_seqlens_q, num_tokens, num_qo_heads, max_q_len, scale, 1, dtype, out, lse,
+                                 workspace, workspace_bytes, stream}, window, sinks);
 }
 
 }  // extern "C"

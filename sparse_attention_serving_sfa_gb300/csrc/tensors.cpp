@@ -28,6 +28,11 @@ struct {
     decltype(&::paged_run) run;
     decltype(&::paged_workspace_size) ws_size;
     decltype(&::varlen_run) varlen;
+    decltype(&::paged_append_rotated) rotated;
+    decltype(&::paged_run_window) window;
+    decltype(&::varlen_run_window) varlen_window;
+    decltype(&::paged_run_shared) shared;
+    decltype(&::paged_shared_workspace_size) shared_ws_size;
 } fn;
 
 // An argument error, raised in Python as `type`.
@@ -217,6 +222,54 @@ PyObject* py_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
     SFA_LEAVE
 }
 
+// k_new, v_new, cu_seqlens, k_pages, v_pages, page_table, kv_lens, layout, scale_k, scale_v, inv_freq, q, interleaved,
+// q_out, stream
+PyObject* py_rotated(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    SFA_ENTER
+    arity(n, 15);
+    at::Device dev(at::kCPU);
+    const paged_kv c = cache(o + 3, integer(o[7]), o[8], o[9], dev);
+    const at::Tensor &k = tensor(o[0], "k_new"), &v = tensor(o[1], "v_new"), &freq = tensor(o[10], "inv_freq");
+    const at::Tensor *q = maybe(o[11], "q"), *given = maybe(o[13], "q_out");
+    expect(k.sizes() == v.sizes() && k.scalar_type() == v.scalar_type() && k.device() == dev && v.device() == dev,
+           "k_new and v_new: one shape and type, on the pools' device, expected");
+    const int64_t ks = rows(k, "k_new", c.num_kv_heads, c.head_dim), vs = rows(v, "v_new", c.num_kv_heads, c.head_dim);
+    const int32_t* cu = list(tensor(o[2], "cu_seqlens"), "cu_seqlens", dev, (int64_t)c.num_seqs + 1);
+    expect(freq.scalar_type() == at::kFloat && freq.dim() == 1 && freq.is_contiguous() && freq.device() == dev,
+           "inv_freq: contiguous float32 (rotary_dim / 2) on the keys' device expected");
+    const int rotary = count(2 * freq.numel(), "rotary_dim"), t = type_code(k.scalar_type()), T = count(k.size(0), "tokens");
+    const bool pairs = truth(o[12]);
+    int64_t qs = 0, os = 0;
+    int Hq = 0;
+    expect(q || !given, "q_out: only with q");
+    if (q) {
+        expect(q->device() == dev && q->scalar_type() == k.scalar_type(), "q: the keys' type and device expected");
+        qs = rows(*q, "q", -1, c.head_dim);
+        expect(q->size(0) == T, "q: as many rows as k_new expected");
+        Hq = count(q->size(1), "heads");
+        if (given) {
+            expect(given->sizes() == q->sizes() && given->scalar_type() == q->scalar_type() && given->device() == dev,
+                   "q_out: q's shape, type and device expected");
+            os = rows(*given, "q_out", Hq, c.head_dim);
+            expect(given->const_data_ptr() != q->const_data_ptr() || os == qs, "q_out: in place of q with another stride");
+        } else {
+            os = (int64_t)Hq * c.head_dim;
+        }
+    }
+    On on(dev, o[14]);
+    at::Tensor out;
+    int st;
+    {
+        Unlocked here;
+        if (q) out = given ? *given : fresh(q->sizes(), q->scalar_type(), dev);
+        st = fn.rotated(&c, q ? q->const_data_ptr() : nullptr, k.const_data_ptr(), v.const_data_ptr(),
+                        q ? out.data_ptr() : nullptr, qs, ks, vs, os, cu, T, Hq, freq.const_data_ptr<float>(), rotary, pairs,
+                        (sfa_dtype)t, on.stream);
+    }
+    return Py_BuildValue("(iN)", st, out.defined() ? THPVariable_Wrap(out) : Py_NewRef(Py_None));
+    SFA_LEAVE
+}
+
 // k_pages, v_pages, page_table, kv_lens, cu_seqlens, num_tokens, dtype (-1: default), layout, scale_k, scale_v,
 // k_out, v_out, stream
 PyObject* py_read(PyObject*, PyObject* const* o, Py_ssize_t n) {
@@ -277,11 +330,18 @@ struct Outputs {
     float* lse_ptr() const { return lse.defined() ? lse.data_ptr<float>() : nullptr; }
 };
 
+// Which keys a row sees: all (causally: up to its own), those in a window and the
+// sinks, or a shared prefix's and its own.
+enum Keys { ALL, WINDOW, SHARED };
+
+void causal_window(bool causal) { expect(causal, "window: causal attention only"); }
+
 // q, k_pages, v_pages, page_table, kv_lens, cu_seqlens_q, scale, causal, layout, scale_k, scale_v, return_lse,
-// max_q_len, out, lse, workspace, stream
+// max_q_len, out, lse, workspace, stream; then window, sinks, or cu_shared, shared_lens
+template <Keys K>
 PyObject* py_paged(PyObject*, PyObject* const* o, Py_ssize_t n) {
     SFA_ENTER
-    arity(n, 17);
+    arity(n, K == ALL ? 17 : 19);
     at::Device dev(at::kCPU);
     const paged_kv c = cache(o + 1, integer(o[8]), o[9], o[10], dev);
     const at::Tensor& q = tensor(o[0], "q");
@@ -292,25 +352,46 @@ PyObject* py_paged(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const int T = count(q.size(0), "tokens"), Hq = count(q.size(1), "heads"), hint = count(o[12], "max_q_len");
     const int t = type_code(q.scalar_type());
     const bool causal = truth(o[7]);
+    int window = 0, sinks = 0, groups = 0;
+    const int32_t *cu_shared = nullptr, *shared_lens = nullptr;
+    if constexpr (K == WINDOW) {
+        window = count(o[17], "window");
+        sinks = count(o[18], "sinks");
+        causal_window(causal);
+    } else if constexpr (K == SHARED) {
+        const at::Tensor& lens = tensor(o[18], "shared_lens");
+        shared_lens = list(lens, "shared_lens", dev, -1);
+        groups = count(lens.numel(), "groups");
+        cu_shared = list(tensor(o[17], "cu_shared"), "cu_shared", dev, (int64_t)groups + 1);
+    }
     Outputs r(o + 13, truth(o[11]));
     On on(dev, o[16]);
     size_t need = 0;
-    int st = fn.ws_size(c.num_seqs, T, Hq, c.num_kv_heads, c.head_dim, &need);
+    int st = (K == SHARED ? fn.shared_ws_size : fn.ws_size)(c.num_seqs, T, Hq, c.num_kv_heads, c.head_dim, &need);
     if (st != SFA_OK) return Py_BuildValue("(iOO)", st, Py_None, Py_None);
     {
         Unlocked here;
         r.make(q, need);
-        st = fn.run(&c, q.const_data_ptr(), qs, cu, T, Hq, hint, scale, causal, (sfa_dtype)t,
-                    r.out.data_ptr(), r.lse_ptr(), r.ws, r.ws_bytes, on.stream);
+        if constexpr (K == WINDOW)
+            st = fn.window(&c, q.const_data_ptr(), qs, cu, T, Hq, hint, window, sinks, scale, (sfa_dtype)t,
+                           r.out.data_ptr(), r.lse_ptr(), r.ws, r.ws_bytes, on.stream);
+        else if constexpr (K == SHARED)
+            st = fn.shared(&c, q.const_data_ptr(), qs, cu, T, Hq, hint, cu_shared, shared_lens, groups, scale, causal,
+                           (sfa_dtype)t, r.out.data_ptr(), r.lse_ptr(), r.ws, r.ws_bytes, on.stream);
+        else
+            st = fn.run(&c, q.const_data_ptr(), qs, cu, T, Hq, hint, scale, causal, (sfa_dtype)t,
+                        r.out.data_ptr(), r.lse_ptr(), r.ws, r.ws_bytes, on.stream);
     }
     return wrap(st, r.out, r.lse);
     SFA_LEAVE
 }
 
-// q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, return_lse, max_q_len, out, lse, workspace, stream
+// q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, return_lse, max_q_len, out, lse, workspace, stream; then
+// window, sinks
+template <Keys K>
 PyObject* py_varlen(PyObject*, PyObject* const* o, Py_ssize_t n) {
     SFA_ENTER
-    arity(n, 13);
+    arity(n, K == ALL ? 13 : 15);
     const at::Tensor &q = tensor(o[0], "q"), &k = tensor(o[1], "k"), &v = tensor(o[2], "v");
     const at::Device dev = q.device();
     expect(k.device() == dev && v.device() == dev && k.scalar_type() == q.scalar_type() &&
@@ -326,6 +407,12 @@ PyObject* py_varlen(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const int N = count(k.size(0), "keys"), Hkv = count(k.size(1), "heads"), hint = count(o[8], "max_q_len");
     const int t = type_code(q.scalar_type());
     const bool causal = truth(o[6]);
+    int window = 0, sinks = 0;
+    if constexpr (K == WINDOW) {
+        window = count(o[13], "window");
+        sinks = count(o[14], "sinks");
+        causal_window(causal);
+    }
     Outputs r(o + 9, truth(o[7]));
     On on(dev, o[12]);
     size_t need = 0;
@@ -334,9 +421,14 @@ PyObject* py_varlen(PyObject*, PyObject* const* o, Py_ssize_t n) {
     {
         Unlocked here;
         r.make(q, need);
-        st = fn.varlen(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qs, ks, vs, cq, ck, B, T, N, Hq, Hkv,
-                       (int)D, hint, scale, causal, (sfa_dtype)t, r.out.data_ptr(), r.lse_ptr(),
-                       r.ws, r.ws_bytes, on.stream);
+        if constexpr (K == WINDOW)
+            st = fn.varlen_window(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qs, ks, vs, cq, ck, B, T, N,
+                                  Hq, Hkv, (int)D, hint, window, sinks, scale, (sfa_dtype)t, r.out.data_ptr(), r.lse_ptr(),
+                                  r.ws, r.ws_bytes, on.stream);
+        else
+            st = fn.varlen(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qs, ks, vs, cq, ck, B, T, N, Hq, Hkv,
+                           (int)D, hint, scale, causal, (sfa_dtype)t, r.out.data_ptr(), r.lse_ptr(),
+                           r.ws, r.ws_bytes, on.stream);
     }
     return wrap(st, r.out, r.lse);
     SFA_LEAVE
@@ -356,10 +448,28 @@ PyObject* py_bind(PyObject*, PyObject* const* o, Py_ssize_t n) {
     SFA_LEAVE
 }
 
+// Addresses of paged_append_rotated, paged_run_window, varlen_run_window, paged_run_shared,
+// paged_shared_workspace_size.
+PyObject* py_bind_more(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    SFA_ENTER
+    arity(n, 5);
+    fn.rotated = reinterpret_cast<decltype(fn.rotated)>(PyLong_AsVoidPtr(o[0]));
+    fn.window = reinterpret_cast<decltype(fn.window)>(PyLong_AsVoidPtr(o[1]));
+    fn.varlen_window = reinterpret_cast<decltype(fn.varlen_window)>(PyLong_AsVoidPtr(o[2]));
+    fn.shared = reinterpret_cast<decltype(fn.shared)>(PyLong_AsVoidPtr(o[3]));
+    fn.shared_ws_size = reinterpret_cast<decltype(fn.shared_ws_size)>(PyLong_AsVoidPtr(o[4]));
+    if (PyErr_Occurred()) throw python_error();
+    Py_RETURN_NONE;
+    SFA_LEAVE
+}
+
 #define SFA_FN(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SFA_FN("bind", py_bind), SFA_FN("paged_append", py_append), SFA_FN("paged_read", py_read),
-                         SFA_FN("paged_attention", py_paged), SFA_FN("varlen_attention", py_varlen),
-                         {nullptr, nullptr, 0, nullptr}};
+                         SFA_FN("paged_attention", py_paged<ALL>), SFA_FN("varlen_attention", py_varlen<ALL>),
+                         SFA_FN("bind_more", py_bind_more), SFA_FN("paged_append_rotated", py_rotated),
+                         SFA_FN("paged_attention_window", py_paged<WINDOW>),
+                         SFA_FN("varlen_attention_window", py_varlen<WINDOW>),
+                         SFA_FN("shared_prefix_attention", py_paged<SHARED>), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
