@@ -84,10 +84,13 @@ bool few_rows(int64_t rows, int64_t tiles, int64_t keys, bool f8) {
     return rows <= (f8 ? 32 : 16) || (tiles <= (f8 ? 128 : 64) && tiles * keys <= (f8 ? 524288 : 196608));
 }
 
+// Keys that the longest sequence can have (below 2^30).
+int64_t most_keys(const SeqKV& kv) { return kv.page_table ? (int64_t)kv.max_pages * kv.page_size : kv.rows; }
+
 // The same for a call as described.  (The lengths are on the device; what counts is
 // what the table or the packed rows can hold and a window can show.)
 bool few_rows(const SeqAttn& p) {
-    int64_t keys = p.kv.page_table ? (int64_t)p.kv.max_pages * p.kv.page_size : p.kv.rows;
+    int64_t keys = most_keys(p.kv);
     int64_t rows = (int64_t)p.max_q_len * p.G, seqs = p.kv.num_seqs;
     if (p.parts.phase == PHASE_PREFIX) {
         // all rows of a group are one sequence's
@@ -150,10 +153,10 @@ sfa_status resolve_call(SeqAttn& p, const Call& c, size_t need) {
 sfa_status launch_attention(SeqAttn& p, bool parts, const Call& c) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(c.stream);
     cudaError_t err;
-    if (!few_rows(p) && attn_tc_supported(p.kv, p.G) && !parts) {
+    if (!few_rows(p) && attn_tc_supported(p.kv, p.G)) {
         p.err_word = device_error_word();
         if (!p.err_word) return SFA_ERR_CUDA;
-        err = launch_attn_tc(p, c.dtype, num_sms(), s);
+        err = parts ? launch_attn_tc_parts(p, c.dtype, num_sms(), s) : launch_attn_tc(p, c.dtype, num_sms(), s);
     } else {
         err = parts ? launch_attn_rows_parts(p, c.dtype, num_sms(), s) : launch_attn_rows(p, c.dtype, num_sms(), s);
     }
@@ -189,9 +192,10 @@ constexpr int kNoWindow = 1 << 30;     // (no position is larger)
 sfa_status run_attention(SeqAttn& p, const Call& c, int window, int sinks) {
     sfa_status st = resolve_call(p, c, attention_ws_bytes(c.Hq, p.kv.Hkv, p.kv.D));
     if (st != SFA_OK || c.tokens == 0) return st;
-    if (window == 0) return launch_attention(p, false, c);
-    p.parts.window = window < kNoWindow ? window : kNoWindow;
-    p.parts.sinks = sinks < kNoWindow ? sinks : kNoWindow;
+    // (nothing lies between the two where they reach over all that the call can hold)
+    if (window == 0 || (int64_t)window + sinks >= most_keys(p.kv)) return launch_attention(p, false, c);
+    p.parts.window = window;
+    p.parts.sinks = sinks;
     return launch_attention(p, true, c);
 }
 
