@@ -482,6 +482,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// The lowest n bits of a word (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return __funnelshift_rc(0xffffffffu, 0u, 32 - max(min(n, 32), 0));
+}
 // 32 bytes at once (a full sector a thread).
 __device__ __forceinline__ void st_32(void* to, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -1090,48 +1094,35 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 uint32_t sv[128];
                 tmem_ld128_sync(lane_base, sv);
                 const int key0 = real_step<PARTS>(p, it, it.s0 + st) * kStep;
-                if constexpr (PARTS) {
-                    if (lo_max > key0 && key0 + kStep > a.parts.sinks) {
-                        // 32 keys at a time, where a row of this warp begins behind or in them
-                        const int rel = lo - key0, rel_max = lo_max - key0, head = a.parts.sinks - key0;
+                const bool begins = PARTS && lo_max > key0 && key0 + kStep > a.parts.sinks;
+                if (lim_min < key0 + kStep || begins || (PAGED && missing)) {
+                    // 128 bits, one a key: which ones this row sees
+                    uint32_t in[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (rel_max > 32 * q && head < 32 * (q + 1)) {
-#pragma unroll
-                                for (int j = 32 * q; j < 32 * (q + 1); ++j)
-                                    if (j < rel && j >= head) sv[j] = __float_as_uint(-INFINITY);
-                            }
+                    for (int q = 0; q < 4; ++q) {
+                        in[q] = bits_below(lim - key0 - 32 * q);
+                        if constexpr (PARTS) in[q] &= ~bits_below(lo - key0 - 32 * q) | bits_below(a.parts.sinks - key0 - 32 * q);
                     }
-                }
-                if (lim_min < key0 + kStep || missing) {
-                    const int rel = lim - key0, rel_min = lim_min - key0;
-                    // 32 keys at a time, where a row of this warp ends before or in them
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (rel_min < 32 * (q + 1)) {
-#pragma unroll
-                            for (int j = 32 * q; j < 32 * (q + 1); ++j)
-                                if (j >= rel) sv[j] = __float_as_uint(-INFINITY);
-                        }
                     if (PAGED && missing) {
-                        // 128 bits, one a key: the words' bits spread over their boxes
-                        unsigned gone[4] = {0, 0, 0, 0};
+                        // without those of the boxes that have no page
 #pragma unroll
                         for (int i = 0; i < kWords; ++i) {
                             const unsigned w = __ballot_sync(0xffffffffu, (bad >> i) & 1u);
                             for (unsigned x = w; x; x &= x - 1) {
                                 const int key = (__ffs(x) - 1 + 32 * i) << p.box_shift;
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int lo = max(key - 32 * q, 0), hi = min(key + p.box - 32 * q, 32);
-                                    if (lo < hi) gone[q] |= (hi - lo == 32 ? 0xffffffffu : ((1u << (hi - lo)) - 1u)) << lo;
-                                }
+                                for (int q = 0; q < 4; ++q) in[q] &= ~(bits_below(key + p.box - 32 * q) & ~bits_below(key - 32 * q));
                             }
                         }
-#pragma unroll
-                        for (int j = 0; j < 128; ++j)
-                            if ((gone[j >> 5] >> (j & 31)) & 1u) sv[j] = __float_as_uint(-INFINITY);
                     }
+                    // 32 keys at a time, where a row of this warp does not see all
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (__any_sync(0xffffffffu, in[q] != 0xffffffffu)) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!((in[q] >> j) & 1u)) sv[32 * q + j] = __float_as_uint(-INFINITY);
+                        }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1216,7 +1207,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             // parts: [D / 4][row][4], so that the lanes (rows) write side by side
             const int64_t slot = 2 * blockIdx.x + (it.s0 == 0 ? 1 : 0);
             float* part = p.ws_o + slot * kItemRows * D + (t * kTileM + r) * 4;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t ov[32];
                 if (n > 0) {
