@@ -1091,39 +1091,37 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     if (st == n - 1) mbar_arrive(bar(B_Q_FREE));
                 }
                 tc_fence_after();
-                uint32_t sv[128];
-                tmem_ld128_sync(lane_base, sv);
                 const int key0 = real_step<PARTS>(p, it, it.s0 + st) * kStep;
                 const bool begins = PARTS && lo_max > key0 && key0 + kStep > a.parts.sinks;
                 if (lim_min < key0 + kStep || begins || (PAGED && missing)) {
-                    // 128 bits, one a key: which ones this row sees
-                    uint32_t in[4];
+                    // Masked in place, 32 keys at a time where a row of this warp does
+                    // not see all.  (A loop through tensor memory, not 128 registers:
+                    // what counts here is the code to be fetched.)
+#pragma unroll 1
+                    for (int q = 0; q < kStep; q += 32) {
+                        uint32_t in = bits_below(lim - key0 - q);       // a bit a key: which ones this row sees
+                        if constexpr (PARTS) in &= ~bits_below(lo - key0 - q) | bits_below(a.parts.sinks - key0 - q);
+                        if (PAGED && missing) {
+                            // without those of the boxes that have no page
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        in[q] = bits_below(lim - key0 - 32 * q);
-                        if constexpr (PARTS) in[q] &= ~bits_below(lo - key0 - 32 * q) | bits_below(a.parts.sinks - key0 - 32 * q);
-                    }
-                    if (PAGED && missing) {
-                        // without those of the boxes that have no page
-#pragma unroll
-                        for (int i = 0; i < kWords; ++i) {
-                            const unsigned w = __ballot_sync(0xffffffffu, (bad >> i) & 1u);
-                            for (unsigned x = w; x; x &= x - 1) {
-                                const int key = (__ffs(x) - 1 + 32 * i) << p.box_shift;
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) in[q] &= ~(bits_below(key + p.box - 32 * q) & ~bits_below(key - 32 * q));
-                            }
+                            for (int i = 0; i < kWords; ++i)
+                                for (unsigned x = __ballot_sync(0xffffffffu, (bad >> i) & 1u); x; x &= x - 1) {
+                                    const int key = ((__ffs(x) - 1 + 32 * i) << p.box_shift) - q;
+                                    in &= ~(bits_below(key + p.box) & ~bits_below(key));
+                                }
                         }
+                        if (!__any_sync(0xffffffffu, in != 0xffffffffu)) continue;
+                        uint32_t x[32];
+                        tmem_ld32_sync(lane_base + q, x);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!((in >> j) & 1u)) x[j] = __float_as_uint(-INFINITY);
+                        tmem_st32(lane_base + q, x);
                     }
-                    // 32 keys at a time, where a row of this warp does not see all
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (__any_sync(0xffffffffu, in[q] != 0xffffffffu)) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!((in[q] >> j) & 1u)) sv[32 * q + j] = __float_as_uint(-INFINITY);
-                        }
+                    tmem_wait_st();
                 }
+                uint32_t sv[128];
+                tmem_ld128_sync(lane_base, sv);
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int j = 0; j < 128; j += 2)
