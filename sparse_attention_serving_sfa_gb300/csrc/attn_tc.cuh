@@ -105,7 +105,7 @@ template <int SRC>
 struct TcBlock {
     static constexpr bool movers = SRC >= SRC_G16;
     static constexpr int threads = movers ? 512 : 384;
-    static constexpr int launch = movers ? 128 : 168, control = movers ? 64 : 80, softmax = movers ? 192 : 208;
+    static constexpr int launch = movers ? 128 : 168, control = movers ? 96 : 80, softmax = movers ? 160 : 208;
     static_assert(softmax * kSoftWarps * 32 + control * (threads - kSoftWarps * 32) <= launch * threads,
                   "the register split fits what the block was launched with");
 };
@@ -481,6 +481,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+// Waits for this thread's loads from tensor memory; x is what one of them brings.
+__device__ __forceinline__ void tmem_landed(uint32_t (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]), "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]), "+r"(x[16]), "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]), "+r"(x[23]), "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29]), "+r"(x[30]), "+r"(x[31])
+                 :: "memory");
 }
 // The lowest n bits of a word (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t bits_below(int n) {
@@ -1120,14 +1126,38 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     }
                     tmem_wait_st();
                 }
-                uint32_t sv[128];
-                tmem_ld128_sync(lane_base, sv);
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                constexpr bool kLoop = L::gather;
+                uint32_t sv[kLoop ? 1 : 128], xa[32], xb[32];
+                float top;
+                if constexpr (kLoop) {
+                    // 32 scores at a time, the next under way: once for the maximum, once
+                    // more for the weights
+                    float mx[2] = {-INFINITY, -INFINITY};
+                    tmem_ld32(lane_base, xa);
+#pragma unroll 1
+                    for (int h = 0; h < 128; h += 64) {
+                        tmem_landed(xa);
+                        tmem_ld32(lane_base + h + 32, xb);
 #pragma unroll
-                for (int j = 0; j < 128; j += 2)
-                    mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], __uint_as_float(sv[j])), __uint_as_float(sv[j + 1]));
+                        for (int j = 0; j < 32; j += 2)
+                            mx[(j >> 1) & 1] = fmaxf(fmaxf(mx[(j >> 1) & 1], __uint_as_float(xa[j])), __uint_as_float(xa[j + 1]));
+                        tmem_landed(xb);
+                        tmem_ld32(lane_base + 64 - h, xa);              // (the last: the first scores again)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+                            mx[(j >> 1) & 1] = fmaxf(fmaxf(mx[(j >> 1) & 1], __uint_as_float(xb[j])), __uint_as_float(xb[j + 1]));
+                    }
+                    top = fmaxf(mx[0], mx[1]);
+                } else {
+                    tmem_ld128_sync(lane_base, sv);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int j = 0; j < 128; j += 2)
+                        mx[(j >> 1) & 3] = fmaxf(fmaxf(mx[(j >> 1) & 3], __uint_as_float(sv[j])), __uint_as_float(sv[j + 1]));
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                }
                 // the scale is positive and rounding monotonic: max of scaled = scaled max
-                const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rs);
+                const float m_new = fmaxf(m_used, top * rs);
                 const bool need = m_new > m_used + kRescale;
                 // the P.V before this step's Q.K^T is complete: O is settled
                 if (st > 0 && __any_sync(0xffffffffu, need)) {
@@ -1146,32 +1176,62 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 // (a row that has seen no key has only -inf scores: subtracting 0 gives P = 0)
                 const float sub = m_used == -INFINITY ? 0.f : m_used - kPShift;
                 const uint64_t rs2 = pair(rs, rs), sub2 = pair(-sub, -sub);
-                uint64_t ls[2] = {0, 0};
-                auto weights = [&](int k) {              // keys 2 k, 2 k + 1
-                    const uint64_t u = fma2(pair(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), rs2, sub2);
-                    const float p0 = fast_exp2(low(u)), p1 = fast_exp2(high(u));
-                    ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
-                    sv[k] = M::pack2(p0, p1);
-                };
+                if constexpr (kLoop) {
+                    uint64_t ls[2] = {0, 0};
+                    auto weights = [&](uint32_t (&x)[32], uint32_t to) {
+                        uint32_t w[16];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) weights(k);
-                tmem_st32(lane_base, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                // (the first half's store completes under the next weights)
+                        for (int k = 0; k < 16; ++k) {
+                            const uint64_t u = fma2(pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), rs2, sub2);
+                            const float p0 = fast_exp2(low(u)), p1 = fast_exp2(high(u));
+                            ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
+                            w[k] = M::pack2(p0, p1);
+                        }
+                        tmem_st16(to, w);
+                    };
+#pragma unroll 1
+                    for (int h = 0; h < 128; h += 64) {
+                        tmem_landed(xa);
+                        tmem_ld32(lane_base + h + 32, xb);
+                        weights(xa, lane_base + h / 2);
+                        tmem_landed(xb);
+                        if (h == 0) tmem_ld32(lane_base + 64, xa);
+                        weights(xb, lane_base + h / 2 + 16);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar((h == 0 ? B_PH : B_P) + t));
+                    }
+                    const uint64_t l2 = add2(ls[0], ls[1]);
+                    l += low(l2) + high(l2);
+                } else {
+                    uint64_t ls[2] = {0, 0};
+                    auto weights = [&](int k) {              // keys 2 k, 2 k + 1
+                        const uint64_t u = fma2(pair(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), rs2, sub2);
+                        const float p0 = fast_exp2(low(u)), p1 = fast_exp2(high(u));
+                        ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
+                        sv[k] = M::pack2(p0, p1);
+                    };
 #pragma unroll
-                for (int k = 32; k < 44; ++k) weights(k);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_PH + t));
+                    for (int k = 0; k < 32; ++k) weights(k);
+                    tmem_st32(lane_base, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    // (the first half's store completes under the next weights)
 #pragma unroll
-                for (int k = 44; k < 64; ++k) weights(k);
-                tmem_st32(lane_base + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-                const uint64_t l2 = add2(ls[0], ls[1]);
-                l += low(l2) + high(l2);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_P + t));
+                    for (int k = 32; k < 44; ++k) weights(k);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_PH + t));
+#pragma unroll
+                    for (int k = 44; k < 64; ++k) weights(k);
+                    tmem_st32(lane_base + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                    const uint64_t l2 = add2(ls[0], ls[1]);
+                    l += low(l2) + high(l2);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_P + t));
+                }
             }
             if (!ok) break;
             // ---- epilogue ----
@@ -1376,6 +1436,86 @@ __global__ void __launch_bounds__(kMergeThreads, 4) attn_tc_merge(const TcParams
     }
 }
 
+// Joins the parts of a prefix's items where those are fewer than the ranges, each cut
+// into many parts: units of a few rows dealt out over one wave of blocks, a thread
+// has four dims of a row (eight rows of a unit lie side by side in a part, so a
+// warp reads 128 bytes at four places) and kBatch of its parts in flight.  Every
+// block first counts the cuts that the ranges wrote down.  (8 items of 19 parts: 18
+// us in blocks of a range and 32 rows, few of which have all the work; now 5.  With
+// many items of 2 parts these units take 7 us longer than those blocks.)
+constexpr int kPrefixBlocks = 4;                         // an SM
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads, kPrefixBlocks) attn_tc_merge_prefix(const TcParams p, int ranges) {
+    constexpr int kGroups = D / 4;                       // threads of a row
+    constexpr int kUnit = kMergeThreads / kGroups;       // rows of a unit
+    constexpr int kBatch = 4;
+    __shared__ int first_cut[kMaxCtas];                  // the ranges that cut an item first
+    __shared__ int in_warp[kMergeThreads / 32];
+    static_assert(kMaxCtas <= kMergeThreads, "a thread a range");
+    const SeqAttn& a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependency_wait();
+    const bool cuts = tid < ranges && p.ws_cut[tid].N > 0;
+    const unsigned which = __ballot_sync(0xffffffffu, cuts);
+    if (lane == 0) in_warp[warp] = __popc(which);
+    __syncthreads();
+    int before = 0, count = 0;
+#pragma unroll
+    for (int i = 0; i < kMergeThreads / 32; ++i) {
+        if (i < warp) before += in_warp[i];
+        count += in_warp[i];
+    }
+    if (cuts) first_cut[before + __popc(which & ((1u << lane) - 1u))] = tid;
+    __syncthreads();
+    // row of the unit and group of four dims: lanes 0 .. 7 are eight rows
+    const int ur = (tid & 7) + (kUnit > 8 ? 8 * (warp / (kGroups / 4)) : 0), d4 = (lane >> 3) + 4 * (warp % (kGroups / 4));
+    for (int u = blockIdx.x; u < count * (kItemRows / kUnit); u += gridDim.x) {
+        const int x = first_cut[u / (kItemRows / kUnit)];
+        const CutItem it = p.ws_cut[x];
+        const int N = it.N, h = it.h;
+        const int r = u % (kItemRows / kUnit) * kUnit + ur, rr = r % kTileM, tok = it.tok0 + r / kTileM * p.TR + rr / a.G;
+        if (rr >= p.TR * a.G || tok >= it.n_q) continue;
+        float M = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        // (`last`: steps before part i; two borders can move to the same step)
+        for (int i = 0, last = 0; last < N; i += kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int end = last < N ? cut(it.x + (i + j) * it.per, it.c, N) : last;
+                const bool some = end != last;
+                last = end;
+                const int64_t slot = i + j == 0 ? 2 * x + 1 : 2 * (x + i + j);
+                ml[j] = some ? *reinterpret_cast<const float2*>(p.ws_ml + (slot * kItemRows + r) * 2) : make_float2(-INFINITY, 0.f);
+                v[j] = some ? *reinterpret_cast<const float4*>(p.ws_o + slot * kItemRows * D + (d4 * kItemRows + r) * 4)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            // two at a time (a part without a visible key: m = -inf, everything else 0)
+#pragma unroll
+            for (int j = 0; j < kBatch; j += 2) {
+                const float m_new = fmaxf(fmaxf(M, ml[j].x), ml[j + 1].x), old = rescale_factor(M, m_new);
+                M = m_new;
+                l *= old;
+                acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+                for (int k = j; k < j + 2; ++k) {
+                    const float f = rescale_factor(ml[k].x, M);
+                    l += ml[k].y * f;
+                    acc.x += v[k].x * f;
+                    acc.y += v[k].y * f;
+                    acc.z += v[k].z * f;
+                    acc.w += v[k].w * f;
+                }
+            }
+        }
+        const int64_t row = (int64_t)(it.q_row + tok) * a.Hq + h * a.G + rr % a.G;
+        reinterpret_cast<float4*>(a.parts.px_o + row * D)[d4] = acc;
+        if (d4 == 0) *reinterpret_cast<float2*>(a.parts.px_ml + row * 2) = make_float2(M, l);
+    }
+}
+
 // q, or packed k / v: [rows][heads][D] with rows `stride` elements apart; box
 // 64 dims x hb heads x rb rows, 128-byte swizzle.
 bool rows_map(CUtensorMap* m, const void* base, bool bf16, int D, int heads, int rows, int64_t stride, int hb, int rb) {
@@ -1449,7 +1589,15 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStr
     count_launches(1);
     // items of fewer than 2 kMinShare steps are never cut
     if (longest >= 2 * kMinShare * kStep - kStep + 1) {
-        err = launch_pdl(attn_tc_merge<E, D, PARTS>, dim3(ctas - 1, kItemRows / 32), dim3(kMergeThreads), 0, stream, p);
+        // (a prefix's items at most; with fewer than ranges most are cut often)
+        const int64_t items = PARTS && a.parts.phase == PHASE_PREFIX
+                                  ? ((int64_t)a.tokens / (2 * p.TR) + a.parts.groups) * a.kv.Hkv : ctas;
+        if constexpr (PARTS) {
+            if (items < ctas)
+                err = launch_pdl(attn_tc_merge_prefix<D>, dim3(kPrefixBlocks * ctas), dim3(kMergeThreads), 0, stream, p, ctas - 1);
+        }
+        if (items >= ctas)
+            err = launch_pdl(attn_tc_merge<E, D, PARTS>, dim3(ctas - 1, kItemRows / 32), dim3(kMergeThreads), 0, stream, p);
         if (err == cudaSuccess) count_launches(1);
     }
     return err;
