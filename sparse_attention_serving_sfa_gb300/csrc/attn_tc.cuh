@@ -784,22 +784,32 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 const Item& it = next_item;
                 const int n = max(it.n[0], it.n[1]);
                 if (n == 0) continue;
-                if constexpr (!kScaledQ) {
-                    if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                // the item's Q, as soon as the item before has been multiplied
+                auto load_q = [&]() {
+                    if constexpr (!kScaledQ) {
+                        if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) return;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (it.n[t] == 0) continue;
-                        ++qs[t];
-                        if (lane != 0) continue;
-                        mbar_arrive_expect_tx(bar(B_Q + t), L::panels * p.TR * G * 128);
-                        for (int pn = 0; pn < L::panels; ++pn)
-                            tma_load_3d(sbase + L::q + t * L::tile + pn * L::panel, &mq, pn * 64, it.h * G,
-                                        it.q_row + it.tok0 + t * p.TR, bar(B_Q + t));
+                        for (int t = 0; t < 2; ++t) {
+                            if (it.n[t] == 0) continue;
+                            ++qs[t];
+                            if (lane != 0) continue;
+                            mbar_arrive_expect_tx(bar(B_Q + t), L::panels * p.TR * G * 128);
+                            for (int pn = 0; pn < L::panels; ++pn)
+                                tma_load_3d(sbase + L::q + t * L::tile + pn * L::panel, &mq, pn * 64, it.h * G,
+                                            it.q_row + it.tok0 + t * p.TR, bar(B_Q + t));
+                        }
                     }
+                    ++items;
+                };
+                // With PARTS behind the first K and V, which are then on their way while Q is
+                // still in use.  (Chunks through a window 184 -> 178 us; but over all keys,
+                // where items are longer, 211 -> 218 us.)
+                if (!PARTS || !tma) {
+                    load_q();
+                    if (!ok) break;
                 }
-                ++items;
                 if (!tma) continue;
                 // page of this lane's box of a step, -1 if there is none to read
                 // (left as loaded, so that nothing waits for the load)
@@ -811,10 +821,30 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 };
                 int page = 0;
                 if constexpr (PAGED) page = page_of(0);
+                // A V tile with rows to be cleared (the V tile of a step, slot `tail`):
+                // waits for it, clears those rows and hands it on.  That is left until
+                // the next loads are on their way.
+                int tail = -1, real = 0, gap0 = 0, gap1 = 0;
+                auto clear_tail = [&]() {
+                    if (tail < 0) return;
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_TAIL), tails & 1, err, abort_flag)) != 0;
+                    ++tails;
+                    if (!ok) return;
+                    unsigned char* row = smem + L::ring + tail * L::tile;
+                    auto clear = [&](int from, int to) {
+                        for (int x = from * 8 + lane; x < to * 8; x += 32)
+                            for (int pn = 0; pn < L::panels; ++pn)
+                                *reinterpret_cast<uint4*>(row + pn * L::panel + x * 16) = make_uint4(0, 0, 0, 0);
+                    };
+                    clear(real, kStep);
+                    if constexpr (PARTS) clear(gap0, gap1);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_FULL + tail));
+                    tail = -1;
+                };
                 for (int st = 0; st < n && ok; ++st) {
                     const int key0 = real_step<PARTS>(p, it, it.s0 + st) * kStep;
-                    // keys of the step, [gap0, gap1), that lie between the sinks and the item's lowest
-                    const int gap0 = PARTS ? max(a.parts.sinks - key0, 0) : 0, gap1 = PARTS ? min(it.lo - key0, kStep) : 0;
                     const int pg = (unsigned)page < (unsigned)a.kv.num_pages ? page : -1;
                     if constexpr (PAGED) page = page_of(st + 1);
                     for (int kv = 0; kv < 2 && ok; ++kv) {
@@ -826,9 +856,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         const uint32_t dst = sbase + (L::gather ? L::staging + s * kStep * D : L::ring + s * L::tile);
-                        const int real = it.kv_len - key0;             // keys of this tile that exist
-                        const bool tail = !L::gather && kv == 1 && (real < kStep || gap0 < gap1);
-                        const uint32_t b = bar(tail ? B_TAIL : (L::gather ? B_STAGE : B_FULL) + s);
+                        bool clears = false;
+                        if (!L::gather && kv == 1) {
+                            real = it.kv_len - key0;                   // keys of this tile that exist
+                            if constexpr (PARTS) {
+                                // those between the sinks and the item's lowest, [gap0, gap1)
+                                gap0 = max(a.parts.sinks - key0, 0);
+                                gap1 = min(it.lo - key0, kStep);
+                            }
+                            clears = real < kStep || gap0 < gap1;
+                            if (clears) tail = s;
+                        }
+                        const uint32_t b = bar(clears ? B_TAIL : (L::gather ? B_STAGE : B_FULL) + s);
                         const CUtensorMap* map = kv ? &mv : &mk;
                         if (lane == 0) mbar_arrive_expect_tx(b, L::gather ? kStep * D : L::tile);
                         __syncwarp();
@@ -849,25 +888,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                             for (int pn = 0; pn < L::panels; ++pn)
                                 tma_load_3d(dst + pn * L::panel, map, pn * 64, it.h, it.k_row + key0, b);
                         }
-                        if (tail) {
-                            __syncwarp();
-                            ok = mbar_wait(b, tails & 1, err, abort_flag);
-                            ++tails;
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
-                            unsigned char* row = smem + L::ring + s * L::tile;
-                            auto clear = [&](int from, int to) {
-                                for (int x = from * 8 + lane; x < to * 8; x += 32)
-                                    for (int pn = 0; pn < L::panels; ++pn)
-                                        *reinterpret_cast<uint4*>(row + pn * L::panel + x * 16) = make_uint4(0, 0, 0, 0);
-                            };
-                            clear(real, kStep);
-                            if constexpr (PARTS) clear(gap0, gap1);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(B_FULL + s));
-                        }
                         ++loads;
+                        if (PARTS && kv == 1 && st == 0) load_q();
+                        if (ok && (kv == 0 || st == n - 1)) clear_tail();
                     }
                 }
                 if (!ok) break;
