@@ -572,10 +572,10 @@ sfa_status paged_append(const paged_kv* cache, const void* k_new, const void* v_
  *   interleaved   0: pair i is elements (i, i + rotary_dim / 2);
  *                 else (2 i, 2 i + 1).
  * The angle is taken of the exact product, whatever the position (off by at most
- * 2^-22 of a radian where |pos * inv_freq[i]| < 2^28); the rotation is
- * fp32, rounded once: to `dtype`, or in an 8-bit cache to the code nearest to its
- * quotient by the head's scale.  A query whose position is negative is rotated by
- * it, its key is not written.
+ * 2^-22 of a radian); the rotation is fp32, rounded once: to `dtype`, or in an 8-bit
+ * cache to the code nearest to its quotient by the head's scale (next to a border
+ * between two codes the rotation is computed in 64 bits).  A query whose position is
+ * negative is rotated by it, its key is not written.
  * Errors: as paged_append; SFA_ERR_UNSUPPORTED for another even rotary_dim.
  */
 sfa_status paged_append_rotated(const paged_kv* cache, const void* q, const void* k_new,

@@ -115,7 +115,7 @@ struct RotateAppend {
     const float* inv_freq;       // [rotary / 2]
     int tokens, Hq, rotary, interleaved;
     int block_tokens;            // tokens of a block
-    Divisor by_token;            // 16-element pieces of a token
+    Divisor by_heads;            // heads of a token: queries, keys, values
 };
 cudaError_t launch_paged_rotate(RotateAppend p, sfa_dtype dtype, cudaStream_t stream);
 

@@ -60,7 +60,13 @@ __device__ __forceinline__ float quotient(float x, float s) {
     return q;
 }
 
-// Codes of eight values.
+// Eight values as the nearest codes.
+template <bool E5>
+__device__ __forceinline__ uint2 codes8(const float (&q)[8]) {
+    return make_uint2(f8_pack2<E5>(q[0], q[1]) | (f8_pack2<E5>(q[2], q[3]) << 16),
+                      f8_pack2<E5>(q[4], q[5]) | (f8_pack2<E5>(q[6], q[7]) << 16));
+}
+// Codes of eight values' quotients.
 template <bool E5>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv) {
     float q[8];
@@ -76,8 +82,7 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv
 #pragma unroll
         for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], s);
     }
-    return make_uint2(f8_pack2<E5>(q[0], q[1]) | (f8_pack2<E5>(q[2], q[3]) << 16),
-                      f8_pack2<E5>(q[4], q[5]) | (f8_pack2<E5>(q[6], q[7]) << 16));
+    return codes8<E5>(q);
 }
 template <class E>
 __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
