@@ -44,10 +44,10 @@
 // 2^-39 of it.  The power leaves with the scores.
 //
 // PARTS (a template parameter): a row sees parts of the keys only (KeyParts).  A
-// tile then goes through the chunks that hold the first `sinks` keys and through
-// those from its lowest row's first key on; chunk numbers in what follows count
-// those alone ("steps on the way", real_chunk() says where one lies).  Keys no row
-// of the tile sees are never fetched.
+// tile then goes through the first `sinks` keys and at once behind them through those
+// from its lowest row's first key on, as if nothing lay between: key u of its way is
+// key u or u + shift, and chunks are counted along the way.  Keys on the way that no
+// row of the tile sees are never fetched.
 #pragma once
 
 #include <type_traits>
@@ -104,16 +104,12 @@ struct Seq : LineSeq {
     int tiles, chunks;
 };
 
-// Chunks that hold sinks.
-__device__ __forceinline__ int head_chunks(const SeqAttn& p, int chunk) { return (p.parts.sinks + chunk - 1) / chunk; }
 // First key behind the sinks that query token i sees (any token, also one before the first).
 __device__ __forceinline__ int lowest(const SeqAttn& p, const Seq& s, int i) {
     return max(s.first, i + s.kv_len - s.n_q - p.parts.window + 1);
 }
-// First chunk of a tile's way behind the sinks' chunks (tile_lo: the lowest of its rows).
-__device__ __forceinline__ int rest_chunk(const SeqAttn& p, int tile_lo, int chunk) {
-    return max(head_chunks(p, chunk), tile_lo / chunk);
-}
+// Keys left out on a tile's way (tile_lo: the lowest of its rows).
+__device__ __forceinline__ int left_out(const SeqAttn& p, int tile_lo) { return max(0, tile_lo - p.parts.sinks); }
 
 template <bool PARTS>
 __device__ __forceinline__ Seq seq_of(const SeqAttn& p, int b, int chunk) {
@@ -122,12 +118,11 @@ __device__ __forceinline__ Seq seq_of(const SeqAttn& p, int b, int chunk) {
     s.tiles = (s.n_q * p.G + kRows - 1) / kRows;             // (tokens * heads fits 30 bits)
     s.chunks = max(1, (s.kv_len + chunk - 1) / chunk);
     if constexpr (PARTS) {
-        // the longest way of its tiles: all of it from the lowest key of the first
-        // tile on, or what the windows of the tokens in 16 rows can touch
-        const int head = min(head_chunks(p, chunk), s.chunks);
-        const int rest = max(0, s.chunks - rest_chunk(p, lowest(p, s, 0), chunk));
-        const int64_t touched = ((int64_t)p.parts.window + (kRows + p.G - 2) / p.G + chunk - 1) / chunk + 1;
-        s.chunks = max(1, head + (s.tiles <= 1 ? rest : (int)min((int64_t)rest, touched)));
+        // the longest way of its tiles: all from the lowest key of the first tile on, or
+        // what the sinks and the windows of the tokens in 16 rows hold
+        int64_t way = s.kv_len - min(left_out(p, lowest(p, s, 0)), s.kv_len);
+        if (s.tiles > 1) way = min(way, (int64_t)p.parts.sinks + p.parts.window + (kRows + p.G - 2) / p.G);
+        s.chunks = max(1, (int)((way + chunk - 1) / chunk));
     }
     return s;
 }
@@ -351,35 +346,27 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
         const int tile_lim = limit(last_row);
         const int lim0 = limit(g), lim1 = limit(g + 8);
         // first key behind the sinks of the tile and of this thread's rows
-        int tile_lo = 0, lo0 = 0, lo1 = 0, rest = 0;
-        const int head = PARTS ? head_chunks(p, C::chunk) : 0;
+        int tile_lo = 0, lo0 = 0, lo1 = 0, shift = 0;
         if constexpr (PARTS) {
-            const int i0 = over(row_base, p.by_group);
-            tile_lo = lowest(p, sq, i0);
+            tile_lo = lowest(p, sq, over(row_base, p.by_group));
             lo0 = row_base + g < rows ? lowest(p, sq, over(row_base + g, p.by_group)) : tile_lo;
             lo1 = row_base + g + 8 < rows ? lowest(p, sq, over(row_base + g + 8, p.by_group)) : tile_lo;
-            rest = rest_chunk(p, tile_lo, C::chunk);
+            shift = left_out(p, tile_lo);
         }
-        // the chunk that is number v on the tile's way
-        auto real_chunk = [&](int v) { return PARTS && v >= head ? v - head + rest : v; };
+        // key u of the tile's way
+        auto key_at = [&](int u) { return PARTS && u >= p.parts.sinks ? u + shift : u; };
 
-        // ---- K / V fetch: step st of this warp is keys key0(st) .. + KS - 1 ----
-        int nsteps;
-        if constexpr (PARTS) {
-            const int end = (tile_lim + C::chunk - 1) / C::chunk;       // chunks that hold visible keys end here
-            nsteps = max(0, min(c1, end <= head ? end : head + max(0, end - rest)) - c0);
-        } else {
-            nsteps = min(c1 - c0, max(0, (tile_lim - c0 * C::chunk + C::chunk - 1) / C::chunk));
-        }
-        auto key0 = [&](int st) { return real_chunk(c0 + st) * C::chunk + warp * KS; };
+        // ---- K / V fetch: step st of this warp is keys u0(st) .. + KS - 1 of the way ----
+        const int end = PARTS ? max(tile_lim - shift, min(tile_lim, p.parts.sinks)) : tile_lim;
+        const int nsteps = min(c1 - c0, max(0, (end - c0 * C::chunk + C::chunk - 1) / C::chunk));
+        auto key0 = [&](int st) { return (c0 + st) * C::chunk + warp * KS; };
         const char* kb = static_cast<const char*>(p.kv.k) + h * p.kv.s_head * C::EB;
         const char* vb = static_cast<const char*>(p.kv.v) + h * (PAGED ? p.kv.s_head : p.kv.sv_head) * C::EB;
         // page of this lane's key of step st, or -1: looked up a step early, and
         // left as loaded, so that nothing waits for the load
         auto page_of = [&](int st) -> int {
-            const int key = key0(st) + lane;
+            const int key = key_at(key0(st) + lane);
             if (st >= nsteps || lane >= KS || key >= kv_len) return -1;
-            if (PARTS && key < tile_lo && key >= p.parts.sinks) return -1;
             if constexpr (!PAGED) return 0;
             return p.kv.page_table[(int64_t)(PARTS ? sq.table : b) * p.kv.max_pages + over(key, p.kv.by_page)];
         };
@@ -387,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             if (PAGED && (unsigned)page >= (unsigned)p.kv.num_pages) page = -1;
             if (st < nsteps) {
                 const int s = st % NS;
-                const int key = key0(st) + lane;
+                const int key = key_at(key0(st) + lane);
                 int64_t ko = -1, vo = -1;
                 if (page >= 0) {
                     if constexpr (PAGED) {
@@ -534,9 +521,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             }
             // ---- scale, mask, running maximum ----
             const int kfirst = key0(st);
+            // (PARTS: behind the sinks and every row's lowest; of a step among the sinks, masked
+            // or not, nothing is asked)
             const bool whole = valid == (KS == 32 ? 0xffffffffu : (1u << KS) - 1u) &&
-                               kfirst + KS <= min(lim0, lim1) &&
-                               (!PARTS || kfirst >= max(lo0, lo1) || kfirst + KS <= p.parts.sinks);
+                               (PARTS ? kfirst >= max(max(lo0, lo1) - shift, p.parts.sinks) && kfirst + KS <= min(lim0, lim1) - shift
+                                      : kfirst + KS <= min(lim0, lim1));
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -546,11 +535,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                     if (!whole) {
                         const int kk = nt * 8 + 2 * c + j;
                         const bool in = (valid >> kk) & 1u;
-                        if (!in || kfirst + kk >= lim0) a = -INFINITY;
-                        if (!in || kfirst + kk >= lim1) d = -INFINITY;
-                        if (PARTS && kfirst + kk >= p.parts.sinks) {
-                            if (kfirst + kk < lo0) a = -INFINITY;
-                            if (kfirst + kk < lo1) d = -INFINITY;
+                        const int key = key_at(kfirst + kk);
+                        if (!in || key >= lim0) a = -INFINITY;
+                        if (!in || key >= lim1) d = -INFINITY;
+                        if (PARTS && key >= p.parts.sinks) {
+                            if (key < lo0) a = -INFINITY;
+                            if (key < lo1) d = -INFINITY;
                         }
                     }
                     sc[nt][j] = a;

@@ -61,10 +61,11 @@
 // us, 1.01 to 1.09 PFLOP/s; 40 prompts of up to 700 tokens, 12/4 heads of 64, 31 us.
 //
 // PARTS (a template parameter): a row sees parts of the keys only (KeyParts).  An
-// item then goes through the steps that hold the first `sinks` keys and through
-// those from its lowest row's first key on; steps are counted along that way
-// (Item::skip of them lie between the two).  Keys of those steps that no row of
-// the item sees are cleared like those behind kv_len.
+// item then goes through the first keys, as many as there are sinks, rounded up to
+// whole boxes (TcParams::head of them), and behind them at once through those from
+// its lowest row's first key on, rounded down to a box's: what is left out between
+// the two is Item::shift keys, and key u of its way is key u or u + shift.  Keys on the
+// way that no row of the item sees are cleared like those behind kv_len.
 #pragma once
 
 #include <type_traits>
@@ -92,6 +93,7 @@ constexpr int kMinShare = 2;                // fewest steps of a part (1: 8 prom
 // pages of 32 tokens 195 us, of 16 217, of 8 317 (row by row 302); E4M3 pages of
 // 16 tokens 290 us, of 8 300 (row by row 415).
 constexpr int kMinBox = 16, kMinBox8 = 8;
+constexpr int kBoxWindow = 32;
 constexpr int kMinRange = kStep;            // shortest range of a CTA, in keys
 constexpr int kMaxCtas = 160;               // ranges (the workspace's size goes by it)
 
@@ -155,7 +157,7 @@ struct TcParams {
     uint64_t ctas_mul;                  // x / ctas = high word of x * ctas_mul for x < 2^56
     int charge;                         // an item's fixed cost, in keys
     int out32;                          // out is 32-byte aligned
-    int head;                           // steps that hold sinks
+    int head, align;                    // keys before the window's on an item's way; what those begin at a multiple of
     int box, box_shift, boxes;          // keys of a TMA box (and its log2), boxes of a step
     float* ws_o;                        // [2 * kMaxCtas][D / 4][kItemRows][4] parts
     float* ws_ml;                       // [2 * kMaxCtas][kItemRows][2] (m, sum)
@@ -207,22 +209,23 @@ __device__ __forceinline__ int lowest(const TcParams& p, const Seq& s, int tok) 
     return max(s.first, tok + s.kv_len - s.n_q - p.a.parts.window + 1);
 }
 
-// Steps on the way to key `end` of an item whose lowest key behind the sinks is lo,
-// and the number of steps left out (no end: a large one).
+// Keys left out on the way of an item whose lowest key behind the sinks is lo.
+__device__ __forceinline__ int left_out(const TcParams& p, int lo) { return max(0, (lo & -p.align) - p.head); }
+
+// Steps on its way to key `end`.
 template <bool PARTS>
 __device__ __forceinline__ int steps_to(const TcParams& p, int end, int lo) {
-    const int n = (end + kStep - 1) / kStep;
-    if (!PARTS || n <= p.head) return n;
-    return p.head + max(0, n - max(p.head, lo / kStep));
+    if constexpr (PARTS) end = max(end - left_out(p, lo), min(end, p.head));
+    return (end + kStep - 1) / kStep;
 }
 
-// What tile j costs: its keys (less those between the sinks' steps and its window;
-// counted in keys, not in steps, for the sum below) and the charge.
+// What tile j costs: its keys (less those between the sinks and its window; without
+// the rounding, for the sum below) and the charge.
 template <bool PARTS>
 __device__ __forceinline__ int cost(const TcParams& p, const Seq& s, int j) {
     const int U = 2 * p.TR, end = visible(p, s, (j + 1) * U);
     if constexpr (!PARTS) return end + p.charge;
-    const int64_t gap = (int64_t)j * U + s.kv_len - s.n_q + 1 - p.a.parts.window - (int64_t)p.head * kStep;
+    const int64_t gap = (int64_t)j * U + s.kv_len - s.n_q + 1 - p.a.parts.window - p.head;
     return max(0, end - s.first) - (int)max(gap, (int64_t)0) + p.charge;
 }
 
@@ -242,7 +245,7 @@ __device__ __forceinline__ int64_t cost_before(const TcParams& p, const Seq& s, 
     sum += (full - first) * off + U * (full * (full + 1) - first * (first + 1)) / 2;
     if constexpr (PARTS) {
         // less the gaps, i U + a for the tiles i >= from where that is positive
-        const int64_t a = (int64_t)s.kv_len - s.n_q + 1 - p.a.parts.window - (int64_t)p.head * kStep;
+        const int64_t a = (int64_t)s.kv_len - s.n_q + 1 - p.a.parts.window - p.head;
         const int64_t from = a > 0 ? 0 : units(p, (int)min(-a, (int64_t)0x7ffffffe)) + 1;
         if (j > from) sum -= (j - from) * a + U * ((int64_t)j * (j - 1) - from * (from - 1)) / 2;
     }
@@ -347,7 +350,7 @@ struct Item {
     int s0, n[2];               // first step, steps of each tile
     int whole;                  // all of the item's keys
     // PARTS:
-    int skip;                   // steps between those of the sinks and the rest of its way
+    int shift;                  // keys left out between the sinks and the rest of its way
     int first, lo;              // keys of a shared prefix; the item's lowest key behind the sinks
     int pad[2];
 };
@@ -389,7 +392,7 @@ struct Walk {
             const int v1 = visible(p, s, (j + 1) * U), N = steps_to<PARTS>(p, v1, lo);
             const int s0 = cut(x0, c, N), s1 = cut(x1, c, N);
             if constexpr (PARTS) {
-                it.skip = max(p.head, lo / kStep) - p.head;
+                it.shift = left_out(p, lo);
                 it.first = s.first;
                 it.lo = lo;
             }
@@ -434,10 +437,10 @@ __device__ __forceinline__ uint32_t codes_h2(uint32_t x) {
     return h;
 }
 
-// The step that is number v on an item's way.
+// Key u of an item's way.
 template <bool PARTS>
-__device__ __forceinline__ int real_step(const TcParams& p, const Item& it, int v) {
-    return PARTS && v >= p.head ? v + it.skip : v;
+__device__ __forceinline__ int key_at(const TcParams& p, const Item& it, int u) {
+    return PARTS && u >= p.head ? u + it.shift : u;
 }
 
 // Hands item number i (counting from 0) on; the end of the range as b < 0.  One thread.
@@ -575,7 +578,7 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
         // loaded, so that nothing waits for the load)
         int ahead;
         auto look_up = [&](int st) {
-            const int key = real_step<PARTS>(p, it, s0 + st) * kStep + x;
+            const int key = key_at<PARTS>(p, it, (s0 + st) * kStep + x);
             const bool seen = !PARTS || key >= it.lo || key < a.parts.sinks;
             ahead = st < n && key < kv_len && seen ? table[page_slot(p, key)] : -1;
         };
@@ -587,7 +590,7 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
         // warp still reads for the last step of an odd number.)
         auto table_of = [&](int st) { return rows + ((steps + st) & 1) * kStep; };
         auto find_rows = [&](int st) -> bool {
-            const int key = real_step<PARTS>(p, it, s0 + st) * kStep + x, place = key - page_slot(p, key) * a.kv.page_size;
+            const int key = key_at<PARTS>(p, it, (s0 + st) * kStep + x), place = key - page_slot(p, key) * a.kv.page_size;
             const uint32_t pg = (uint32_t)ahead;
             table_of(st)[x] = pg >= (uint32_t)a.kv.num_pages ? 0xffffffffu
                               : p.hnd ? (pg * a.kv.Hkv + h) * a.kv.page_size + place
@@ -664,8 +667,9 @@ __device__ __forceinline__ void move_rows(const TcParams& p, unsigned char* smem
                 const int load = loads + 2 * st + g;
                 ok = all(mbar_wait(bar(B_STAGE + g), (load >> 1) & 1, err, abort_flag)) && wait_free(load);
                 if (!ok) break;
-                const int key0 = real_step<PARTS>(p, it, s0 + st) * kStep;
-                widen(load, x & 63, kMovers / 2, kv_len - key0, PARTS ? a.parts.sinks - key0 : 0, PARTS ? it.lo - key0 : 0);
+                const int u0 = (s0 + st) * kStep;
+                widen(load, x & 63, kMovers / 2, (PARTS ? kv_len - it.shift : kv_len) - u0, PARTS ? a.parts.sinks - u0 : 0,
+                      PARTS ? it.lo - it.shift - u0 : 0);
                 arrive(B_STAGE_FREE + g);
                 fence_proxy_async_smem();
                 arrive(B_FULL + load % L::slots);
@@ -814,9 +818,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 // page of this lane's box of a step, -1 if there is none to read
                 // (left as loaded, so that nothing waits for the load)
                 auto page_of = [&](int st) -> int {
-                    const int key = real_step<PARTS>(p, it, it.s0 + st) * kStep + lane * p.box;
+                    const int key = key_at<PARTS>(p, it, (it.s0 + st) * kStep + lane * p.box);
                     if (st >= n || lane >= p.boxes || key >= it.kv_len) return -1;
-                    if (PARTS && key >= a.parts.sinks && key + p.box <= it.lo) return -1;
                     return a.kv.page_table[(int64_t)it.b * a.kv.max_pages + page_slot(p, key)];
                 };
                 int page = 0;
@@ -844,7 +847,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     tail = -1;
                 };
                 for (int st = 0; st < n && ok; ++st) {
-                    const int key0 = real_step<PARTS>(p, it, it.s0 + st) * kStep;
+                    const int u0 = (it.s0 + st) * kStep;
                     const int pg = (unsigned)page < (unsigned)a.kv.num_pages ? page : -1;
                     if constexpr (PAGED) page = page_of(st + 1);
                     for (int kv = 0; kv < 2 && ok; ++kv) {
@@ -858,11 +861,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         const uint32_t dst = sbase + (L::gather ? L::staging + s * kStep * D : L::ring + s * L::tile);
                         bool clears = false;
                         if (!L::gather && kv == 1) {
-                            real = it.kv_len - key0;                   // keys of this tile that exist
+                            real = (PARTS ? it.kv_len - it.shift : it.kv_len) - u0;    // keys of this tile that exist
                             if constexpr (PARTS) {
                                 // those between the sinks and the item's lowest, [gap0, gap1)
-                                gap0 = max(a.parts.sinks - key0, 0);
-                                gap1 = min(it.lo - key0, kStep);
+                                gap0 = max(a.parts.sinks - u0, 0);
+                                gap1 = min(it.lo - it.shift - u0, kStep);
                             }
                             clears = real < kStep || gap0 < gap1;
                             if (clears) tail = s;
@@ -875,7 +878,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                             if (lane < p.boxes) {
                                 // a box without a page reads page num_pages: outside, zeros
                                 const int at = pg < 0 ? a.kv.num_pages : pg;
-                                const int key = key0 + lane * p.box;
+                                const int key = key_at<PARTS>(p, it, u0 + lane * p.box);
                                 const int place = pg < 0 ? 0 : key - page_slot(p, key) * a.kv.page_size;
                                 constexpr int kRow = L::gather ? D : 128;          // bytes of a box's row
                                 for (int pn = 0; pn < (L::gather ? 1 : L::panels); ++pn) {
@@ -884,9 +887,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                                     else tma_load_4d(to, map, pn * 64, it.h, place, at, b);
                                 }
                             }
-                        } else if (lane == 0) {
+                        } else if (lane < (PARTS ? p.boxes : 1)) {
+                            const int row = it.k_row + key_at<PARTS>(p, it, PARTS ? u0 + lane * p.box : u0);
                             for (int pn = 0; pn < L::panels; ++pn)
-                                tma_load_3d(dst + pn * L::panel, map, pn * 64, it.h, it.k_row + key0, b);
+                                tma_load_3d(dst + pn * L::panel + (PARTS ? lane * p.box * 128 : 0), map, pn * 64, it.h, row, b);
                         }
                         ++loads;
                         if (PARTS && kv == 1 && st == 0) load_q();
@@ -1090,11 +1094,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             auto look_up = [&](int st) {
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) {
-                    const int box = lane + 32 * i, key = real_step<PARTS>(p, it, it.s0 + st) * kStep + box * p.box;
+                    const int box = lane + 32 * i, key = key_at<PARTS>(p, it, (it.s0 + st) * kStep + box * p.box);
                     ahead[i] = 0;
                     if (i > 0 && 32 * i >= p.boxes) continue;          // (the same for all lanes)
-                    const bool seen = !PARTS || key + p.box > it.lo || key < a.parts.sinks;
-                    if (st < n && box < p.boxes && key < it.kv_len && seen)
+                    if (st < n && box < p.boxes && key < it.kv_len)
                         ahead[i] = a.kv.page_table[(int64_t)it.b * a.kv.max_pages + page_slot(p, key)];
                 }
             };
@@ -1120,16 +1123,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     if (st == n - 1) mbar_arrive(bar(B_Q_FREE));
                 }
                 tc_fence_after();
-                const int key0 = real_step<PARTS>(p, it, it.s0 + st) * kStep;
-                const bool begins = PARTS && lo_max > key0 && key0 + kStep > a.parts.sinks;
-                if (lim_min < key0 + kStep || begins || (PAGED && missing)) {
+                // (counted along the item's way)
+                const int u0 = (it.s0 + st) * kStep, shift = PARTS ? it.shift : 0;
+                const bool begins = PARTS && u0 < lo_max - shift;
+                if (lim_min - shift < u0 + kStep || begins || (PAGED && missing)) {
                     // Masked in place, 32 keys at a time where a row of this warp does
                     // not see all.  (A loop through tensor memory, not 128 registers:
                     // what counts here is the code to be fetched.)
 #pragma unroll 1
                     for (int q = 0; q < kStep; q += 32) {
-                        uint32_t in = bits_below(lim - key0 - q);       // a bit a key: which ones this row sees
-                        if constexpr (PARTS) in &= ~bits_below(lo - key0 - q) | bits_below(a.parts.sinks - key0 - q);
+                        const int u = u0 + q;
+                        uint32_t in = bits_below(lim - shift - u);       // a bit a key: which ones this row sees
+                        if constexpr (PARTS)
+                            in = (in & ~bits_below(lo - shift - u)) | bits_below(min(a.parts.sinks, lim) - u);
                         if (PAGED && missing) {
                             // without those of the boxes that have no page
 #pragma unroll
@@ -1593,8 +1599,8 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStr
         if (L::f8 && p.box >= kMinBox8 && (!codes_map(&mk, a.kv.k, a.kv, p.hnd, p.box) || !codes_map(&mv, a.kv.v, a.kv, p.hnd, p.box)))
             return cudaErrorInvalidValue;
     } else if (SRC == SRC_PAGES ? (!pool_map(&mk, a.kv.k, bf16, a.kv, p.hnd, p.box) || !pool_map(&mv, a.kv.v, bf16, a.kv, p.hnd, p.box))
-              : (!rows_map(&mk, a.kv.k, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.s_tok, 1, kStep) ||
-                 !rows_map(&mv, a.kv.v, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.sv_tok, 1, kStep))) {
+              : (!rows_map(&mk, a.kv.k, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.s_tok, 1, PARTS ? p.box : kStep) ||
+                 !rows_map(&mv, a.kv.v, bf16, D, a.kv.Hkv, max(a.kv.rows, 1), a.kv.sv_tok, 1, PARTS ? p.box : kStep))) {
         return cudaErrorInvalidValue;
     }
     auto kern = attn_tc_kernel<E, D, SRC, PARTS>;
@@ -1635,10 +1641,15 @@ cudaError_t launch_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaStream
     p.box = kStep;
     if (a.kv.page_table)
         while (a.kv.page_size % p.box != 0) p.box /= 2;
+    // Sinks and windows in boxes of at most 32 keys: what is rounded costs less.  (Packed
+    // rows without sinks begin anywhere, and come as one box.)
+    const bool windowed = PARTS && a.parts.phase == PHASE_ALL;
+    if (windowed && (a.kv.page_table || a.parts.sinks > 0)) p.box = p.box < kBoxWindow ? p.box : kBoxWindow;
+    p.align = a.kv.page_table ? p.box : 1;
+    p.head = PARTS ? (a.parts.sinks + p.box - 1) / p.box * p.box : 0;
     p.boxes = kStep / p.box;
     while ((1 << p.box_shift) < p.box) ++p.box_shift;
     p.by_unit = divide_by(2 * p.TR);
-    p.head = PARTS ? (a.parts.sinks + kStep - 1) / kStep : 0;
     p.ctas_mul = ~uint64_t(0) / (uint64_t)(num_sms < kMaxCtas ? num_sms : kMaxCtas) + 1;
     // Measured (448 / 576): chunks of 200 to 1,024 tokens over 16-bit pages 199.8 /
     // 202.0 us, 4 causal prompts of 2,048 tokens 139.6 / 145.5 us; 64-dim ones (320 /
