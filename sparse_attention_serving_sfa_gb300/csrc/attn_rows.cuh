@@ -179,6 +179,7 @@ __device__ __forceinline__ Line line_at(const SeqAttn& p, int chunk, uint64_t ct
             l.seq.tiles = __shfl_sync(0xffffffffu, mine_seq.tiles, w);
             l.seq.chunks = __shfl_sync(0xffffffffu, mine_seq.chunks, w);
             l.seq.first = PARTS ? __shfl_sync(0xffffffffu, mine_seq.first, w) : 0;
+            l.seq.shared = PARTS ? __shfl_sync(0xffffffffu, mine_seq.shared, w) : 0;
             l.seq.table = PARTS ? __shfl_sync(0xffffffffu, mine_seq.table, w) : l.b;
             return l;
         }
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
     const uint32_t ring_u = smem_u32(ring);
     volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + C::masks) + warp * NS;
     float* ml = reinterpret_cast<float*>(smem + C::ml);
+    const uint64_t policy = PARTS ? l2_policy(p.parts.once) : 0;
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
         auto limit = [&](int r) -> int {
             if (!p.causal || row_base + r >= rows) return kv_len;
             const int i = over(row_base + r, p.by_group);
-            return max(0, min(kv_len, i + kv_len - n_q + 1));
+            return max(PARTS ? sq.shared : 0, min(kv_len, i + kv_len - n_q + 1));
         };
         const int last_row = min(kRows, rows - row_base) - 1;
         const int tile_lim = limit(last_row);
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             const int key = key_at(key0(st) + lane);
             if (st >= nsteps || lane >= KS || key >= kv_len) return -1;
             if constexpr (!PAGED) return 0;
-            return p.kv.page_table[(int64_t)(PARTS ? sq.table : b) * p.kv.max_pages + over(key, p.kv.by_page)];
+            return p.kv.page_table[(int64_t)(PARTS && key < sq.shared ? sq.table : b) * p.kv.max_pages + over(key, p.kv.by_page)];
         };
         auto issue = [&](int st, int page) {
             if (PAGED && (unsigned)page >= (unsigned)p.kv.num_pages) page = -1;
@@ -395,8 +397,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                     int64_t o2 = o;
                     if constexpr (!PAGED) o2 = __shfl_sync(0xffffffffu, vo, key_i);
                     unsigned char* dst = ring + s * C::stage + piece_at<RB, F8>(key_i, ch);
-                    cp_async_16_zfill(dst, kb + (o < 0 ? 0 : o * C::EB + ch * 16), o < 0 ? 0 : 16);
-                    cp_async_16_zfill(dst + C::tile, vb + (o < 0 ? 0 : o2 * C::EB + ch * 16), o < 0 ? 0 : 16);
+                    const char *ks = kb + (o < 0 ? 0 : o * C::EB + ch * 16), *vs = vb + (o < 0 ? 0 : o2 * C::EB + ch * 16);
+                    if constexpr (PARTS) {
+                        cp_async_16_zfill(dst, ks, o < 0 ? 0 : 16, policy);
+                        cp_async_16_zfill(dst + C::tile, vs, o < 0 ? 0 : 16, policy);
+                    } else {
+                        cp_async_16_zfill(dst, ks, o < 0 ? 0 : 16);
+                        cp_async_16_zfill(dst + C::tile, vs, o < 0 ? 0 : 16);
+                    }
                 }
             }
             cp_async_commit();

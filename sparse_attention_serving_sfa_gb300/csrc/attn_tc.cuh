@@ -312,6 +312,7 @@ __device__ __forceinline__ Line line_at(const TcParams& p) {
             l.seq.kv_len = __shfl_sync(0xffffffffu, mine_seq.kv_len, w);
             l.seq.tiles = __shfl_sync(0xffffffffu, mine_seq.tiles, w);
             l.seq.first = PARTS ? __shfl_sync(0xffffffffu, mine_seq.first, w) : 0;
+            l.seq.shared = 0;
             l.seq.table = PARTS ? __shfl_sync(0xffffffffu, mine_seq.table, w) : l.b;
             return l;
         }
@@ -774,6 +775,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             if constexpr (L::gather) move_rows<D, SRC, PARTS>(p, smem, sbase, tid - kMoveWarp * 32);
         } else if (warp == kLoadWarp) {
             // ============================ loader ============================
+            const uint64_t policy = PARTS ? l2_policy(a.parts.once) : 0;
             int number = 0;
             int items = 0, loads = 0, tails = 0;   // items with keys, tiles loaded, tiles cleared
             int qs[2] = {0, 0};                    // Q tiles loaded
@@ -883,8 +885,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                                 constexpr int kRow = L::gather ? D : 128;          // bytes of a box's row
                                 for (int pn = 0; pn < (L::gather ? 1 : L::panels); ++pn) {
                                     const uint32_t to = dst + pn * L::panel + lane * p.box * kRow;
-                                    if (p.hnd) tma_load_4d(to, map, pn * 64, place, it.h, at, b);
-                                    else tma_load_4d(to, map, pn * 64, it.h, place, at, b);
+                                    const int c1 = p.hnd ? place : it.h, c2 = p.hnd ? it.h : place;
+                                    if constexpr (PARTS) tma_load_4d(to, map, pn * 64, c1, c2, at, b, policy);
+                                    else tma_load_4d(to, map, pn * 64, c1, c2, at, b);
                                 }
                             }
                         } else if (lane < (PARTS ? p.boxes : 1)) {
@@ -1587,6 +1590,11 @@ bool codes_map(CUtensorMap* m, const void* base, const SeqKV& kv, bool hnd, int 
               kv.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Items of a prefix's pass at most.
+int64_t prefix_items(const SeqAttn& a) {
+    return ((int64_t)a.tokens / (2 * (kTileM / a.G)) + a.parts.groups) * a.kv.Hkv;
+}
+
 template <class E, int D, int SRC, bool PARTS>
 cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStream_t stream) {
     using L = TcSmem<D, SRC>;
@@ -1619,8 +1627,7 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStr
     // items of fewer than 2 kMinShare steps are never cut
     if (longest >= 2 * kMinShare * kStep - kStep + 1) {
         // (a prefix's items at most; with fewer than ranges most are cut often)
-        const int64_t items = PARTS && a.parts.phase == PHASE_PREFIX
-                                  ? ((int64_t)a.tokens / (2 * p.TR) + a.parts.groups) * a.kv.Hkv : ctas;
+        const int64_t items = PARTS && a.parts.phase == PHASE_PREFIX ? prefix_items(a) : ctas;
         if constexpr (PARTS) {
             if (items < ctas)
                 err = launch_pdl(attn_tc_merge_prefix<D>, dim3(kPrefixBlocks * ctas), dim3(kMergeThreads), 0, stream, p, ctas - 1);
@@ -1636,6 +1643,8 @@ template <bool PARTS>
 cudaError_t launch_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaStream_t stream) {
     TcParams p{};
     p.a = a;
+    // (a prefix of few items; with many its keys are read again and again)
+    p.a.parts.once = PARTS && a.parts.phase == PHASE_PREFIX && prefix_items(a) < num_sms;
     p.TR = kTileM / a.G;
     p.hnd = a.kv.s_tok == a.kv.D && a.kv.Hkv > 1 ? 1 : 0;
     p.box = kStep;

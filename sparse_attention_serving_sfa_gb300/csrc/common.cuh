@@ -91,6 +91,15 @@ __device__ __forceinline__ void cp_async_16_zfill(void* smem_dst, const void* gm
                  : "memory");
 }
 
+// The same under an L2 policy (l2_policy()).
+__device__ __forceinline__ void cp_async_16_zfill(void* smem_dst, const void* gmem_src, int src_bytes,
+                                                  uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n" ::"r"(
+                     smem_u32(smem_dst)),
+                 "l"(gmem_src), "r"(src_bytes), "l"(policy)
+                 : "memory");
+}
+
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;\n" ::: "memory");
 }

@@ -55,10 +55,13 @@ struct SeqKV {
 // groups, whose rows are those of all sequences of the group and whose keys are the
 // first shared_lens[g] of its first sequence, all visible; results stay
 // unnormalised in px_o and px_ml, a row a row.  OWN: each sequence's rows over its
-// keys from `first` on, joined with those results at the end.
-enum { PHASE_ALL = 0, PHASE_PREFIX = 1, PHASE_OWN = 2 };
+// keys from `first` on, joined with those results at the end.  Or, where there is
+// little to share, once (DIRECT, few rows only): each sequence's rows over the shared
+// keys, from the pages of the group's first sequence, and its own.
+enum { PHASE_ALL = 0, PHASE_PREFIX = 1, PHASE_OWN = 2, PHASE_DIRECT = 3 };
 struct KeyParts {
     int phase;
+    int once;                    // the pass reads each key about once
     int window, sinks;           // at most 2^30; window 2^30: none
     const int32_t* cu_shared;    // [groups + 1]: group g is sequences cu_shared[g] .. cu_shared[g + 1] - 1
     const int32_t* shared_lens;  // [groups]
@@ -135,10 +138,11 @@ __device__ __forceinline__ int2 seq_keys(const SeqKV& kv, int b) {
     return make_int2(r.x, r.y - r.x);
 }
 
-// Sequence b of the line of a call: its rows [q_row, q_row + n_q), keys (k_row and
-// kv_len as seq_keys; `first` of them belong to a shared prefix) and page table row.
+// Sequence b of the line of a call: its rows [q_row, q_row + n_q) and keys (k_row and
+// kv_len as seq_keys).  With parts: its rows see none before `first`; the pages of the
+// first `shared` are in row `table` of the page table, and all rows see those.
 struct LineSeq {
-    int q_row, n_q, k_row, kv_len, first, table;
+    int q_row, n_q, k_row, kv_len, first, shared, table;
 };
 template <bool PARTS>
 __device__ __forceinline__ int line_seqs(const SeqAttn& p) {
@@ -147,7 +151,7 @@ __device__ __forceinline__ int line_seqs(const SeqAttn& p) {
 template <bool PARTS>
 __device__ __forceinline__ LineSeq line_seq(const SeqAttn& p, int b) {
     LineSeq s;
-    s.first = 0;
+    s.first = s.shared = 0;
     s.table = b;
     const KeyParts& x = p.parts;
     if (PARTS && x.phase == PHASE_PREFIX) {
@@ -156,7 +160,7 @@ __device__ __forceinline__ LineSeq line_seq(const SeqAttn& p, int b) {
         s.q_row = min(max(p.cu_q[in.x], 0), p.tokens);
         s.n_q = in.x < in.y ? min(max(p.cu_q[in.y], s.q_row), p.tokens) - s.q_row : 0;
         s.k_row = 0;
-        s.kv_len = (int)min((int64_t)max(x.shared_lens[b], 0), (int64_t)p.kv.max_pages * p.kv.page_size);
+        s.kv_len = s.shared = (int)min((int64_t)max(x.shared_lens[b], 0), (int64_t)p.kv.max_pages * p.kv.page_size);
         return s;
     }
     const int2 q = seq_rows(p.cu_q, b, p.tokens);
@@ -165,7 +169,7 @@ __device__ __forceinline__ LineSeq line_seq(const SeqAttn& p, int b) {
     s.n_q = q.y - q.x;
     s.k_row = k.x;
     s.kv_len = k.y;
-    if (PARTS && x.phase == PHASE_OWN) {
+    if (PARTS && x.phase >= PHASE_OWN) {
         // its group: the last that begins at or before b
         int lo = 0, hi = x.groups;                       // lo: cu_shared[1 .. lo] <= b
         while (lo < hi) {
@@ -173,8 +177,15 @@ __device__ __forceinline__ LineSeq line_seq(const SeqAttn& p, int b) {
             if (x.cu_shared[mid + 1] <= b) lo = mid + 1;
             else hi = mid;
         }
-        if (lo < x.groups && x.cu_shared[lo] <= b)
+        if (lo < x.groups && x.cu_shared[lo] <= b) {
             s.first = (int)min((int64_t)max(x.shared_lens[lo], 0), (int64_t)p.kv.max_pages * p.kv.page_size);
+            if (x.phase == PHASE_DIRECT) {
+                s.shared = s.first;
+                s.first = 0;
+                s.kv_len = max(s.kv_len, s.shared);
+                s.table = max(x.cu_shared[lo], 0);
+            }
+        }
     }
     return s;
 }

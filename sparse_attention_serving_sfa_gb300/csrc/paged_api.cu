@@ -163,6 +163,11 @@ sfa_status launch_attention(SeqAttn& p, bool parts, const Call& c) {
     return err == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
+sfa_status launch_rows_parts(const SeqAttn& p, const Call& c) {
+    const cudaError_t err = launch_attn_rows_parts(p, c.dtype, num_sms(), reinterpret_cast<cudaStream_t>(c.stream));
+    return err == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+}
+
 // Packed keys and values as `kv`.
 sfa_status resolve_packed(SeqKV& kv, const void* q, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                           const int32_t* cu_seqlens_k, int num_seqs, int num_keys, int Hq, int Hkv, int D) {
@@ -197,6 +202,18 @@ sfa_status run_attention(SeqAttn& p, const Call& c, int window, int sinks) {
     p.parts.window = window;
     p.parts.sinks = sinks;
     return launch_attention(p, true, c);
+}
+
+// Where every sequence reading the shared keys for itself moves no more than this (by
+// what the table can hold, and few rows each), one pass over all keys is faster than
+// two passes and their joins.  Two passes and one, us: 8 sequences behind 500 keys (20
+// MB) 16.5 and 9.9, behind 2,000 (66 MB) 20.6 and 14.4, behind 8,000 (254 MB) 27.8 and
+// 35.7; 16 behind 2,000 (133 MB) 22.1 and 21.5; 32 behind 2,000 (266 MB) 27.1 and
+// 36.4; E4M3, 16 behind 4,000 (129 MB) 28.8 and 27.7, 32 behind 4,000 (258 MB) 37.4
+// and 46.6; 2 kv heads, 8 behind 4,000 (32 MB) 21.6 and 11.7.
+constexpr int64_t kDirectBytes = 128 << 20;
+int64_t direct_bytes(const SeqAttn& p) {
+    return p.kv.num_seqs * most_keys(p.kv) * p.kv.Hkv * p.kv.D * (p.kv.f8 ? 2 : 4);
 }
 
 // Results of a shared prefix's pass, behind the workspace of a pass.
@@ -342,6 +359,9 @@ sfa_status paged_run_shared(const paged_kv* cache, const void* q, int64_t q_stri
     p.parts.window = kNoWindow;
     p.parts.px_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + pass);
     p.parts.px_ml = p.parts.px_o + (int64_t)num_tokens * num_qo_heads * p.kv.D;
+    p.parts.phase = PHASE_DIRECT;
+    if (few_rows(p) && (int64_t)direct_bytes(p) <= kDirectBytes) return launch_rows_parts(p, c);
+    p.parts.once = 1;
     SeqAttn prefix = p;
     prefix.parts.phase = PHASE_PREFIX;
     prefix.causal = 0;
