@@ -710,17 +710,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
                 if (PARTS && p.parts.phase == PHASE_PREFIX) {
                     store_prefix(p, row, D, d0, acc, M, L, (tid & 7) == 0);
                 } else {
-                if (PARTS && sq.first > 0) join_prefix(p, row, D, d0, acc, M, L);
-                const float vs = F8 && p.kv.scale_v ? p.kv.scale_v[h] : 1.f;
-                const bool none = L == 0.f;        // no visible key (a NaN sum is not that)
-                const float inv = none ? 0.f : vs / L;
-                typename E::T* dst = static_cast<typename E::T*>(p.out) + row * D + d0;
+                    if (PARTS && sq.first > 0) join_prefix(p, row, D, d0, acc, M, L);
+                    const float vs = F8 && p.kv.scale_v ? p.kv.scale_v[h] : 1.f;
+                    const bool none = L == 0.f;        // no visible key (a NaN sum is not that)
+                    const float inv = none ? 0.f : vs / L;
+                    typename E::T* dst = static_cast<typename E::T*>(p.out) + row * D + d0;
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    *reinterpret_cast<uint2*>(dst + 32 * i) =
-                        none ? make_uint2(0u, 0u)
-                             : make_uint2(E::pack2(acc[i].x * inv, acc[i].y * inv), E::pack2(acc[i].z * inv, acc[i].w * inv));
-                if (p.lse && (tid & 7) == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L) - kPShift<E, F8>) * kLn2;
+                    for (int i = 0; i < N; ++i)
+                        *reinterpret_cast<uint2*>(dst + 32 * i) =
+                            none ? make_uint2(0u, 0u)
+                                 : make_uint2(E::pack2(acc[i].x * inv, acc[i].y * inv), E::pack2(acc[i].z * inv, acc[i].w * inv));
+                    if (p.lse && (tid & 7) == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L) - kPShift<E, F8>) * kLn2;
                 }
             } else {
                 const int slot = 2 * blockIdx.x + (c0 == 0 ? 1 : 0);

@@ -1,6 +1,7 @@
 """Attention of batches that share their first tokens, on the GPU, against plain 64-bit
 arithmetic and against attention over each sequence's own pages; and runs of rotated
 appends, windowed and shared attention as a serving program makes them."""
+import ctypes
 import math
 from concurrent.futures import ThreadPoolExecutor
 
@@ -114,16 +115,19 @@ def test_shared_prefix(shape, cache, layout, dtype):
 
 
 @pytest.mark.parametrize("cache,dtype,page", [("same", "bf16", 16), ("same", "f16", 20), ("e4m3", "f16", 64), ("e5m2", "bf16", 12)])
-@pytest.mark.parametrize("shape", [1, 2, 4, 5, 7])
+@pytest.mark.parametrize("shape", [0, 1, 2, 4, 5, 6, 7])
 def test_table_much_wider_than_the_sequences(shape, page, cache, dtype):
-    """The large tiles on both passes wherever there are more than a few rows."""
+    """By what the table could hold there is much to share: a pass over the prefixes and
+    one over the own tokens, on either kernel, the large tiles wherever there are more
+    than a few rows."""
     q_lens, own, heads, kv_heads, dim, _, groups, skip = SHAPES[shape]
     c = Shared(400 + shape, q_lens, own, heads, kv_heads, dim, page, dtype, cache, groups=groups, skip=skip, behind=1).poison()
     c.table = torch.cat([c.table, torch.full((len(q_lens), (1 << 20) // page), -1, dtype=torch.int32)], 1)
-    out, lse = run_shared(c, True, 0)
-    check_shared(c, out, lse, True)
-    again, lse2 = run_shared(c, True, 0)
-    assert torch.equal(out, again) and torch.equal(lse, lse2)          # nothing depends on timing
+    for hint in (max(q_lens), 1, 0):
+        out, lse = run_shared(c, True, hint)
+        check_shared(c, out, lse, True)
+        again, lse2 = run_shared(c, True, hint)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)      # nothing depends on timing
 
 
 @pytest.mark.parametrize("cache,dtype", [("same", "bf16"), ("e4m3", "bf16")])
@@ -280,6 +284,25 @@ def calls(c, d, freq, out):
                                 max_q_len=max(c.q_lens), out=out[2], **kw(c, d))
 
 
+def test_the_interpreter_lock_is_let_go():
+    """While the library runs, other Python threads can: its entry points, stood in for
+    by the function that tells whether the calling thread holds the lock."""
+    lib, native = sfa.load(), sfa._native()
+
+    def address(f):
+        return ctypes.cast(f, ctypes.c_void_p).value
+    held = address(ctypes.pythonapi.PyGILState_Check)
+    c, d, freq, out = setup(3)
+    q, k, v = c.split(d["qkv"])
+    native.bind_more(held, held, held, held, address(lib.paged_shared_workspace_size))
+    try:                                    # status 1 (held) would raise
+        calls(c, d, freq, out)
+        sfa.varlen_attention(q, k, v, d["cu"], d["cu"], window=5)
+    finally:
+        native.bind_more(*[address(f) for f in (lib.paged_append_rotated, lib.paged_run_window, lib.varlen_run_window,
+                                                lib.paged_run_shared, lib.paged_shared_workspace_size)])
+
+
 def setup(i, q_len=1, cache="same", dtype="f16"):
     n = 9
     c = Shared(50 + i, [q_len + (b % 3 if q_len > 1 else 0) for b in range(n)], [q_len + 9 * b + 2 for b in range(n)], 16, 4, 128, 16,
@@ -349,10 +372,15 @@ def test_streams_graphs_and_threads(q_len, cache):
     assert sfa.sfa_get_last_error() == sfa.SFA_OK
 
 
-def test_captured_step_follows_the_lists():
+@pytest.mark.parametrize("wide", [False, True])
+def test_captured_step_follows_the_lists(wide):
     """One captured step, replayed as lengths, groups and shared lengths change on the
-    device."""
+    device; with a wide table the shared tokens have a pass of their own."""
     c, d, freq, out = setup(9, 1, "same", "bf16")
+    if wide:
+        room = torch.full((9, 1 << 15), -1, dtype=torch.int32)
+        c.table = torch.cat([c.table, room], 1)
+        d["table"] = c.table.cuda()
     final = d["lens"].clone()
     d["lens"] -= 4
 
