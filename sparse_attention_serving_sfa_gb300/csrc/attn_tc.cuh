@@ -124,7 +124,7 @@ struct TcSmem {
     static constexpr int staging = ring + slots * tile;    // two tiles of 8-bit rows
     static constexpr int rows = staging + (f8 ? 2 * kStep * D : 0);   // row numbers of two steps
     static constexpr int bars = rows + (gather ? 2 * kStep * 4 : 0);
-    static constexpr int items = bars + 8 * 38;            // the two items being worked on
+    static constexpr int items = bars + 8 * 40;            // the two items being worked on
     static constexpr int abort = items + 2 * 64;
     static constexpr int tmem_slot = abort + 4;
     static constexpr int total = abort + 16;
@@ -147,7 +147,8 @@ enum {
     B_ITEM = 30,        // + i: item slot i written
     B_ITEM_FREE = 32,   // + i: item slot i read by the MMA, softmax and mover warps
     B_STAGE = 34,       // + i: staging tile i landed
-    B_STAGE_FREE = 36   // + i: staging tile i read (one arrival a mover warp that does)
+    B_STAGE_FREE = 36,  // + i: staging tile i read (one arrival a mover warp that does)
+    B_QRAW = 38         // + t: rows of Q tile t landed, still to be scaled
 };
 
 struct TcParams {
@@ -740,6 +741,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(bar(B_PH + t), 4);
             mbar_init(bar(B_O + t), 1);
             mbar_init(bar(B_Q + t), kScaledQ ? 4 : 1);
+            mbar_init(bar(B_QRAW + t), 1);
         }
         for (int s = 0; s < L::slots; ++s) {
             mbar_init(bar(B_FULL + s), !L::gather ? 1 : (L::f8 && p.box >= kMinBox8 ? kMovers / 64 : kMovers / 32));
@@ -792,20 +794,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 if (n == 0) continue;
                 // the item's Q, as soon as the item before has been multiplied
                 auto load_q = [&]() {
-                    if constexpr (!kScaledQ) {
-                        if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) return;
+                    if (items > 0) ok = mbar_wait(bar(B_Q_FREE), (items - 1) & 1, err, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) return;
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (it.n[t] == 0) continue;
-                            ++qs[t];
-                            if (lane != 0) continue;
-                            mbar_arrive_expect_tx(bar(B_Q + t), L::panels * p.TR * G * 128);
-                            for (int pn = 0; pn < L::panels; ++pn)
-                                tma_load_3d(sbase + L::q + t * L::tile + pn * L::panel, &mq, pn * 64, it.h * G,
-                                            it.q_row + it.tok0 + t * p.TR, bar(B_Q + t));
-                        }
+                    for (int t = 0; t < 2; ++t) {
+                        if (it.n[t] == 0) continue;
+                        ++qs[t];
+                        if (lane != 0) continue;
+                        const uint32_t to = bar((kScaledQ ? B_QRAW : B_Q) + t);
+                        mbar_arrive_expect_tx(to, L::panels * p.TR * G * 128);
+                        for (int pn = 0; pn < L::panels; ++pn)
+                            tma_load_3d(sbase + L::q + t * L::tile + pn * L::panel, &mq, pn * 64, it.h * G,
+                                        it.q_row + it.tok0 + t * p.TR, to);
                     }
                     ++items;
                 };
@@ -905,7 +906,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             if (!ok && lane == 0) {
                 // a wait gave up: let the copies in flight land (bounded) before leaving
                 for (int t = 0; t < 2; ++t)
-                    if (qs[t] > 0) mbar_wait(bar(B_Q + t), (qs[t] - 1) & 1, nullptr, nullptr, 100000000ull);
+                    if (qs[t] > 0) mbar_wait(bar((kScaledQ ? B_QRAW : B_Q) + t), (qs[t] - 1) & 1, nullptr, nullptr, 100000000ull);
                 constexpr int kDepth = L::gather ? 2 : L::slots;
                 for (int x = max(0, loads - kDepth); x < loads; ++x)
                     mbar_wait(bar((L::gather ? B_STAGE : B_FULL) + x % kDepth), (x / kDepth) & 1, nullptr, nullptr, 100000000ull);
@@ -1015,7 +1016,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int t = warp >> 2;
         const int r = tid & 127;                            // row of the tile = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + t * kTileCols;
-        int steps = 0, outs = 0;                            // barrier phases of this tile so far
+        int steps = 0, outs = 0, raws = 0;                  // barrier phases of this tile so far
         int base = 0;                                       // ring index of the item's first tile
         Item it;
         bool ok = true;
@@ -1046,35 +1047,40 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
             float rs = a.scale_log2;
             if constexpr (kScaledQ) {
-                // This thread's row of q as fp16, scaled by 2^-e.  (The last
-                // Q.K^T that read the tile was done before the S of the item
-                // before was there.)
+                // This thread's row of q as fp16, scaled by 2^-e, where TMA put it.  (Read
+                // from memory by the threads, 32 lines a load, it took 4,000 cycles longer.)
                 if (n > 0) {
-                    uint32_t w[D / 2];
-                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                                      (int64_t)(it.q_row + tok) * a.q_stride + head * D);
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        reinterpret_cast<uint4*>(w)[c] = valid ? src[c] : make_uint4(0, 0, 0, 0);
+                    ok = mbar_wait(bar(B_QRAW + t), raws & 1, err, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    ++raws;
+                    uint4* const row = reinterpret_cast<uint4*>(smem + L::q + t * L::tile + r * 128);
+                    auto piece = [&](int c) -> uint4& { return row[(c >> 3) * (L::panel / 16) + ((c & 7) ^ (r & 7))]; };
                     float top = 0.f;
+#pragma unroll 4
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 x = piece(c);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int c = 0; c < D / 2; ++c) {
-                        const float2 f = BF16::unpack2(w[c]);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = BF16::unpack2(w[i]);
+                            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
                     }
                     const int e8 = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
                     const int e = (top == 0.f || e8 > 127) ? 0 : max(e8 - 14, -120);
                     const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-                    for (int c = 0; c < D / 2; ++c) {
-                        const float2 y = BF16::unpack2(w[c]);
-                        w[c] = F16::pack2(y.x * f, y.y * f);
+                    auto scaled = [&](uint32_t w) {
+                        const float2 y = BF16::unpack2(w);
+                        return F16::pack2(y.x * f, y.y * f);
+                    };
+#pragma unroll 4
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 x = piece(c);
+                        piece(c) = make_uint4(scaled(x.x), scaled(x.y), scaled(x.z), scaled(x.w));
                     }
-                    unsigned char* to = smem + L::q + t * L::tile + r * 128;
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        *reinterpret_cast<uint4*>(to + (c >> 3) * L::panel + (((c & 7) ^ (r & 7)) << 4)) =
-                            reinterpret_cast<const uint4*>(w)[c];
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_Q + t));
@@ -1666,6 +1672,8 @@ cudaError_t launch_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaStream
     // E4M3 pages (320 / 448 / 640) 336 / 334 / 341 us, through a window 173 / 166 / 170.
     // A step of 128 keys takes about 2,700 cycles (64-dim 2,400, 8-bit 3,300).
     p.charge = a.kv.f8 || a.kv.D == 128 ? 448 : 320;
+    // (an item behind a prefix reads that one's sums, too, and is mostly short)
+    if (PARTS && a.parts.phase == PHASE_OWN) p.charge = 1152;
     p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.ws_o = static_cast<float*>(a.ws);
     p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;
