@@ -16,9 +16,9 @@
 // attn_tc_merge joins in order of their keys.
 //
 // Warp roles, 384 threads (512 with movers):
-//   - softmax warpgroups 0, 1: tile t, thread = row = TMEM lane.  Read the
-//     128 scores of a step, mask them (only where a row's limit or a missing
-//     page falls into the step), update m (O is rescaled only when m grows by
+//   - softmax warpgroups 0, 1: tile t, thread = row = TMEM lane.  Mask the 128
+//     scores of a step in TMEM (only where a row's limit or a missing page falls
+//     into the step), read them, update m (O is rescaled only when m grows by
 //     more than 2^8), write P = exp2(s - m) rounded to 16 bits over S.  At the
 //     end divide and store.
 //   - MMA thread: S_t = Q_t K^T into TMEM, O_t += P_t V with P from TMEM and
@@ -51,21 +51,29 @@
 // Bound: the way from one barrier to the next.  S, softmax, P and P.V of a step
 // follow one another; two tiles of a CTA hide the one behind the other, and
 // still nothing is busy throughout (tensor pipe, issue slots, exponentials' unit:
-// long prompt 72%, 41%, 36%; chunks over 16-bit pages 60%, 40%, 30%, over E4M3
-// 48%, 44%, 24%, whose conversion takes slots; short prompts 12%, 23%, 13%).  208
-// registers a softmax thread hold a row's 128 scores, so that S is read from
-// TMEM once.  Measured: one causal prompt of 16,384 tokens, 32/8 heads of 128,
+// long prompt 72%, 41%, 36%; chunks over 16-bit pages 60%, 40%, 30%; chunks over
+// E4M3 through a window 38%, 40%, 19%).  Next to that the code itself: where a
+// step's is fetched anew the warps stand still.  So masks and the epilogue are
+// loops, and where the movers take registers the softmax is one, too, over 32 scores
+// at a time, read twice from TMEM (chunks over E4M3 384 -> 352 us; in the other
+// kernels 208 registers a thread hold a row's 128 scores, read once, which is 2 to 6%
+// faster there).  Measured: one causal prompt of 16,384 tokens, 32/8 heads of 128,
 // 1.38 to 1.53 ms, 1.43 to 1.59 PFLOP/s (0.85 to 0.94 of a sustained library
 // product's rate); chunks of 200 to 1,024 tokens over up to 8,192 keys in
-// 32-token pages 200 to 214 us, 1.17 to 1.25 PFLOP/s; over E4M3 pages 386 to 417
-// us, 1.01 to 1.09 PFLOP/s; 40 prompts of up to 700 tokens, 12/4 heads of 64, 31 us.
+// 32-token pages 204 to 216 us, 1.16 to 1.23 PFLOP/s; over E4M3 pages 334 to 350
+// us, 1.20 to 1.26 PFLOP/s; 40 prompts of up to 700 tokens, 12/4 heads of 64, 29 us.
 //
 // PARTS (a template parameter): a row sees parts of the keys only (KeyParts).  An
 // item then goes through the first keys, as many as there are sinks, rounded up to
 // whole boxes (TcParams::head of them), and behind them at once through those from
 // its lowest row's first key on, rounded down to a box's: what is left out between
 // the two is Item::shift keys, and key u of its way is key u or u + shift.  Keys on the
-// way that no row of the item sees are cleared like those behind kv_len.
+// way that no row of the item sees are cleared like those behind kv_len.  Measured:
+// 16,384 tokens through a window of 4,096 675 to 690 us (1.28 us a step, 0.71 to 0.73
+// of the burst rate); chunks over E4M3 pages through 2,000 keys 165 us (1.9 us a
+// step, 4.5 an item); 24 prompts of up to 2,500 tokens through 333 keys 49 us (with the
+// sinks in a step of their own and steps at multiples of 128 57); 64 requests' rows
+// over a shared prefix of 16,384 tokens 21 us.
 #pragma once
 
 #include <type_traits>
