@@ -130,6 +130,26 @@ def test_table_much_wider_than_the_sequences(shape, page, cache, dtype):
         assert torch.equal(out, again) and torch.equal(lse, lse2)      # nothing depends on timing
 
 
+@pytest.mark.parametrize("cache,dtype,dim", [("same", "bf16", 128), ("same", "f16", 64), ("e4m3", "bf16", 64), ("e5m2", "f16", 128)])
+@pytest.mark.parametrize("q_lens,own,heads,kv_heads,groups", [
+    ([1, 1, 1], [700, 3, 40], 8, 2, [(3, 6000)]),                   # few rows, either pass cut into many parts
+    ([2, 1, 3], [2, 2500, 9], 5, 5, [(2, 9000), (1, 70)]),
+    ([170] * 8, [170 + 9 * b for b in range(8)], 32, 8, [(8, 1500)]),  # more items than ranges
+    ([900, 450], [900, 1450], 16, 4, [(2, 700)]),
+    ([3, 9], [40, 30], 160, 1, [(2, 300)]),                         # a group of 160 heads
+    ([1] * 70, [1 + 5 * b % 37 for b in range(70)], 4, 1, [(1, 40 + b) for b in range(66)]),  # many groups of one
+])
+def test_passes_of_any_size(q_lens, own, heads, kv_heads, groups, cache, dtype, dim):
+    c = Shared(500, q_lens, own, heads, kv_heads, dim, 16, dtype, cache, groups=groups, before=1, behind=1).poison()
+    narrow = c.table
+    for wide in (False, True):
+        if wide:
+            c.table = torch.cat([narrow, torch.full((len(q_lens), 1 << 16), -1, dtype=torch.int32)], 1)
+        for hint in (max(q_lens), 0):
+            out, lse = run_shared(c, True, hint)
+            check_shared(c, out, lse, True)
+
+
 @pytest.mark.parametrize("cache,dtype", [("same", "bf16"), ("e4m3", "bf16")])
 @pytest.mark.parametrize("q_len,hint", [(1, 1), (21, 0)])
 def test_equals_attention_over_own_pages(q_len, hint, cache, dtype):
