@@ -261,10 +261,17 @@ __device__ __forceinline__ int64_t cost_before(const TcParams& p, const Seq& s, 
     return sum;
 }
 
-// Steps of an item of N steps before point x of its length c.
-__device__ __forceinline__ int cut(int64_t x, int c, int N) {
-    if (x <= 0) return 0;
+// Steps of an item of N steps before point x of its length c.  PARTS: the charge lies
+// at the item's beginning, so that a range which begins a second item gets fewer
+// steps (else it is spread over the item).
+template <bool PARTS>
+__device__ __forceinline__ int cut(const TcParams& p, int64_t x, int c, int N) {
+    if constexpr (PARTS) {
+        x -= p.charge;
+        c -= p.charge;
+    }
     if (x >= c) return N;
+    if (x <= 0) return 0;
     // (fp32: monotonic in x, and the same wherever a border is looked at)
     const int st = (int)__fdividef(__ll2float_rn(x) * (float)N, (float)c);
     return st < kMinShare ? 0 : (st > N - kMinShare ? N : st);
@@ -400,7 +407,7 @@ struct Walk {
             const int64_t x0 = x, x1 = min((int64_t)c, x + left);
             const int lo = PARTS ? lowest(p, s, j * U) : 0;
             const int v1 = visible(p, s, (j + 1) * U), N = steps_to<PARTS>(p, v1, lo);
-            const int s0 = cut(x0, c, N), s1 = cut(x1, c, N);
+            const int s0 = cut<PARTS>(p, x0, c, N), s1 = cut<PARTS>(p, x1, c, N);
             if constexpr (PARTS) {
                 it.shift = left_out(p, lo);
                 it.first = s.first;
@@ -1410,7 +1417,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) attn_tc_merge(const TcParams
         float4 v[kBatch][Q];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int end = last < N ? cut(it.x + (i + j) * it.per, it.c, N) : last;
+            const int end = last < N ? cut<PARTS>(p, it.x + (i + j) * it.per, it.c, N) : last;
             const bool some = valid && end != last;      // (two borders can move to the same step)
             last = end;
             const int64_t slot = i + j == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i + j);
@@ -1530,7 +1537,7 @@ __global__ void __launch_bounds__(kMergeThreads, kPrefixBlocks) attn_tc_merge_pr
             float4 v[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int end = last < N ? cut(it.x + (i + j) * it.per, it.c, N) : last;
+                const int end = last < N ? cut<true>(p, it.x + (i + j) * it.per, it.c, N) : last;
                 const bool some = end != last;
                 last = end;
                 const int64_t slot = i + j == 0 ? 2 * x + 1 : 2 * (x + i + j);
@@ -1681,7 +1688,7 @@ cudaError_t launch_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaStream
     // A step of 128 keys takes about 2,700 cycles (64-dim 2,400, 8-bit 3,300).
     p.charge = a.kv.f8 || a.kv.D == 128 ? 448 : 320;
     // (an item behind a prefix reads that one's sums, too, and is mostly short)
-    if (PARTS && a.parts.phase == PHASE_OWN) p.charge = 1152;
+    if (PARTS && a.parts.phase == PHASE_OWN) p.charge = 900;
     p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.ws_o = static_cast<float*>(a.ws);
     p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;

@@ -115,7 +115,7 @@ def test_shared_prefix(shape, cache, layout, dtype):
 
 
 @pytest.mark.parametrize("cache,dtype,page", [("same", "bf16", 16), ("same", "f16", 20), ("e4m3", "f16", 64), ("e5m2", "bf16", 12)])
-@pytest.mark.parametrize("shape", [0, 1, 2, 4, 5, 6, 7])
+@pytest.mark.parametrize("shape", [0, 1, 2, 4, 5, 6, 7, 8, 9])
 def test_table_much_wider_than_the_sequences(shape, page, cache, dtype):
     """By what the table could hold there is much to share: a pass over the prefixes and
     one over the own tokens, on either kernel, the large tiles wherever there are more
