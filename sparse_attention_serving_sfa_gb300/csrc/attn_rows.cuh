@@ -307,13 +307,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
     volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + C::masks) + warp * NS;
     float* ml = reinterpret_cast<float*>(smem + C::ml);
     const uint64_t policy = PARTS ? l2_policy(p.parts.once) : 0;
-    grid_dependency_wait();
+    // The pass over the own tokens starts while the prefixes' sums are joined: what it
+    // reads until it writes is older than the prefixes' kernel, which waited for it
+    // before the join could start.  (It waits below, in every block: this grid must not
+    // be over before the join.)
+    const bool late = PARTS && p.parts.phase == PHASE_OWN;
+    if (!late) grid_dependency_wait();
     grid_launch_dependents();
 
     const Line line = line_at<PARTS>(p, C::chunk, ctas_mul, 0);
     int64_t u = line.at;
     const int64_t u_end = min(line.total, u + line.per);
-    if (u >= u_end) return;
+    if (u >= u_end) {
+        if (late) grid_dependency_wait();
+        return;
+    }
     int b = line.b;
     int64_t seq_start = line.start;
     Seq sq = line.seq;
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
         const int64_t seq_units = (int64_t)sq.tiles * (sq.chunks + kCharge) * p.kv.Hkv;
         if (u >= seq_start + seq_units) {
             seq_start += seq_units;
-            if (++b >= line_seqs<PARTS>(p)) return;
+            if (++b >= line_seqs<PARTS>(p)) break;
             sq = seq_of<PARTS>(p, b, C::chunk);
             continue;
         }
@@ -679,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
             mw[2 * (g + 8) + 1] = l1;
         }
         __syncthreads();
+        if (late) grid_dependency_wait();          // the prefixes' sums, and their parts' memory
         const int r = tid >> 3;
         if (r < rows_here) {
             // dims 32 i + d0 .. + 3: the eight threads of a row read side by side
@@ -735,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const SeqAttn p,
         }
         __syncthreads();       // the rings are free for the next tile
     }
+    if (late) grid_dependency_wait();
 }
 
 // Block x joins the parts of the tile that border x (between the ranges of
@@ -744,6 +754,7 @@ template <class E, int D, int F8, bool PARTS>
 __global__ void __launch_bounds__(32 * kRows, 1) attn_rows_merge(const SeqAttn p, uint64_t ctas_mul) {
     constexpr int chunk = RowsCfg<D, F8>::chunk;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (PARTS && p.parts.phase == PHASE_PREFIX) grid_launch_dependents();      // (the pass over the own tokens)
     // The lists are older than the main kernel, which waited for them before
     // this one could start; its parts are not.  (Every block waits, also those
     // with nothing to do: this grid must not be over before the main one.)

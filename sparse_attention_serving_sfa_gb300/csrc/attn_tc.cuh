@@ -1400,6 +1400,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) attn_tc_merge(const TcParams
     const SeqAttn& a = p.a;
     const float kPShift = std::is_same<E, BF16>::value && a.kv.f8 == 0 ? 0.f : 7.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (PARTS && a.parts.phase == PHASE_PREFIX) grid_launch_dependents();      // (the pass over the own tokens)
     grid_dependency_wait();
     const CutItem it = p.ws_cut[blockIdx.x];
     const int N = it.N, h = it.h;
@@ -1508,6 +1509,7 @@ __global__ void __launch_bounds__(kMergeThreads, kPrefixBlocks) attn_tc_merge_pr
     static_assert(kMaxCtas <= kMergeThreads, "a thread a range");
     const SeqAttn& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_launch_dependents();        // (the pass over the own tokens)
     grid_dependency_wait();
     const bool cuts = tid < ranges && p.ws_cut[tid].N > 0;
     const unsigned which = __ballot_sync(0xffffffffu, cuts);
