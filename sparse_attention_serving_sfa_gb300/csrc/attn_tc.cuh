@@ -69,9 +69,9 @@
 // its lowest row's first key on, rounded down to a box's: what is left out between
 // the two is Item::shift keys, and key u of its way is key u or u + shift.  Keys on the
 // way that no row of the item sees are cleared like those behind kv_len.  Measured:
-// 16,384 tokens through a window of 4,096 675 to 690 us (1.28 us a step, 0.71 to 0.73
+// 16,384 tokens through a window of 4,096 670 to 690 us (1.28 us a step, 0.71 to 0.73
 // of the burst rate); chunks over E4M3 pages through 2,000 keys 165 us (1.9 us a
-// step, 4.5 an item); 24 prompts of up to 2,500 tokens through 333 keys 49 us (with the
+// step, 4.5 an item); 24 prompts of up to 2,500 tokens through 333 keys 48 us (with the
 // sinks in a step of their own and steps at multiples of 128 57); 64 requests' rows
 // over a shared prefix of 16,384 tokens 21 us.
 #pragma once
