@@ -373,6 +373,13 @@ struct Item {
 };
 static_assert(sizeof(Item) == 64, "TcSmem::items");
 
+// The pass over the own tokens starts while the prefixes' sums are joined, and waits
+// for that where it writes (their lists of cuts, their parts' memory) or reads those
+// sums.  What it reads before is older than the prefixes' kernel, which waited for it
+// before the join could start.
+template <bool PARTS>
+__device__ __forceinline__ bool starts_early(const TcParams& p) { return PARTS && p.a.parts.phase == PHASE_OWN; }
+
 // Walks the shares of this CTA's range: the producer does, and hands each item
 // to the MMA thread and the softmax through two slots in shared memory.
 template <bool PARTS>
@@ -380,9 +387,11 @@ struct Walk {
     int64_t left, per;          // of the range: what is left, its length
     int64_t x;                  // point within the item (j, h)
     int b, j, h;
+    bool cuts;                  // an item was written down
     Seq s;
 
     __device__ __forceinline__ void begin(const TcParams& p, const Line& l) {
+        cuts = false;
         left = x = 0;
         per = l.per;
         b = l.b;
@@ -426,8 +435,11 @@ struct Walk {
             const int v0 = two ? visible(p, s, it.tok0 + p.TR) : v1;
             it.n[0] = max(0, min(steps_to<PARTS>(p, v0, lo), s1) - s0);
             it.n[1] = two ? s1 - s0 : 0;
-            if (s0 == 0 && s1 > 0 && s1 < N && (threadIdx.x & 31) == 0)
-                p.ws_cut[blockIdx.x] = CutItem{N, c, h, s.q_row, s.n_q, j * U, s.first, x1, per};
+            if (s0 == 0 && s1 > 0 && s1 < N) {
+                cuts = true;
+                if constexpr (PARTS) grid_dependency_wait();
+                if ((threadIdx.x & 31) == 0) p.ws_cut[blockIdx.x] = CutItem{N, c, h, s.q_row, s.n_q, j * U, s.first, x1, per};
+            }
             left -= x1 - x0;
             x = x1;
             if (x1 == c) {
@@ -774,16 +786,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             tma_prefetch_map(&mk);
             tma_prefetch_map(&mv);
         }
-        grid_dependency_wait();
+        if (!starts_early<PARTS>(p)) grid_dependency_wait();
         walk.begin(p, line_at<PARTS>(p));
-        if (lane == 0) p.ws_cut[blockIdx.x].N = 0;
+        if (!PARTS && lane == 0) p.ws_cut[blockIdx.x].N = 0;
         more = walk.next(p, next_item);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::tmem_slot);
-    grid_dependency_wait();
+    if (!starts_early<PARTS>(p)) grid_dependency_wait();
     grid_launch_dependents();
 
     if (warp >= kSoftWarps) {
@@ -917,6 +929,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     }
                 }
                 if (!ok) break;
+            }
+            if (PARTS && !walk.cuts) {
+                grid_dependency_wait();
+                if (lane == 0) p.ws_cut[blockIdx.x].N = 0;
             }
             if (!ok && lane == 0) {
                 // a wait gave up: let the copies in flight land (bounded) before leaving
@@ -1300,6 +1316,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
             base += 2 * n_all;
             const int64_t row = (int64_t)(it.q_row + tok) * a.Hq + head;
+            if constexpr (PARTS) grid_dependency_wait();           // (see starts_early; else it is over)
             // PARTS: whole items of a prefix leave their sums, those behind one are joined with them
             const bool to_px = PARTS && a.parts.phase == PHASE_PREFIX, with_px = PARTS && it.first > 0 && valid && it.whole;
             float* const px = PARTS ? a.parts.px_o + row * D : nullptr;
@@ -1375,6 +1392,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
         }
     }
+    if constexpr (PARTS) grid_dependency_wait();       // (in every block: this grid must not be over before the join)
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
