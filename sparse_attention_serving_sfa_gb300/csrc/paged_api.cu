@@ -207,11 +207,11 @@ sfa_status run_attention(SeqAttn& p, const Call& c, int window, int sinks) {
 // Where every sequence reading the shared keys for itself moves no more than this (by
 // what the table can hold, and few rows each), one pass over all keys is faster than
 // two passes and their joins.  Two passes and one, us: 8 sequences behind 500 keys (20
-// MB) 16.5 and 9.9, behind 2,000 (66 MB) 20.6 and 14.4, behind 8,000 (254 MB) 27.8 and
-// 35.7; 16 behind 2,000 (133 MB) 22.1 and 21.5; 32 behind 2,000 (266 MB) 27.1 and
-// 36.4; E4M3, 16 behind 4,000 (129 MB) 28.8 and 27.7, 32 behind 4,000 (258 MB) 37.4
-// and 46.6; 2 kv heads, 8 behind 4,000 (32 MB) 21.6 and 11.7.
-constexpr int64_t kDirectBytes = 128 << 20;
+// MB) 15.1 and 9.8, behind 2,000 (66 MB) 17.0 and 14.4, behind 8,000 (254 MB) 22.8 and
+// 35.7; 16 behind 2,000 (133 MB) 19.4 and 21.5; 32 behind 500 (80 MB) 18.9 and 17.8,
+// behind 2,000 (266 MB) 24.7 and 36.4; E4M3, 8 behind 8,000 (127 MB) 26.4 and 27.3, 32
+// behind 1,000 (71 MB) 23.0 and 21.5; 2 kv heads, 8 behind 4,000 (32 MB) 17.8 and 11.8.
+constexpr int64_t kDirectBytes = 96 << 20;
 int64_t direct_bytes(const SeqAttn& p) {
     return p.kv.num_seqs * most_keys(p.kv) * p.kv.Hkv * p.kv.D * (p.kv.f8 ? 2 : 4);
 }
