@@ -565,8 +565,9 @@ sfa_status paged_append(const paged_kv* cache, const void* k_new, const void* v_
  *     (x, y) -> (x cos(angle) - y sin(angle), x sin(angle) + y cos(angle)),
  * in q and k; their other elements and v move as they are.
  *   q, q_out      device packed rows of num_qo_heads heads, `dtype`, each with its
- *                 stride; q_out may be q itself (same stride).  q NULL: keys and
- *                 values alone.  Rows of no sequence are left alone.
+ *                 stride; q_out is q itself (same stride) or shares no element with
+ *                 q; nor does it with k_new or v_new.  q NULL: keys and values alone.
+ *                 Rows of no sequence are left alone.
  *   inv_freq      device float32 [rotary_dim / 2], finite.
  *   rotary_dim    even, at most head_dim; a multiple of 16 in this build.
  *   interleaved   0: pair i is elements (i, i + rotary_dim / 2);
@@ -576,7 +577,8 @@ sfa_status paged_append(const paged_kv* cache, const void* k_new, const void* v_
  * cache to the code nearest to its quotient by the head's scale (next to a border
  * between two codes the rotation is computed in 64 bits).  A query whose position is
  * negative is rotated by it, its key is not written.
- * Errors: as paged_append; SFA_ERR_UNSUPPORTED for another even rotary_dim.
+ * Errors: as paged_append; SFA_ERR_UNSUPPORTED for another even rotary_dim,
+ * SFA_ERR_INVALID_ARG for rows of q_out over rows that are read.
  */
 sfa_status paged_append_rotated(const paged_kv* cache, const void* q, const void* k_new,
                                 const void* v_new, void* q_out, int64_t q_stride, int64_t k_stride,

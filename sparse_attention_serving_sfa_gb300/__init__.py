@@ -561,7 +561,8 @@ def paged_append_rotated(k_new, v_new, cu_seqlens, k_pages, v_pages, page_table,
     their positions on the way, pair i of a head by position * inv_freq[i]
     (float32, rotary_dim / 2 of them; pairs are halves apart, or neighbours with
     interleaved).  q (tokens, qo heads, head_dim): the same rows' queries, rotated
-    into q_out (q itself, say; a new tensor unless given), which is returned."""
+    into q_out (q itself, or memory of its own; a new tensor unless given), which is
+    returned."""
     st, q_out = (_tensors or _native()).paged_append_rotated(
         k_new, v_new, cu_seqlens, k_pages, v_pages, page_table, kv_lens, _enum(kv_layout, KV_LAYOUTS),
         scale_k, scale_v, inv_freq, q, interleaved, q_out, _stream(stream))

@@ -62,6 +62,35 @@ bool bad_stride(int64_t stride, int heads, int D) {
     return stride < (int64_t)heads * D || stride % 8 != 0 || stride > (int64_t)1 << 38;
 }
 
+// Rows of one call, `width` elements of 16 bits each.
+struct Rows {
+    const void* at;
+    int64_t stride;
+    int64_t width;
+};
+
+// Whether `n` rows of x and of y have an element in common.
+bool rows_meet(Rows x, Rows y, int64_t n) {
+    // y's first element counted from x's (both begin at 16 bytes)
+    const int64_t d = (int64_t)(reinterpret_cast<intptr_t>(y.at) - reinterpret_cast<intptr_t>(x.at)) / 2;
+    if (d >= (n - 1) * x.stride + x.width || -d >= (n - 1) * y.stride + y.width) return false;
+    if (x.stride == y.stride) {
+        // row j of y lies d + (j - i) stride behind row i of x: a row or two nearest to it
+        for (int64_t t = -d / x.stride - 1; t <= -d / x.stride + 1; ++t) {
+            const int64_t off = d + t * x.stride;
+            if (t > -n && t < n && off < x.width && -off < y.width) return true;
+        }
+        return false;
+    }
+    for (int64_t i = 0; i < n; ++i) {
+        // the first row of y that ends behind the beginning of row i of x
+        const int64_t from = i * x.stride - d;               // counted from y's first element
+        const int64_t j = from < y.width ? 0 : (from - y.width) / y.stride + 1;
+        if (j < n && j * y.stride < from + x.width) return true;
+    }
+    return false;
+}
+
 // 16-row tiles read the keys at HBM's pace and begin early; the 128-row
 // tensor-core tiles stand mostly empty with few rows, but more rows cost them
 // nothing.  So 16-row tiles take (times: 16-row tiles, 128-row tiles; head_dim
@@ -265,6 +294,14 @@ sfa_status paged_append_rotated(const paged_kv* cache, const void* q, const void
     if (num_tokens == 0) return SFA_OK;
     if (!k_new || !v_new || !al(k_new, 16) || !al(v_new, 16)) return SFA_ERR_INVALID_ARG;
     if (q && (!q_out || !al(q, 16) || !al(q_out, 16))) return SFA_ERR_INVALID_ARG;
+    if (q) {
+        // in place, or over no row that is still to be read
+        const Rows to{q_out, q_out_stride, (int64_t)num_qo_heads * p.kv.D}, from{q, q_stride, to.width};
+        const Rows k{k_new, k_stride, (int64_t)p.kv.Hkv * p.kv.D}, v{v_new, v_stride, k.width};
+        const bool in_place = q_out == q && (q_out_stride == q_stride || num_tokens == 1);
+        if ((!in_place && rows_meet(to, from, num_tokens)) || rows_meet(to, k, num_tokens) || rows_meet(to, v, num_tokens))
+            return SFA_ERR_INVALID_ARG;
+    }
     p.q = q; p.k = k_new; p.v = v_new; p.q_out = q_out;
     p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride; p.q_out_stride = q_out_stride;
     p.cu = cu_seqlens;
