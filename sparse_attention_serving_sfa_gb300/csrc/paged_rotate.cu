@@ -49,11 +49,14 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
 // The code nearest to the exact quotient y / scale.  A float near it decides, unless
 // it lies within 8 units in the last place of a border between codes (which has zeros
 // behind its fourth fraction bit): then the border times the scale, exact in 64 bits,
-// does.
+// does.  (Three roundings make the float, of y, the reciprocal and their product; where
+// one could be out of the normal numbers it is the 64-bit quotient rounded.)
 template <bool E5>
 __device__ __forceinline__ uint32_t nearest_code(double y, float scale) {
-    float q = (float)y * __frcp_rn(scale);
-    if (!(fabsf(q) >= 1e-30f && fabsf(q) < 1e30f)) q = __fdiv_rn((float)y, scale);     // (a reciprocal out of the normal range)
+    const float f = (float)y;
+    float q = f * __frcp_rn(scale);
+    auto middling = [](float v) { return fabsf(v) >= 1e-30f && fabsf(v) < 1e30f; };
+    if (!(middling(f) && middling(q))) q = (float)(y / (double)scale);
     const uint32_t bits = __float_as_uint(q), border = (bits + 0x40000u) & ~0x7ffffu;
     if (bits - border + 8u <= 16u) {
         const double d = fabs(y) - (double)fabsf(__uint_as_float(border)) * (double)scale;
@@ -189,7 +192,9 @@ __global__ void __launch_bounds__(kThreads, 3) paged_rotate_kernel(const RotateA
             if (turns) {
                 // The codes, if they are the same 2^-22 of the sum of the pair's magnitudes to
                 // either side (six times what the rotation and the reciprocal are off by in the
-                // mean).  So it mostly is; the other pairs' are found in 64 bits.
+                // mean).  So it mostly is; the other pairs' are found in 64 bits, and so is
+                // every pair whose scale is beyond 2^100 or below 2^-100: there the rotation
+                // could leave the normal numbers and its error that margin.
                 auto codes = [&](const float (&v)[8], uint4 raw, uint4 other, uint2& differ) {
                     float m[8], lo[8], hi[8];
                     unpack8<E>(raw, m);
@@ -203,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, 3) paged_rotate_kernel(const RotateA
                         hi[j] = v[j] * inv + e;
                     }
                     const uint2 c = codes8<F8 == 2>(lo), o = codes8<F8 == 2>(hi);
-                    const bool normal = inv >= 1.1754944e-38f && inv < INFINITY;
-                    differ = normal ? make_uint2(c.x ^ o.x, c.y ^ o.y) : make_uint2(~0u, ~0u);
+                    const bool middling = inv >= 7.8886091e-31f && inv <= 1.2676506e30f;
+                    differ = middling ? make_uint2(c.x ^ o.x, c.y ^ o.y) : make_uint2(~0u, ~0u);
                     return c;
                 };
                 uint2 da, db;
