@@ -53,7 +53,10 @@ __device__ __forceinline__ int64_t place_of(const SeqKV& kv, const int32_t* cu, 
 __device__ __forceinline__ float quotient(float x, float s) {
     float q = __fdiv_rn(x, s);
     if ((__float_as_uint(q) & 0x7ffffu) == 0u) {
-        const float r = fmaf(-q, s, x);      // exact; its sign is the true quotient's side (s > 0)
+        // Exact; its sign is the true quotient's side (s > 0).  (Of a small scale and its value
+        // both times 2^64, that the remainder is not below the smallest number.)
+        const float up = s < 5.4210109e-20f ? 18446744073709551616.f : 1.f;
+        const float r = fmaf(-q, s * up, x * up);
         if (r != 0.f && q != 0.f && isfinite(q))
             q = __uint_as_float(__float_as_uint(q) + (((r > 0.f) == (q > 0.f)) ? 1u : ~0u));
     }

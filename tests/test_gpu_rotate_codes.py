@@ -188,3 +188,40 @@ def test_ties(dtype, kind, interleaved):
     want = P.nearest_code(q, kind)
     assert torch.equal(got[off == 0], want[off == 0])
     check(got, q, off, kind)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("rotated", [False, True])
+def test_subnormal_values_and_scales(kind, rotated):
+    """Values as they are: every subnormal bf16 number over subnormal scales whose quotient
+    rounded to fp32 is a border that the exact one only nearly is, the difference being below
+    the smallest fp32 number."""
+    grid = P.code_values(kind)
+    borders = (grid[1:] + grid[:-1]) / 2
+    m = torch.arange(128, dtype=torch.float64)
+    x = m * 2.0 ** -133
+    # scales: the multiples of 2^-149 around the exact x / border, where that is subnormal
+    at = (x[1:, None] / borders).flatten()
+    s = torch.cat([torch.floor(at * 2.0 ** 149), torch.ceil(at * 2.0 ** 149)]).unique()
+    s = s[(s >= 1) & (s < 2 ** 23)] * 2.0 ** -149
+    q = x / s[:, None]                                       # off by 2^-53 of itself; borders by 2^-33 or more, or met
+    rounded = torch.isin(q.float().double(), borders) & ~torch.isin(q, borders)
+    s = s[rounded.sum(1).topk(64).indices]
+    q, rounded = x / s[:, None], (x / s[:, None]).float().double()
+    want = P.nearest_code(q, kind)
+    # what makes this a test: the quotient in fp32 gives other codes
+    assert (P.nearest_code(rounded, kind) != want).sum() >= 64
+    k = x.to(torch.bfloat16).expand(64, 128).contiguous()
+    assert torch.equal(k.double(), x.expand(64, 128))
+    new = torch.stack((k, -k)).cuda()                        # two tokens of 64 heads
+    pools = [torch.zeros(1, 16, 64, 128, dtype=P.TORCH[kind], device="cuda") for _ in "kv"]
+    lists = [torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 2], [[0]], [2])]
+    scale = s.float().cuda()
+    if rotated:
+        sfa.paged_append_rotated(new, new, lists[0], *pools, *lists[1:], frequencies(64).cuda(), scale_k=scale, scale_v=scale)
+    else:
+        sfa.paged_append(new, new, lists[0], *pools, *lists[1:], scale_k=scale, scale_v=scale)
+    for pool, first in ((pools[0], 64 if rotated else 0), (pools[1], 0)):        # (what does not turn)
+        got = raw(pool)[0, :2]
+        assert torch.equal(got[0, :, max(first, 1):], want[:, max(first, 1):])
+        assert torch.equal(got[1, :, max(first, 1):], want[:, max(first, 1):] + 128)
