@@ -190,11 +190,14 @@ __global__ void __launch_bounds__(kThreads, 3) paged_rotate_kernel(const RotateA
             uint8_t* dst = static_cast<uint8_t*>(const_cast<void*>(is_v ? kv.v : kv.k)) + at;
             uint2 ca, cb;
             if (turns) {
-                // The codes, if they are the same 2^-22 of the sum of the pair's magnitudes to
-                // either side (six times what the rotation and the reciprocal are off by in the
-                // mean).  So it mostly is; the other pairs' are found in 64 bits, and so is
-                // every pair whose scale is beyond 2^100 or below 2^-100: there the rotation
-                // could leave the normal numbers and its error that margin.
+                // The codes, if they are the same 5.25 2^-24 of the sum of the pair's magnitudes
+                // to either side.  That is a bound: in units of 2^-24 of an element's magnitude,
+                // at t within an eighth of a turn, the cosine is off by 1 and by 0.4 sin t for its
+                // angle's rounding (the sine by less than 1 and by 0.4 cos t), and the product
+                // rounded by itself, the sum, the reciprocal and the quotient add cos t (sin t)
+                // each; 5.02 at most, at t = 0.08.  So it mostly is; the other pairs' are found in
+                // 64 bits, and so is every pair whose scale is beyond 2^100 or below 2^-100: there
+                // the rotation could leave the normal numbers and its error that margin.
                 auto codes = [&](const float (&v)[8], uint4 raw, uint4 other, uint2& differ) {
                     float m[8], lo[8], hi[8];
                     unpack8<E>(raw, m);
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_rotate_kernel(const RotateA
                     for (int j = 0; j < 8; ++j) lo[j] = fabsf(m[j]) + fabsf(PAIRS ? m[j ^ 1] : hi[j]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float e = lo[j] * inv * 2.384185791015625e-07f;
+                        const float e = lo[j] * inv * 3.1292439e-07f;
                         lo[j] = v[j] * inv - e;
                         hi[j] = v[j] * inv + e;
                     }
