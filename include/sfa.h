@@ -568,15 +568,17 @@ sfa_status paged_append(const paged_kv* cache, const void* k_new, const void* v_
  *                 stride; q_out is q itself (same stride) or shares no element with
  *                 q; nor does it with k_new or v_new.  q NULL: keys and values alone.
  *                 Rows of no sequence are left alone.
- *   inv_freq      device float32 [rotary_dim / 2], finite.
+ *   inv_freq      device float32 [rotary_dim / 2], magnitudes up to 2^20 (at larger
+ *                 finite ones the angle is less exact, by their ratio to that).
  *   rotary_dim    even, at most head_dim; a multiple of 16 in this build.
  *   interleaved   0: pair i is elements (i, i + rotary_dim / 2);
  *                 else (2 i, 2 i + 1).
  * The angle is taken of the exact product, whatever the position (off by at most
  * 2^-22 of a radian); the rotation is fp32, rounded once: to `dtype`, or in an 8-bit
- * cache to the code nearest to its quotient by the head's scale (next to a border
- * between two codes the rotation is computed in 64 bits).  A query whose position is
- * negative is rotated by it, its key is not written.
+ * cache to the code nearest to its quotient by the head's scale.  Next to a border
+ * between two codes the rotation is computed in 64 bits: off by at most 2^-45 of
+ * |x| + |y| and, for frequencies up to 1, an angle of 2^-59 of a radian a position.  A
+ * query whose position is negative is rotated by it, its key is not written.
  * Errors: as paged_append; SFA_ERR_UNSUPPORTED for another even rotary_dim,
  * SFA_ERR_INVALID_ARG for rows of q_out over rows that are read.
  */

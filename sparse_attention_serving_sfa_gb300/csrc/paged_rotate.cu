@@ -9,7 +9,7 @@
 // interleaved; dims from r on, and values, move as they are.
 //
 // Angles are kept in turns, as 64-bit fractions: inv_freq / (2 pi) in units of
-// 2^-64 turns (to a few units), times pos, wraps by itself.  What is left within an
+// 2^-64 turns (turns_of), times pos, wraps by itself.  What is left within an
 // eighth of a turn goes to fp32 (2^-24 of itself) and sincospif, the quarters are put
 // back by swaps and signs: far positions cost no accuracy.
 //
@@ -35,8 +35,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 8;      // of a block
 
-// f / (2 pi) as a fraction of a turn in units of 2^-64 (whole turns drop out), to a
-// few units: 1 / (2 pi) as three floats, the first two products with their remainders.
+// f / (2 pi) as a fraction of a turn in units of 2^-64 (whole turns drop out), to 3
+// units (five roundings) and 1.6e-4 |f| of one: 1 / (2 pi) as three floats, the first
+// two products with their remainders, the third rounded.  So an angle is off by 2^-59
+// of a radian a position for frequencies up to 1, and by 2^-24 at any position (below
+// 2^30) for those up to 2^20.
 // (In fp64 arithmetic this took up to 58% of that pipe's time, and the kernel up to
 // 25% more.)
 __device__ __forceinline__ uint64_t turns_of(float f) {

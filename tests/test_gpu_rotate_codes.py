@@ -7,6 +7,7 @@ import torch
 
 import sparse_attention_serving_sfa_gb300 as sfa
 from tests import paged_testlib as P
+from tests import parts_testlib as X
 from tests.test_gpu_paged import raw
 
 pytestmark = pytest.mark.gpu
@@ -225,3 +226,24 @@ def test_subnormal_values_and_scales(kind, rotated):
         got = raw(pool)[0, :2]
         assert torch.equal(got[0, :, max(first, 1):], want[:, max(first, 1):])
         assert torch.equal(got[1, :, max(first, 1):], want[:, max(first, 1):] + 128)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_large_frequencies(interleaved):
+    """Angles of frequencies up to 2^20 at positions up to the last a table can have."""
+    page, T, R = 1 << 20, 3, 32
+    freq = torch.logspace(0, 20, R, base=2.0) * (torch.arange(R) % 3 - 1).sign().add(0.5).sign()
+    freq[-1], freq[-2] = 2.0 ** 20, -1e6
+    g = torch.Generator().manual_seed(8)
+    qk = torch.randn((T, 2, 2 * R), generator=g).half()
+    pools = [torch.zeros(1, page, 1, 2 * R, dtype=torch.float16, device="cuda") for _ in "kv"]
+    for last in (1023 * page, 700000001):
+        table = torch.full((1, 1023), 0, dtype=torch.int32)
+        lens, cu = torch.tensor([last], dtype=torch.int32), torch.tensor([0, T], dtype=torch.int32)
+        d = qk.cuda()
+        out = sfa.paged_append_rotated(d[:, 1:], d[:, 1:], cu.cuda(), *pools, table.cuda(), lens.cuda(), freq.cuda(), q=d[:, :1],
+                                       interleaved=interleaved)
+        pos = list(range(last - T, last))
+        X.check_rotated(out.cpu(), *X.rotated(qk[:, :1], pos, freq, interleaved), "f16")
+        got = pools[0].cpu()[0, [p % page for p in pos]]
+        X.check_rotated(got, *X.rotated(qk[:, 1:], pos, freq, interleaved), "f16")
