@@ -1631,11 +1631,6 @@ bool codes_map(CUtensorMap* m, const void* base, const SeqKV& kv, bool hnd, int 
               kv.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Items of a prefix's pass at most.
-int64_t prefix_items(const SeqAttn& a) {
-    return ((int64_t)a.tokens / (2 * (kTileM / a.G)) + a.parts.groups) * a.kv.Hkv;
-}
-
 template <class E, int D, int SRC, bool PARTS>
 cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStream_t stream) {
     using L = TcSmem<D, SRC>;
@@ -1668,7 +1663,7 @@ cudaError_t launch_tc_t(const TcParams& p, int64_t longest, int num_sms, cudaStr
     // items of fewer than 2 kMinShare steps are never cut
     if (longest >= 2 * kMinShare * kStep - kStep + 1) {
         // (a prefix's items at most; with fewer than ranges most are cut often)
-        const int64_t items = PARTS && a.parts.phase == PHASE_PREFIX ? prefix_items(a) : ctas;
+        const int64_t items = PARTS && a.parts.phase == PHASE_PREFIX ? tc_prefix_items(a) : ctas;
         if constexpr (PARTS) {
             if (items < ctas)
                 err = launch_pdl(attn_tc_merge_prefix<D>, dim3(kPrefixBlocks * ctas), dim3(kMergeThreads), 0, stream, p, ctas - 1);
@@ -1684,8 +1679,6 @@ template <bool PARTS>
 cudaError_t launch_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaStream_t stream) {
     TcParams p{};
     p.a = a;
-    // (a prefix of few items; with many its keys are read again and again)
-    p.a.parts.once = PARTS && a.parts.phase == PHASE_PREFIX && prefix_items(a) < num_sms;
     p.TR = kTileM / a.G;
     p.hnd = a.kv.s_tok == a.kv.D && a.kv.Hkv > 1 ? 1 : 0;
     p.box = kStep;

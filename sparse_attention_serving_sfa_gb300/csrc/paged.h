@@ -61,7 +61,8 @@ struct SeqKV {
 enum { PHASE_ALL = 0, PHASE_PREFIX = 1, PHASE_OWN = 2, PHASE_DIRECT = 3 };
 struct KeyParts {
     int phase;
-    int once;                    // the pass reads each key about once
+    int once;                    // loads of keys leave L2 first: the pass reads each about once (no
+                                 // matter where the tensor-core kernel gathers pages row by row)
     int window, sinks;           // at most 2^30; window 2^30: none
     const int32_t* cu_shared;    // [groups + 1]: group g is sequences cu_shared[g] .. cu_shared[g + 1] - 1
     const int32_t* shared_lens;  // [groups]
@@ -85,6 +86,11 @@ struct SeqAttn {
     int* err_word;
     KeyParts parts;
 };
+
+// Items of a prefixes' pass on the tensor-core path, at most (G up to 128).
+inline int64_t tc_prefix_items(const SeqAttn& p) {
+    return ((int64_t)p.tokens / (2 * (128 / p.G)) + p.parts.groups) * p.kv.Hkv;
+}
 
 // Row-tile path (16 rows of one kv head per tile, warp MMAs): any page size
 // and group size.

@@ -178,11 +178,25 @@ sfa_status resolve_call(SeqAttn& p, const Call& c, size_t need) {
     return SFA_OK;
 }
 
+// Whether the keys of a call's pass leave L2 first (KeyParts::once): in the two passes
+// of 16-row tiles, and on the tensor cores in the prefixes' where its items are fewer
+// than SMs.  Then each key is read once, or by a few items next to one another.  32/8
+// heads of 128, us with and without: 64 requests behind 16,384 tokens (one item a kv
+// head) 57 and 65; 300 behind them (5 items) and 300 own tokens each 160 and 167, and
+// 2,000 own 484 and 477; 200 behind 60,000 241 and 248.  40 requests of 16 heads behind
+// 4,900, one kv head (40 16-row tiles), 33.7 and 33.7.
+bool leaves_l2_first(const SeqAttn& p, bool tc) {
+    if (p.parts.phase == PHASE_PREFIX) return !tc || tc_prefix_items(p) < num_sms();
+    return p.parts.phase == PHASE_OWN && !tc;
+}
+
 // One pass of a resolved call; `parts`: over parts of the keys.
 sfa_status launch_attention(SeqAttn& p, bool parts, const Call& c) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(c.stream);
     cudaError_t err;
-    if (!few_rows(p) && attn_tc_supported(p.kv, p.G)) {
+    const bool tc = !few_rows(p) && attn_tc_supported(p.kv, p.G);
+    p.parts.once = leaves_l2_first(p, tc);
+    if (tc) {
         p.err_word = device_error_word();
         if (!p.err_word) return SFA_ERR_CUDA;
         err = parts ? launch_attn_tc_parts(p, c.dtype, num_sms(), s) : launch_attn_tc(p, c.dtype, num_sms(), s);
@@ -398,7 +412,6 @@ sfa_status paged_run_shared(const paged_kv* cache, const void* q, int64_t q_stri
     p.parts.px_ml = p.parts.px_o + (int64_t)num_tokens * num_qo_heads * p.kv.D;
     p.parts.phase = PHASE_DIRECT;
     if (few_rows(p) && (int64_t)direct_bytes(p) <= kDirectBytes) return launch_rows_parts(p, c);
-    p.parts.once = 1;
     SeqAttn prefix = p;
     prefix.parts.phase = PHASE_PREFIX;
     prefix.causal = 0;
