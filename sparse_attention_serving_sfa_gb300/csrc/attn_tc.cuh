@@ -1694,14 +1694,14 @@ cudaError_t launch_tc(const SeqAttn& a, sfa_dtype dtype, int num_sms, cudaStream
     while ((1 << p.box_shift) < p.box) ++p.box_shift;
     p.by_unit = divide_by(2 * p.TR);
     p.ctas_mul = ~uint64_t(0) / (uint64_t)(num_sms < kMaxCtas ? num_sms : kMaxCtas) + 1;
-    // Measured (448 / 576): chunks of 200 to 1,024 tokens over 16-bit pages 199.8 /
-    // 202.0 us, 4 causal prompts of 2,048 tokens 139.6 / 145.5 us; 64-dim ones (320 /
-    // 448) 101.2 / 103.8 us, prompts of up to 700 tokens 30.9 / 31.2 us; chunks over
-    // E4M3 pages (320 / 448 / 640) 336 / 334 / 341 us, through a window 173 / 166 / 170.
+    // Measured, us (320 / 448 / 576 / 640): chunks of 200 to 1,024 tokens over 16-bit
+    // pages 210.5 / 210.6 / 210.2 / 211.6, over E4M3 335 / 335 / 338 / 340, through a
+    // window 169 / 164 / 165 / 168; a prompt of 16,384 tokens 1,510 / 1,514 / 1,518 /
+    // 1,518; 64-dim prompts of up to 700 tokens 28.7 / 30.0 / 30.5 / 29.6.  Own tokens
+    // behind a prefix (320 / 448 / 640 / 900 / 1,152): 16 chunks of 200 tokens 452 / 452 /
+    // 454 / 456 / 449, decode batches and groups the same within 0.2%.
     // A step of 128 keys takes about 2,700 cycles (64-dim 2,400, 8-bit 3,300).
     p.charge = a.kv.f8 || a.kv.D == 128 ? 448 : 320;
-    // (an item behind a prefix reads that one's sums, too, and is mostly short)
-    if (PARTS && a.parts.phase == PHASE_OWN) p.charge = 900;
     p.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.ws_o = static_cast<float*>(a.ws);
     p.ws_ml = p.ws_o + (int64_t)2 * kMaxCtas * kItemRows * a.kv.D;
