@@ -663,7 +663,8 @@ sfa_status paged_run_window(const paged_kv* cache, const void* q, int64_t q_stri
                             sfa_stream_t stream);
 
 /* Bytes of workspace paged_run_shared needs for these sizes on the current
- * device.  Host only. */
+ * device: paged_workspace_size() and head_dim + 2 floats for each row and qo head.
+ * Host only. */
 sfa_status paged_shared_workspace_size(int num_seqs, int num_tokens, int num_qo_heads,
                                        int num_kv_heads, int head_dim, size_t* bytes);
 
@@ -682,7 +683,11 @@ sfa_status paged_shared_workspace_size(int num_seqs, int num_tokens, int num_qo_
  * end, the result is paged_run's.  kv_lens and page_table count and list the shared
  * tokens, too; what the sequences but the first hold in their places is not
  * looked at.  Lists that overlap or decrease give unspecified numbers.
- * Other arguments, precision and errors as paged_run.
+ * One pass or two, and their kernels, are chosen by what the page table can hold: a
+ * table much wider than the sequences costs a few requests behind a short prefix time.
+ * Other arguments and errors as paged_run.  Precision, too, each pass by its kernel: where
+ * many rows share a prefix, single tokens among them, the weights of the shared keys are
+ * rounded once to 16 bits, also where paged_run would carry their remainders.
  */
 sfa_status paged_run_shared(const paged_kv* cache, const void* q, int64_t q_stride,
                             const int32_t* cu_seqlens_q, int num_tokens, int num_qo_heads,

@@ -69,11 +69,14 @@
 // its lowest row's first key on, rounded down to a box's: what is left out between
 // the two is Item::shift keys, and key u of its way is key u or u + shift.  Keys on the
 // way that no row of the item sees are cleared like those behind kv_len.  Measured:
-// 16,384 tokens through a window of 4,096 670 to 690 us (1.28 us a step, 0.71 to 0.73
-// of the burst rate); chunks over E4M3 pages through 2,000 keys 165 us (1.9 us a
-// step, 4.5 an item); 24 prompts of up to 2,500 tokens through 333 keys 48 us (with the
-// sinks in a step of their own and steps at multiples of 128 57); 64 requests' rows
-// over a shared prefix of 16,384 tokens 21 us.
+// 16,384 tokens through a window of 4,096 627 us at 2.07 GHz, for a few passes, and
+// 670 to 690 (0.71 to 0.73 of the burst rate) at the 1.9 GHz that the power cap leaves:
+// 389 steps and 13.5 items a CTA, 1.28 to 1.30 million cycles, 3,300 a step with all that
+// its item costs; chunks over E4M3 pages through 2,000 keys 165 us (1.9 us a step, 4.5
+// an item), over 16-bit pages 127; 24 prompts of up to 2,500 tokens through 333 keys 48 us
+// (with the sinks in a step of their own and steps at multiples of 128 57); 64 requests'
+// rows over a shared prefix of 16,384 tokens 21 us; 16 questions of 30 to 400 tokens behind
+// 16,000 of E4M3 591 to 594 us, over 16-bit pages 485 to 520.
 #pragma once
 
 #include <type_traits>

@@ -254,6 +254,8 @@ sfa_status run_attention(SeqAttn& p, const Call& c, int window, int sinks) {
 // 35.7; 16 behind 2,000 (133 MB) 19.4 and 21.5; 32 behind 500 (80 MB) 18.9 and 17.8,
 // behind 2,000 (266 MB) 24.7 and 36.4; E4M3, 8 behind 8,000 (127 MB) 26.4 and 27.3, 32
 // behind 1,000 (71 MB) 23.0 and 21.5; 2 kv heads, 8 behind 4,000 (32 MB) 17.8 and 11.8.
+// (Tables as wide as the sequences.  One with room for 32,768 tokens counts as that much:
+// 5 behind 1,500 take two passes then, 22.2 us instead of 11.2.)
 constexpr int64_t kDirectBytes = 96 << 20;
 int64_t direct_bytes(const SeqAttn& p) {
     return p.kv.num_seqs * most_keys(p.kv) * p.kv.Hkv * p.kv.D * (p.kv.f8 ? 2 : 4);

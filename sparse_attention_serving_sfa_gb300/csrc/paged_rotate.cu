@@ -18,11 +18,11 @@
 // memory for all heads (the float4 of two angles lie by piece, so that the eight
 // threads of a head read side by side), then a thread moves 16 elements of a head at
 // a time, in two 16-byte halves that hold both sides of eight pairs, the next under
-// way.  Measured: 12,837 tokens of 32 / 8 heads of 128 into E4M3 pages 62 to 63 us
+// way.  Measured: 12,837 tokens of 32 / 8 heads of 128 into E4M3 pages 62 to 63.5 us
 // (289 MB, 4.6 TB/s, 0.69 of the measured copy rate; a fetch not under way 67 us, four
 // blocks an SM with spills 68, a warp a token with its angles in registers 71);
-// 7,210 of 16 / 4 heads of 64 into 16-bit pages 12 us; one token each of 64 requests
-// 5.0 us, 3.5 of them where no code has to be found in 64 bits.
+// 7,210 of 16 / 4 heads of 64 into 16-bit pages 12 to 13.7 us; one token each of 64
+// requests 4.7 to 5.1 us, 3.5 of them where no code has to be found in 64 bits.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
